@@ -298,6 +298,21 @@ __device__ void entry128(int d, const float* gate, T* outK, T* outV, int parity,
   __syncthreads();   // the rows may be refetched for the next entry
 }
 
+// Whether the page of position `pos` of request b can be written: true without pages.  A page id
+// outside the pool (an unmapped page, say) records TV_ERR_ARG; the caller skips its writes, which
+// layer_row would send to page 0.
+__device__ __forceinline__ bool page_writable(const Paging& pg, int b, int64_t pos,
+                                              int32_t* status) {
+  if (pg.page_tokens == 0) return true;
+  const int64_t g = pos / pg.page_tokens;
+  if (g < pg.max_pages) {
+    const int32_t page = pg.table[(int64_t)b * pg.max_pages + g];
+    if (page >= 0 && page < pg.n_pool_pages) return true;
+  }
+  record_error(status, TV_ERR_ARG);
+  return false;
+}
+
 // ---- prefill: every complete block of the committed prefix ---------------------------------
 // C4: grid.x entry index (strided), grid.y request.
 template <typename T>
@@ -318,6 +333,7 @@ __global__ void __launch_bounds__(kThreads) prefill4_kernel(
   for (int i = threadIdx.x; i < d; i += blockDim.x) sm.gate4[i] = g[i];
   const int n = Lb / 4;
   for (int j = blockIdx.x; j < n; j += gridDim.x) {
+    if (!page_writable(pg, b, (int64_t)j * 4, status)) continue;   // uniform over the CTA
     if (threadIdx.x < 4) {
       const int64_t row = layer_row(pg, b, (int64_t)j * 4 + threadIdx.x, raw_cap, 1, status);
       rowK[threadIdx.x] = rawK + row * d;
@@ -353,6 +369,7 @@ __global__ void __cluster_dims__(kC128Ranks, 1, 1) __launch_bounds__(kThreads)
   const int n = Lb / 128;
   int parity = 0;
   for (int j = blockIdx.y; j < n; j += gridDim.y, parity ^= 1) {
+    if (!page_writable(pg, b, (int64_t)j * 128, status)) continue;   // uniform over the cluster
     if (threadIdx.x < kC128Tokens) {
       const int64_t row =
           layer_row(pg, b, (int64_t)j * 128 + kC128Tokens * rank + threadIdx.x, raw_cap, 1, status);
@@ -562,7 +579,7 @@ __global__ void __cluster_dims__(kC128Ranks, 1, 1) __launch_bounds__(kThreads)
   for (int v = rank; v < D; v += kC128Ranks) {
     const int pos = Lb + s_dep[v];
     const int64_t out = ((int64_t)b * D + v) * d;
-    if (ok && stage && s_cached[v] && pos < raw_cap) {
+    if (ok && stage && s_cached[v] && pos < raw_cap && page_writable(pg, b, pos, status)) {
       const int64_t dst = layer_row(pg, b, pos, raw_cap, 1, status) * d;
       for (int i = tid; i < d; i += blockDim.x) {
         rawK[dst + i] = treeK[out + i];
@@ -597,7 +614,8 @@ __global__ void __cluster_dims__(kC128Ranks, 1, 1) __launch_bounds__(kThreads)
     const int64_t entry = (pos + 1) / 4 - 1;
     T* sK = nullptr;
     T* sV = nullptr;
-    if (stage && s_cached[v] && entry < c4_cap) {   // C4 refreshes promptly
+    if (stage && s_cached[v] && entry < c4_cap &&   // C4 refreshes promptly
+        page_writable(pg, b, pos, status)) {
       const int64_t dst = layer_row(pg, b, entry, c4_cap, 4, status) * d;
       sK = c4K + dst;
       sV = c4V + dst;
@@ -674,6 +692,11 @@ __global__ void refresh_kernel(Paging pg, int D, int d, int es, int comp_mask, i
       if (Lnew > raw_cap) { ok = 0; code = TV_ERR_CAPACITY; }
       if ((comp_mask & TV_COMP_C4) && Lnew / 4 > c4_cap) { ok = 0; code = TV_ERR_CAPACITY; }
       if ((comp_mask & TV_COMP_C128) && Lnew / 128 > c128_cap) { ok = 0; code = TV_ERR_CAPACITY; }
+      // every page the commit writes is there (n <= 64 positions lie in at most two pages)
+      if (ok && !(page_writable(pg, b, Lb, status) && page_writable(pg, b, Lnew - 1, status))) {
+        ok = 0;
+        code = TV_ERR_ARG;
+      }
     }
     if (!ok) record_error(status, code);
     // with staging, the accepted nodes on the cached chain (the root, its lowest-numbered child,
