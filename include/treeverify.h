@@ -83,6 +83,7 @@ typedef struct CUstream_st* tv_stream_t; /* the same handle type as cudaStream_t
 #define TV_ERR_SELECTION (-9)  /* a selection index is outside the request's C4 entries */
 #define TV_ERR_BOUNDS (-10)    /* bounds-checked build only: a global index failed its range
                                   check (the access was skipped; the site is printed once) */
+#define TV_ERR_VALUE (-11)     /* a NaN or +inf among the logits of a row */
 
 /* tv_shape.tail_mode */
 #define TV_TAIL_WINDOW 0
@@ -119,7 +120,8 @@ typedef struct tv_shape {
    * c128K [n_pool_pages][P/128][d] (V alike) -- and logical page g of request b (tokens
    * g*P .. g*P+P-1, with their C4 and C128 entries) lives in page page_table[b][g] of all three;
    * raw_cap, c4_cap and c128_cap must then be max_pages * P, * P/4 and * P/128.  A page id outside
-   * 0 .. n_pool_pages-1 is reported as TV_ERR_ARG on the device (and page 0 is read instead). */
+   * 0 .. n_pool_pages-1 that a call needs is reported as TV_ERR_ARG on the device (page 0 is read
+   * instead, and nothing is written). */
   int32_t page_tokens;
   int32_t max_pages;           /* logical pages per request (columns of page_table) */
   int32_t n_pool_pages;        /* pages in each pool */
@@ -132,7 +134,9 @@ typedef struct tv_shape {
    * until tv_refresh_commit advances L), and tv_refresh_commit copies only the accepted nodes off
    * that chain and the accepted C128 entries.  A single-chain tree then commits by advancing L. */
   int32_t stage_chain;
-  const int32_t* page_table;   /* device [B][max_pages] int32 (page_tokens > 0 only) */
+  const int32_t* page_table;   /* device [B][max_pages] int32 (page_tokens > 0 only); -1: no page.
+                                  tv_pages_fork, _reserve and _compact write it, the other calls
+                                  read the entries of the positions they touch */
 } tv_shape;
 
 /* Library version string (static storage). */
@@ -299,7 +303,8 @@ int tv_accept_walk(const tv_shape* shape, const int32_t* parents, const int32_t*
  * entry, and every C128 entry the accepted path closes, are copied as above.
  *   parents [B][D] in (stage_chain == 1 only, else nullable)
  * Device errors: TV_ERR_CAPACITY (L+n > raw_cap or an entry beyond cap_m; request untouched),
- * TV_ERR_ARG (accept_len outside 1..D or a path id outside 0..D-1; request untouched).
+ * TV_ERR_ARG (accept_len outside 1..D, a path id outside 0..D-1 or, with pages, no page for a
+ * committed position; request untouched).
  */
 int tv_refresh_commit(const tv_shape* shape, const int32_t* parents, const int32_t* accept_len,
                       const int32_t* path, const void* treeK, const void* treeV, const void* scrK4,
@@ -329,6 +334,108 @@ size_t tv_indexer_workspace_size(const tv_shape* shape);
 int tv_indexer_topk(const tv_shape* shape, int d_idx, const void* q_idx, const void* k_idx,
                     const int32_t* L, int32_t* sel, void* workspace, size_t ws_bytes,
                     int32_t* status, tv_stream_t stream);
+
+/*
+ * From a round's logits to the integers and log probabilities around it: the target tokens that
+ * tv_accept_walk takes, the alternatives a draft tree is grown from, the log probabilities of the
+ * tokens a tree holds, and the entropy of every node's distribution.  The report leaves the step
+ * from logits to target tokens to the model runtime; greedy verification takes the largest logit
+ * ([TSD-V4] §3.2).  With x the logits of row (b, v) and p = softmax(scale * x) over the vocabulary:
+ *   lse      [B][D] fp32: natural-log sum of exp(scale * x)
+ *   entropy  [B][D] fp32: -sum p ln p, in nats
+ *   target   [B][D] int32: the token of the largest logit (equal logits: the lower id)
+ *   top_ids, top_logprobs [B][D][n_top]: the n_top tokens of largest logit, descending (equal
+ *            logits: the lower id first), with ln p; logits of -inf are never listed, places left
+ *            over hold -1 and -inf
+ *   logprobs [B][n_tok] fp32: ln p(tokens[b][i]) under the distribution of node nodes[b][i]; 0
+ *            where the node or the token is negative.  tokens = the draft tokens and nodes =
+ *            parents (n_tok = D) scores every draft token under its parent, the root as 0.
+ * Sums are kept in fp32 relative to the largest logit.  A logit of -inf is a masked token
+ * (probability 0, ln p = -inf).  A row of -inf only has lse = -inf, entropy 0, target -1, no
+ * alternatives and ln p = -inf.  The type's lowest finite value is an ordinary logit.
+ *   Uses shape->B and D (rows = B * D).  vocab 1..2^30; logits [B][D] rows of vocab elements, ld
+ *   >= vocab elements apart, of type logits_dtype (TV_F32 | TV_BF16), aligned to that type only.
+ *   n_tok 0..1024, tokens and nodes [B][n_tok] int32 in (nullable when n_tok == 0; nodes null:
+ *   entry i is on node i, n_tok <= D); scale > 0; n_top 0..32.  lse, entropy and target are
+ *   nullable (not wanted), logprobs when n_tok == 0, top_ids and top_logprobs when n_top == 0.
+ * Device errors: TV_ERR_VALUE (a NaN or +inf among a row's logits: that row's floats are NaN, its
+ * ids -1), TV_ERR_ARG (a node >= D or a token >= vocab: that log probability is 0).
+ */
+int tv_token_logprobs(const tv_shape* shape, int32_t vocab, int64_t ld, int32_t logits_dtype,
+                      const void* logits, int32_t n_tok, const int32_t* tokens,
+                      const int32_t* nodes, float scale, int32_t n_top, float* lse, float* entropy,
+                      float* logprobs, int32_t* top_ids, float* top_logprobs, int32_t* target,
+                      int32_t* status, tv_stream_t stream);
+
+/*
+ * Pages of the pools ([TSD-V4] §4.2: one logical layer over three physical layers with shared
+ * page pointers; the report keeps their allocation in its serving engine).  For shapes with
+ * page_tokens = P > 0.  The state is shape->page_table (entries -1 where no page is mapped), L, and
+ *   page_refs [n_pool_pages] int32: holders of every page.  A table entry counts as one; a caller
+ *   that holds a page of its own (a cached prefix, say) adds one itself.  0: the page is free.
+ * The calls keep one rule: a page that more than one holder has holds only complete, committed
+ * tokens of every request that maps it, so no round writes a shared page.  They run on the stream
+ * like the others and can be captured; all three leave everything as it was when there are not
+ * enough free pages (TV_ERR_CAPACITY).  Pages are taken in the order of the requests and positions
+ * that need them, the lowest-numbered free page first, so results do not depend on timing.
+ * workspace: device buffer of ws_bytes >= tv_pages_workspace_size(shape), 256-byte aligned; calls
+ * that overlap on the GPU need one each.
+ */
+size_t tv_pages_workspace_size(const tv_shape* shape);
+
+/*
+ * Releases, truncates and branches requests.  Per slot b, from the state before the call:
+ *   source[b] == b   the slot stays; with 0 <= keep[b] < L[b] its length becomes keep[b] and the
+ *                    pages behind that are released; a partial last page that others hold is
+ *                    replaced by a copy
+ *   source[b] == -1  the slot is released: its table row becomes -1, L[b] = 0
+ *   source[b] == s   the slot's pages are released and it becomes a copy of slot s (source[s] == s
+ *                    is required) at the smallest of L[s] and the non-negative ones of keep[s]
+ *                    and keep[b]: the full pages are shared, the partial last page is copied
+ * Only the rows of valid tokens and entries are copied; a released page is free when nobody else
+ * holds it, and may be taken again by the same call.
+ *   source [B] in; keep [B] in (nullable: no truncation; negative: none for that slot); L [B] and
+ *   page_refs in and out; rawK .. c128V: the pools, in and out (an inactive compressor's are
+ *   nullable; 16-byte aligned); k_idx: the indexer keys [B][c4_cap][d_idx] bf16 (nullable; 16-byte
+ *   aligned, d_idx a multiple of 8 in 8..256): rows 0 .. L/4 - 1 of a branching slot are copied
+ *   from its source's
+ * Host errors: TV_ERR_ARG, TV_ERR_SHAPE, TV_ERR_WORKSPACE.
+ * Device errors: TV_ERR_ARG (a source out of range, or one that is not a slot that stays, or a
+ * page missing among the source's: that slot stays as it was), TV_ERR_CAPACITY (a source's length
+ * outside 0 .. raw_cap: that slot stays as it was; not enough free pages: all slots do).
+ */
+int tv_pages_fork(const tv_shape* shape, const int32_t* source, const int32_t* keep, int32_t* L,
+                  int32_t* page_refs, void* rawK, void* rawV, void* c4K, void* c4V, void* c128K,
+                  void* c128V, void* k_idx, int32_t d_idx, void* workspace, size_t ws_bytes,
+                  int32_t* status, tv_stream_t stream);
+
+/*
+ * Maps a page wherever one is missing for the positions L[b] .. L[b] + need[b] - 1 (a round's D
+ * tokens, or a prompt to come); need[b] <= 0 leaves the slot alone.
+ *   need [B] in; L [B] in; page_refs in and out
+ * Device errors: TV_ERR_CAPACITY (L + need > raw_cap: that slot stays as it was; not enough free
+ * pages: all slots do), TV_ERR_ARG (L < 0: that slot stays as it was; a table entry outside the
+ * pool: that entry stays).
+ */
+int tv_pages_reserve(const tv_shape* shape, const int32_t* need, const int32_t* L,
+                     int32_t* page_refs, void* workspace, size_t ws_bytes, int32_t* status,
+                     tv_stream_t stream);
+
+/*
+ * Moves the live pages (those somebody holds) into the n_live lowest pages of the pool: the i-th
+ * live page at or above n_live takes the i-th free page below it; the others stay.  Table and
+ * counts follow; of a page that only table entries hold, the rows of valid tokens are copied, of any
+ * other the whole page.
+ *   L [B] in; page_refs in and out; rawK .. c128V: the pools, in and out (16-byte aligned); remap
+ *   [n_pool_pages] int32 out: the new number of every page that was live, -1 for the others; n_live
+ *   [1] int32 out
+ * Device errors: TV_ERR_ARG (a table entry outside the pool: it stays; a page with more table
+ * entries than holders: it is live all the same).
+ */
+int tv_pages_compact(const tv_shape* shape, const int32_t* L, int32_t* page_refs, void* rawK,
+                     void* rawV, void* c4K, void* c4V, void* c128K, void* c128V, int32_t* remap,
+                     int32_t* n_live, void* workspace, size_t ws_bytes, int32_t* status,
+                     tv_stream_t stream);
 
 /*
  * Testing aid for the failure path of the tensor-core attention (the report has no counterpart).

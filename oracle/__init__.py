@@ -25,6 +25,8 @@ accept    the greedy acceptance walk
 refresh   accepted-path commit of raw K/V and completed compressed blocks
 round     one full verify round: the five steps above in order
 indexer   top-k selection of persistent C4 entries by an fp32 indexer score (sparse C4 path)
+logprobs  from logits to target tokens, alternatives, log probabilities and entropy
+pages     branching, reserving and compacting the pages of the pools
 
 Parity status: every function here is pinned by the ``-m "not gpu"`` tests
 (``tests/test_oracle_*.py``) against brute force, closed forms, special cases or library
@@ -46,6 +48,8 @@ from .accept import accept_walk
 from .refresh import refresh_commit_request
 from .round import verify_round
 from .indexer import index_scores, topk_ascending, indexer_select
+from .logprobs import row_logprobs, row_order, token_logprobs
+from . import pages
 
 __all__ = [
     "round_to_storage",
@@ -67,4 +71,8 @@ __all__ = [
     "index_scores",
     "topk_ascending",
     "indexer_select",
+    "row_logprobs",
+    "row_order",
+    "token_logprobs",
+    "pages",
 ]

@@ -1,0 +1,369 @@
+"""tv_pages_fork, tv_pages_reserve and tv_pages_compact on the GPU against the oracle: tables, counts,
+lengths and every row of every pool exactly, over worked cases and random histories; and a decode
+loop on a managed pool against the same rounds on contiguous caches."""
+
+import copy
+import dataclasses
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from oracle import pages
+from tree_speculative_verify_gb300 import _lib, engine, workloads
+
+pytestmark = pytest.mark.gpu
+
+MS = {1: ("rawK", "rawV"), 4: ("c4K", "c4V"), 128: ("c128K", "c128V")}
+
+
+class Pool:
+    """One state on the GPU and its copy for the oracle."""
+
+    def __init__(self, table, L, n_pool, P=512, d=8, dtype="bf16", comp=(4, 128), extra=(), keys=0,
+                 seed=0, ws_spare=0):
+        B, G = len(table), len(table[0])
+        dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+        g = torch.Generator().manual_seed(seed)
+        self.P, self.comp = P, comp
+        self.t = {}
+        for m in (1,) + tuple(comp):
+            for name in MS[m]:
+                self.t[name] = torch.randn((n_pool, P // m, d), generator=g).to(dt).cuda()
+        refs = [0] * n_pool
+        for row in table:
+            for p in row:
+                if 0 <= p < n_pool:
+                    refs[p] += 1
+        for p in extra:
+            refs[p] += 1
+        i32 = lambda a: torch.tensor(a, dtype=torch.int32).cuda()
+        self.table, self.refs, self.L, self.status = i32(table), i32(refs), i32(L), i32([0])
+        self.keys = torch.randn((B, G * P // 4, keys), generator=g).bfloat16().cuda() if keys else None
+        mask = (_lib.TV_COMP_C4 if 4 in comp else 0) | (_lib.TV_COMP_C128 if 128 in comp else 0)
+        self.shape = _lib.make_shape(
+            B=B, D=8, H=1, d=d, comp_mask=mask, dtype=_lib.TV_BF16 if dtype == "bf16" else _lib.TV_F32,
+            raw_cap=G * P, c4_cap=G * P // 4, c128_cap=G * P // 128, page_tokens=P, max_pages=G,
+            n_pool_pages=n_pool, page_table=self.table)
+        self.ws = torch.full((_lib.tv_pages_workspace_size(self.shape) + ws_spare,), 0x5a,
+                             dtype=torch.uint8, device="cuda")
+        self.remap = torch.full((n_pool,), -9, dtype=torch.int32, device="cuda")
+        self.n_live = torch.full((1,), -9, dtype=torch.int32, device="cuda")
+        self.o = dict(table=[list(r) for r in table], refs=refs, L=list(L),
+                      pools={m: tuple(self.np(self.t[k]) for k in MS[m]) for m in (1,) + tuple(comp)},
+                      keys=self.np(self.keys) if keys else None)
+
+    @staticmethod
+    def np(t):
+        return t.float().cpu().numpy()
+
+    def layers(self):
+        return [self.t.get(k) for m in (1, 4, 128) for k in MS[m]]
+
+    def fork(self, source, keep=None, stream=None):
+        i32 = lambda a: None if a is None else torch.tensor(a, dtype=torch.int32).cuda()
+        s, k = i32(source), i32(keep)
+        torch.cuda.synchronize()
+        _lib.tv_pages_fork(self.shape, s, k, self.L, self.refs, *self.layers(), self.keys, self.ws,
+                           self.status, stream)
+        torch.cuda.synchronize()
+        return pages.fork(self.o, self.P, list(source), None if keep is None else list(keep))
+
+    def reserve(self, need):
+        _lib.tv_pages_reserve(self.shape, torch.tensor(need, dtype=torch.int32).cuda(), self.L,
+                              self.refs, self.ws, self.status)
+        return pages.reserve(self.o, self.P, list(need))
+
+    def compact(self):
+        _lib.tv_pages_compact(self.shape, self.L, self.refs, *self.layers(), self.remap, self.n_live,
+                              self.ws, self.status)
+        code, remap, n = pages.compact(self.o, self.P)
+        assert self.remap.tolist() == remap and self.n_live.tolist() == [n]
+        return code
+
+    def check(self, codes):
+        """`codes`: what the oracle returned, in order; the status word holds one of the errors."""
+        torch.cuda.synchronize()
+        assert self.table.tolist() == self.o["table"]
+        assert self.refs.tolist() == self.o["refs"]
+        assert self.L.tolist() == self.o["L"]
+        for m, pools in self.o["pools"].items():
+            for k, want in zip(MS[m], pools):
+                assert np.array_equal(self.np(self.t[k]), want), k
+        if self.keys is not None:
+            assert np.array_equal(self.np(self.keys), self.o["keys"])
+        status = int(self.status.item())
+        errors = [c for c in codes if c]
+        assert (status in (-1, -4)) if errors else status == 0
+        if errors and all(c == errors[0] for c in errors):
+            assert status == errors[0]
+        self.status.zero_()
+
+
+def _random_table(rng, B, G, n_pool, L, P):
+    ids = list(rng.permutation(n_pool))
+    return [[int(ids.pop()) for _ in range(-(-n // P))] + [-1] * (G - -(-n // P)) for n in L]
+
+
+@pytest.mark.parametrize("d,dtype,comp,keys", [(8, "bf16", (4, 128), 0), (512, "bf16", (4, 128), 64),
+                                               (24, "f32", (4,), 8), (72, "bf16", (128,), 0)])
+@pytest.mark.parametrize("P", [512, 1536])
+def test_fork_copies_shares_and_releases(P, d, dtype, comp, keys):
+    rng = np.random.default_rng(P + d)
+    L = [0, 1, 3, P - 1, P, P + 1, 2 * P, 2 * P + 127, 2 * P + 300, 5]
+    s = Pool(_random_table(rng, 10, 4, 40, L, P), L, 40, P, d, dtype, comp, keys=keys)
+    codes = [s.fork([0, 1, 2, 3, 4, 5, 6, 7, 8, 9])]                   # nothing to do
+    codes.append(s.fork([0, 0, 2, 3, 3, 5, 6, 8, 8, 8]))               # empty, partial, many of one
+    s.check(codes)
+    codes = [s.fork([0, 1, 2, -1, -1, 5, 6, 6, -1, 5])]                # release and fork together
+    s.check(codes)
+    codes = [s.fork([0, 1, 2, 5, 6, 5, 6, 6, 8, 5], [-1, -1, 2, 9, P + 1, 1, -1, P, -1, 2000])]
+    s.check(codes)
+
+
+def test_fork_refuses_slots_one_by_one():
+    P = 512
+    L = [700, 40, 600, 1100, 5, 2000, 9]
+    table = [[0, 1, -1], [2, -1, -1], [3, -1, -1], [4, 5, 6], [7, -1, -1], [8, 9, 10], [77, -1, -1]]
+    s = Pool(table, L, 16, P)
+    # out of range; source that moves; source with a missing page; source past the capacity; a
+    # page outside the pool; two good ones
+    s.check([s.fork([0, 9, 2, 2, 3, 5, 5])])
+    s.check([s.fork([0, -2, 2, 0, 6, 5, 6])])
+    s.check([s.fork([0, 0, 2, 3, 4, 5, 0])])
+
+
+def test_one_page_too_few_leaves_everything():
+    P = 512
+    s = Pool([[0, 1], [2, -1], [3, -1], [-1, -1]], [600, 10, 20, 0], 5, P, ws_spare=64)
+    s.check([s.fork([0, 0, 2, 0])])            # released page 2 and free page 4: just enough
+    s.check([s.reserve([0, 0, 500, 0])])       # no page missing but one: none is free
+    s.check([s.fork([0, 0, 0, 0])])            # the copies take the released pages
+    s.check([s.fork([0, 1, -1, 3]), s.reserve([P, 0, 5, 0])])
+    s.check([s.fork([0, 1, 0, 3])])
+
+
+def test_truncation_copies_a_page_that_others_hold():
+    P = 512
+    s = Pool([[0, 1, 2], [-1] * 3, [-1] * 3], [1200, 0, 0], 10, P)
+    s.check([s.fork([0, 0, 0])])
+    s.check([s.fork([0, 1, 2], [100, 1024, 1200])])   # into a shared page, to its end, not at all
+    s.check([s.fork([0, 1, 2], [-1, 600, 600])])      # two holders of one page at once
+    s.check([s.fork([0, 1, 2], [0, 512, 99999])])
+
+
+def test_reserve_windows():
+    P = 512
+    rng = np.random.default_rng(4)
+    L = [0, 511, 512, 505, 100, 1023, 2000]
+    s = Pool(_random_table(rng, 7, 6, 40, L, P), L, 40, P)
+    s.check([s.reserve([1, 1, 8, 8, 0, 2000, -3])])
+    s.check([s.reserve([8] * 7)])
+    s.check([s.reserve([0, 3000, 1, 0, 0, 0, 1072])])   # one past the capacity, one to its end
+    s.L[2] = -4
+    s.o["L"][2] = -4
+    s.check([s.reserve([8] * 7)])
+
+
+@pytest.mark.parametrize("n_pool,B,G", [(3, 1, 2), (40, 6, 5), (700, 50, 8), (5000, 300, 6)])
+def test_compact_moves_the_upper_live_pages(n_pool, B, G):
+    P, rng = 512, np.random.default_rng(n_pool)
+    L = [int(x) for x in rng.integers(0, G * P + 1, size=B)]
+    while sum(-(-n // P) for n in L) > 0.8 * n_pool:
+        L[int(np.argmax(L))] = int(rng.integers(0, 2 * P))
+    table = _random_table(rng, B, G, n_pool, L, P)
+    for b in range(2, B, 3):                            # some share their first full pages
+        for g in range(min(L[b], L[b - 1]) // P):
+            table[b][g] = table[b - 1][g]
+    held = {p for r in table for p in r}
+    extra = [p for p in range(n_pool - 1, 0, -5)][:40]   # pages that others hold too, or alone
+    s = Pool(table, L, n_pool, P, extra=extra)
+    assert s.compact() == 0
+    s.check([])
+    assert int(s.n_live) == len((held | set(extra)) - {-1})
+    assert s.compact() == 0                              # nothing is left to move
+    s.check([])
+    assert s.remap.tolist()[:int(s.n_live)] == list(range(int(s.n_live)))
+
+
+def test_compact_reports_an_inconsistent_table():
+    P = 512
+    s = Pool([[5, 90], [3, -1]], [600, 20], 8, P)
+    s.refs[5] = 0
+    s.o["refs"][5] = 0
+    assert s.compact() == -1
+    s.check([-1])
+
+
+@pytest.mark.parametrize("seed", range(4))
+def test_random_histories(seed):
+    rng = np.random.default_rng(seed)
+    B, G, P, n = int(rng.integers(3, 40)), int(rng.integers(2, 7)), 512, 90
+    s = Pool([[-1] * G for _ in range(B)], [0] * B, n, P, keys=16, seed=seed)
+    for _ in range(25):
+        op, codes = int(rng.integers(4)), []
+        if op <= 1:
+            need = [int(x) for x in rng.integers(-20, 700, size=B)]
+            codes.append(s.reserve(need))
+            for b in range(B):     # a round's commit: the length moves where the pages are there
+                new = s.o["L"][b] + max(0, need[b])
+                if new <= G * P and -1 not in s.o["table"][b][:-(-new // P)]:
+                    s.o["L"][b] = new
+            s.L.copy_(torch.tensor(s.o["L"], dtype=torch.int32))
+        elif op == 2:
+            src = [int(x) if rng.random() < 0.4 else b for b, x in enumerate(rng.integers(-1, B, size=B))]
+            keep = [int(x) for x in rng.integers(-900, G * P, size=B)] if rng.random() < 0.5 else None
+            codes.append(s.fork(src, keep))
+        else:
+            codes.append(s.compact())
+        s.check(codes)
+
+
+def test_host_refusals():
+    s = Pool([[0, -1]], [5], 4)
+    src = torch.zeros(1, dtype=torch.int32, device="cuda")
+    plain = _lib.make_shape(B=1, D=8, H=1, d=8, raw_cap=1024, c4_cap=256, c128_cap=8)
+    for shape, ws, code in ((plain, s.ws, -2), (s.shape, s.ws[:256], -7), (s.shape, None, -1),
+                            (s.shape, s.ws[16:], -1)):
+        with pytest.raises(_lib.TreeVerifyError) as e:
+            _lib.tv_pages_reserve(shape, src, s.L, s.refs, ws, s.status)
+        assert e.value.code == code
+    with pytest.raises(ValueError):
+        _lib.tv_pages_reserve(s.shape, src, s.L, s.refs[:2], s.ws, s.status)
+    with pytest.raises(TypeError):
+        _lib.tv_pages_fork(s.shape, src.long(), None, s.L, s.refs, *s.layers(), None, s.ws, s.status)
+    with pytest.raises(ValueError):
+        _lib.tv_pages_fork(s.shape, src, None, s.L, s.refs, s.t["rawK"][:1], *s.layers()[1:], None,
+                           s.ws, s.status)
+    s.check([])
+
+
+def test_two_captured_graphs_and_another_stream():
+    P = 512
+    s = Pool([[3, 4, -1], [5, -1, -1], [-1] * 3], [700, 30, 0], 12, P)
+    src = torch.tensor([0, 1, 0], dtype=torch.int32).cuda()
+    drop = torch.tensor([0, 1, -1], dtype=torch.int32).cuda()
+    need = torch.tensor([8, 8, 400], dtype=torch.int32).cuda()
+    graphs = []
+    for a in (src, drop):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            _lib.tv_pages_fork(s.shape, a, None, s.L, s.refs, *s.layers(), None, s.ws, s.status)
+            _lib.tv_pages_reserve(s.shape, need, s.L, s.refs, s.ws, s.status)
+            _lib.tv_pages_compact(s.shape, s.L, s.refs, *s.layers(), s.remap, s.n_live, s.ws, s.status)
+        graphs.append(g)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for k in (0, 1, 0, 1):
+        with torch.cuda.stream(side):
+            graphs[k].replay()
+        torch.cuda.synchronize()
+        pages.fork(s.o, P, (src, drop)[k].tolist())
+        pages.reserve(s.o, P, need.tolist())
+        pages.compact(s.o, P)
+        s.check([])
+
+
+def _commit_rows(wl, seed, n):
+    g = torch.Generator().manual_seed(seed)
+    return [(torch.randn((wl.B, wl.D, wl.d), generator=g) * 0.5).to(wl.torch_dtype).cuda()
+            for _ in range(2 * n)]
+
+
+@pytest.mark.parametrize("kernel,stage", [(_lib.TV_ATTN_AUTO, 0), (_lib.TV_ATTN_SIMT, 0), (_lib.TV_ATTN_AUTO, 1)])
+def test_decode_loop_on_a_managed_pool(kernel, stage):
+    """Rounds, branching, releasing and compaction on a managed pool, the targets from logits:
+    every round's outputs and every request's visible cache equal those of contiguous caches that
+    are forked by whole copies."""
+    wl = workloads.serving(B=6, L=(500, 1400))
+    P = 512
+    shape, st = engine.alloc_pool(wl, P, 40, kernel, stage_chain=stage)
+    rb = engine.alloc_round(wl, shape)
+    engine.alloc_scores(rb, shape, 1000, n_top=3)
+    engine.prefill(shape, st, rb)
+    cshape = engine.shape_for(wl, kernel, stage_chain=stage)
+    cshape.raw_cap, cshape.c4_cap, cshape.c128_cap = shape.raw_cap, shape.c4_cap, shape.c128_cap
+    z = lambda rows: torch.zeros((wl.B, rows, wl.d), dtype=wl.torch_dtype, device="cuda")
+    cst = engine.DeviceState(rawK=z(shape.raw_cap), rawV=z(shape.raw_cap), c4K=z(shape.c4_cap),
+                             c4V=z(shape.c4_cap), c128K=z(shape.c128_cap), c128V=z(shape.c128_cap),
+                             L=st.L.clone())
+    cst.rawK[:, :wl.raw_cap], cst.rawV[:, :wl.raw_cap] = wl.rawK.cuda(), wl.rawV.cuda()
+    crb = engine.alloc_round(wl, cshape)
+    engine.prefill(cshape, cst, crb)
+    remap = torch.empty(40, dtype=torch.int32, device="cuda")
+    n_live = torch.empty(1, dtype=torch.int32, device="cuda")
+    rows = _commit_rows(wl, 5, 6)
+    steps = [None, [0, 0, 2, 2, 2, 5], None, [0, 1, 4, -1, 4, 0], "compact", None]
+    for i, step in enumerate(steps):
+        if step == "compact":
+            engine.compact(shape, st, rb, remap, n_live)
+        elif step is not None:
+            engine.fork(shape, st, rb, torch.tensor(step, dtype=torch.int32).cuda())
+            for name in ("rawK", "rawV", "c4K", "c4V", "c128K", "c128V", "L"):
+                t = getattr(cst, name)
+                old = t.clone()
+                for b, s in enumerate(step):
+                    if s >= 0:
+                        t[b] = old[s]
+                    elif name == "L":
+                        t[b] = 0
+        for r in (rb, crb):
+            r.treeK.copy_(rows[2 * i])
+            r.treeV.copy_(rows[2 * i + 1])
+        rb.logits.normal_(generator=torch.Generator(device="cuda").manual_seed(i))
+        draft = torch.tensor(wl.draft).cuda().long() % 1000
+        # most nodes' best token is their first child's
+        first = torch.full((wl.B, wl.D), -1, dtype=torch.long, device="cuda")
+        for v in range(wl.D - 1, 0, -1):
+            par = rb.parents[:, v].long()
+            first.scatter_(1, par[:, None], draft[:, v:v + 1])
+        boost = torch.where(first >= 0, 9.0, -9.0)
+        rb.logits.scatter_(2, first.clamp(min=0)[..., None], boost[..., None].to(rb.logits.dtype))
+        rb.draft.copy_(draft.int())
+        crb.draft.copy_(draft.int())
+        engine.verify_round(shape, st, rb, scored=True)
+        torch.cuda.synchronize()
+        assert int(rb.status.item()) == 0
+        crb.target.copy_(rb.logits.float().argmax(2).int())
+        engine.verify_round(cshape, cst, crb)
+        torch.cuda.synchronize()
+        assert int(crb.status.item()) == 0
+        for name in ("target", "accept_len", "path", "bonus", "committed", "O", "lse"):
+            assert torch.equal(getattr(rb, name), getattr(crb, name)), (i, name)
+        assert torch.equal(st.L, cst.L)
+        assert int(rb.accept_len.max()) > 1
+        table = st.page_table.long()
+        for b in range(wl.B):
+            L = int(st.L[b])
+            for m, (k, v) in MS.items():
+                for name in (k, v):
+                    pool = getattr(st, name)
+                    got = pool[table[b].clamp(min=0)].reshape(-1, wl.d)[:L // m]
+                    assert torch.equal(got, getattr(cst, name)[b, :L // m]), (i, b, name)
+    counts = np.bincount(st.page_table.cpu().numpy().ravel() + 1, minlength=41)[1:]
+    assert st.page_refs.tolist() == counts[:40].tolist()
+
+
+def test_round_without_free_pages_commits_nothing_it_has_no_page_for():
+    # request 0 ends exactly at its page's end, and no page is free: its commit is refused, the other
+    # request's page still has room
+    wl = workloads.serving(B=2, L=(512, 512))
+    wl.L[1] = 300
+    shape, st = engine.alloc_pool(wl, 512, 2)
+    rb = engine.alloc_round(wl, shape)
+    engine.prefill(shape, st, rb)
+    before = {k: getattr(st, k).clone() for k in ("rawK", "c4K", "c128K")}
+    engine.verify_round(shape, st, rb)
+    torch.cuda.synchronize()
+    assert int(rb.status.item()) == _lib_code("TV_ERR_CAPACITY")
+    assert st.L.tolist() == [512, 300 + int(rb.accept_len[1])]
+    assert rb.committed[0].tolist() == [-1] * wl.D
+    page = int(st.page_table[0, 0])
+    for k, t in before.items():
+        assert torch.equal(getattr(st, k)[page], t[page]), k
+
+
+def _lib_code(name):
+    return next(c for c, n in _lib.TV_ERR.items() if n == name)

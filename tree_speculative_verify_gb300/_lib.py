@@ -21,7 +21,7 @@ TV_OK = 0
 TV_ERR = {
     -1: "TV_ERR_ARG", -2: "TV_ERR_SHAPE", -3: "TV_ERR_BAD_TREE", -4: "TV_ERR_CAPACITY",
     -5: "TV_ERR_DTYPE", -6: "TV_ERR_CUDA", -7: "TV_ERR_WORKSPACE", -8: "TV_ERR_TIMEOUT",
-    -9: "TV_ERR_SELECTION", -10: "TV_ERR_BOUNDS",
+    -9: "TV_ERR_SELECTION", -10: "TV_ERR_BOUNDS", -11: "TV_ERR_VALUE",
 }
 TV_TAIL_WINDOW, TV_TAIL_REMAINDER = 0, 1
 TV_COMP_C4, TV_COMP_C128 = 1, 2
@@ -34,6 +34,8 @@ EXPORTS = (
     "tv_build_ancestor_mask", "tv_prefill_compress", "tv_branch_compress",
     "tv_tree_verify_attn", "tv_accept_walk", "tv_refresh_commit", "tv_tree_verify_attn_noalloc",
     "tv_indexer_workspace_size", "tv_indexer_topk", "tv_debug_attn_timeout", "tv_noalloc_prepare",
+    "tv_token_logprobs", "tv_pages_workspace_size", "tv_pages_fork", "tv_pages_reserve",
+    "tv_pages_compact",
 )
 
 
@@ -80,6 +82,14 @@ _SIGS = {
                         ctypes.c_int),
     "tv_noalloc_prepare": ([], ctypes.c_int),
     "tv_debug_attn_timeout": ([ctypes.c_int64, ctypes.c_int32], ctypes.c_int),
+    "tv_token_logprobs": ([_SHAPE, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32, _P,
+                           ctypes.c_int32, _P, _P, ctypes.c_float, ctypes.c_int32] + [_P] * 8,
+                          ctypes.c_int),
+    "tv_pages_workspace_size": ([_SHAPE], ctypes.c_size_t),
+    "tv_pages_fork": ([_SHAPE] + [_P] * 11 + [ctypes.c_int32, _P, ctypes.c_size_t, _P, _P],
+                      ctypes.c_int),
+    "tv_pages_reserve": ([_SHAPE] + [_P] * 4 + [ctypes.c_size_t, _P, _P], ctypes.c_int),
+    "tv_pages_compact": ([_SHAPE] + [_P] * 11 + [ctypes.c_size_t, _P, _P], ctypes.c_int),
 }
 
 
@@ -234,6 +244,127 @@ def tv_indexer_topk(shape, d_idx, q_idx, k_idx, L, sel, workspace, status, strea
                                 _p(L), _p(sel), _p(workspace), ctypes.c_size_t(ws_bytes),
                                 _p(status), _stream(stream))
     _check("tv_indexer_topk", rc)
+
+
+# The calls below check their tensors' types and sizes, and pass plain integers: their kernels are
+# short, so the binding's own time counts.
+def _a(t, dtype, numel, name):
+    """Device address of a contiguous tensor of the given type with at least numel elements on the
+    current device (None: a null pointer)."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor or None")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: tensor arguments must live on the CUDA device")
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name}: the tensor lives on another device than the current one")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: tensor arguments must be contiguous")
+    if t.numel() < numel:
+        raise ValueError(f"{name}: {t.numel()} elements, {numel} needed")
+    return t.data_ptr()
+
+
+def _s(stream):
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+
+
+def tv_token_logprobs(shape, logits, tokens, nodes, scale, lse, entropy, logprobs, top_ids,
+                      top_logprobs, target, status, stream=None):
+    """``logits``: [B][D][vocab] fp32 or bf16 with unit last stride; the rows may lie further apart
+    than the vocabulary (a slice of a padded buffer).  ``tokens``, ``nodes`` and ``logprobs``: [B][n_tok]
+    or None; ``top_ids`` and ``top_logprobs``: [B][D][n_top] or None."""
+    B, D = shape.B, shape.D
+    if logits.dim() != 3 or logits.shape[0] != B or logits.shape[1] != D:
+        raise ValueError(f"logits: expected [{B}][{D}][vocab], got {tuple(logits.shape)}")
+    if not logits.is_cuda or logits.get_device() != torch.cuda.current_device():
+        raise ValueError("logits: the tensor must live on the current CUDA device")
+    dtype = {torch.float32: TV_F32, torch.bfloat16: TV_BF16}.get(logits.dtype)
+    if dtype is None:
+        raise TypeError(f"logits: expected float32 or bfloat16, got {logits.dtype}")
+    vocab, (sB, ld, unit) = logits.shape[2], logits.stride()
+    if D == 1:
+        ld = sB if B > 1 else vocab
+    if B * D == 1:
+        ld = vocab
+    if (unit != 1 and vocab > 1) or ld < vocab or (B > 1 and sB != D * ld):
+        raise ValueError(f"logits: rows must be contiguous and evenly spaced, strides {logits.stride()}")
+    n_tok = 0 if tokens is None else tokens.shape[-1]
+    n_top = 0 if top_ids is None else top_ids.shape[-1]
+    rows, i32, f32 = B * D, torch.int32, torch.float32
+    rc = load().tv_token_logprobs(
+        ctypes.byref(shape), vocab, ld, dtype, logits.data_ptr(), n_tok,
+        _a(tokens, i32, B * n_tok, "tokens"), _a(nodes, i32, B * n_tok, "nodes"), scale, n_top,
+        _a(lse, f32, rows, "lse"), _a(entropy, f32, rows, "entropy"),
+        _a(logprobs, f32, B * n_tok, "logprobs"), _a(top_ids, i32, rows * n_top, "top_ids"),
+        _a(top_logprobs, f32, rows * n_top, "top_logprobs"), _a(target, i32, rows, "target"),
+        _a(status, i32, 1, "status"), _s(stream))
+    if rc:
+        _check("tv_token_logprobs", rc)
+
+
+def tv_pages_workspace_size(shape):
+    return int(load().tv_pages_workspace_size(ctypes.byref(shape)))
+
+
+def _pools(shape, rawK, rawV, c4K, c4V, c128K, c128V):
+    dt = torch.bfloat16 if shape.dtype == TV_BF16 else torch.float32
+    n = shape.n_pool_pages * shape.page_tokens * shape.d
+    n4 = n // 4 if shape.comp_mask & TV_COMP_C4 else 0
+    n128 = n // 128 if shape.comp_mask & TV_COMP_C128 else 0
+    return (_a(rawK, dt, n, "rawK"), _a(rawV, dt, n, "rawV"), _a(c4K, dt, n4, "c4K"),
+            _a(c4V, dt, n4, "c4V"), _a(c128K, dt, n128, "c128K"), _a(c128V, dt, n128, "c128V"))
+
+
+def _workspace(workspace):
+    if workspace is None:
+        return None, 0
+    return (_a(workspace, workspace.dtype, 0, "workspace"),
+            workspace.numel() * workspace.element_size())
+
+
+def tv_pages_fork(shape, source, keep, L, page_refs, rawK, rawV, c4K, c4V, c128K, c128V, k_idx,
+                  workspace, status, stream=None):
+    """``k_idx``: [B][c4_cap][d_idx] bf16 indexer keys, or None."""
+    B, i32 = shape.B, torch.int32
+    d_idx = 0 if k_idx is None else k_idx.shape[-1]
+    ws, ws_bytes = _workspace(workspace)
+    rc = load().tv_pages_fork(
+        ctypes.byref(shape), _a(source, i32, B, "source"), _a(keep, i32, B, "keep"),
+        _a(L, i32, B, "L"), _a(page_refs, i32, shape.n_pool_pages, "page_refs"),
+        *_pools(shape, rawK, rawV, c4K, c4V, c128K, c128V),
+        _a(k_idx, torch.bfloat16, B * shape.c4_cap * d_idx, "k_idx"), d_idx, ws, ws_bytes,
+        _a(status, i32, 1, "status"), _s(stream))
+    if rc:
+        _check("tv_pages_fork", rc)
+
+
+def tv_pages_reserve(shape, need, L, page_refs, workspace, status, stream=None):
+    B, i32 = shape.B, torch.int32
+    ws, ws_bytes = _workspace(workspace)
+    rc = load().tv_pages_reserve(
+        ctypes.byref(shape), _a(need, i32, B, "need"), _a(L, i32, B, "L"),
+        _a(page_refs, i32, shape.n_pool_pages, "page_refs"), ws, ws_bytes,
+        _a(status, i32, 1, "status"), _s(stream))
+    if rc:
+        _check("tv_pages_reserve", rc)
+
+
+def tv_pages_compact(shape, L, page_refs, rawK, rawV, c4K, c4V, c128K, c128V, remap, n_live,
+                     workspace, status, stream=None):
+    B, i32 = shape.B, torch.int32
+    ws, ws_bytes = _workspace(workspace)
+    rc = load().tv_pages_compact(
+        ctypes.byref(shape), _a(L, i32, B, "L"),
+        _a(page_refs, i32, shape.n_pool_pages, "page_refs"),
+        *_pools(shape, rawK, rawV, c4K, c4V, c128K, c128V),
+        _a(remap, i32, shape.n_pool_pages, "remap"), _a(n_live, i32, 1, "n_live"), ws, ws_bytes,
+        _a(status, i32, 1, "status"), _s(stream))
+    if rc:
+        _check("tv_pages_compact", rc)
 
 
 def tv_debug_attn_timeout(timeout_ns, withhold_tile):

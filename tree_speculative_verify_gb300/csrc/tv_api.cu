@@ -44,6 +44,7 @@ extern "C" const char* tv_status_string(int code) {
     case TV_ERR_TIMEOUT: return "TV_ERR_TIMEOUT";
     case TV_ERR_SELECTION: return "TV_ERR_SELECTION";
     case TV_ERR_BOUNDS: return "TV_ERR_BOUNDS";
+    case TV_ERR_VALUE: return "TV_ERR_VALUE";
     default: return "TV_ERR_UNKNOWN";
   }
 }
@@ -129,6 +130,21 @@ int tv_launch_refresh(const tv_shape* s, const int32_t* parents, const int32_t* 
 
 int tv_launch_indexer(const tv_shape* s, int d_idx, const void* q_idx, const void* k_idx,
                       const int32_t* L, int32_t* sel, void* workspace, int32_t* status,
+                      cudaStream_t stream);
+
+int tv_launch_logprobs(const tv_shape* s, int vocab, int64_t ld, int logits_dtype,
+                       const void* logits, int n_tok, const int32_t* tokens, const int32_t* nodes,
+                       float scale, int n_top, float* lse, float* entropy, float* logprobs,
+                       int32_t* top_ids, float* top_logprobs, int32_t* target, int32_t* status,
+                       cudaStream_t stream);
+size_t tv_pages_workspace(const tv_shape* s);
+int tv_launch_fork(const tv_shape* s, const int32_t* source, const int32_t* keep, int32_t* L,
+                   int32_t* refs, void* const pools[6], void* keys, int d_idx, void* workspace,
+                   int32_t* status, cudaStream_t stream);
+int tv_launch_reserve(const tv_shape* s, const int32_t* need, const int32_t* L, int32_t* refs,
+                      void* workspace, int32_t* status, cudaStream_t stream);
+int tv_launch_compact(const tv_shape* s, const int32_t* L, int32_t* refs, void* const pools[6],
+                      int32_t* remap, int32_t* n_live, void* workspace, int32_t* status,
                       cudaStream_t stream);
 
 // ---- split-KV geometry of the SIMT kernel -----------------------------------------------------
@@ -501,5 +517,149 @@ extern "C" int tv_indexer_topk(const tv_shape* s, int d_idx, const void* q_idx, 
     return tv_set_error(TV_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", fn, ws_bytes,
                         need);
   return tv_launch_indexer(s, d_idx, q_idx, k_idx, L, sel, workspace, status,
+                           (cudaStream_t)stream);
+}
+
+// ---- log probabilities ----------------------------------------------------------------------------
+extern "C" int tv_token_logprobs(const tv_shape* s, int32_t vocab, int64_t ld, int32_t logits_dtype,
+                                 const void* logits, int32_t n_tok, const int32_t* tokens,
+                                 const int32_t* nodes, float scale, int32_t n_top, float* lse,
+                                 float* entropy, float* logprobs, int32_t* top_ids,
+                                 float* top_logprobs, int32_t* target, int32_t* status,
+                                 tv_stream_t stream) {
+  const char* fn = "tv_token_logprobs";
+  if (int rc = check_shape(s, fn)) return rc;
+  if (vocab < 1 || vocab > (1 << 30) || ld < vocab || ld > ((int64_t)1 << 40))
+    return tv_set_error(TV_ERR_SHAPE, "%s: vocab = %d outside 1..2^30 or ld = %lld < vocab", fn, vocab,
+                        (long long)ld);
+  if (logits_dtype != TV_F32 && logits_dtype != TV_BF16)
+    return tv_set_error(TV_ERR_ARG, "%s: unknown logits_dtype %d", fn, logits_dtype);
+  if (n_tok < 0 || n_tok > 1024 || n_top < 0 || n_top > 32)
+    return tv_set_error(TV_ERR_SHAPE, "%s: n_tok = %d outside 0..1024 or n_top = %d outside 0..32", fn,
+                        n_tok, n_top);
+  if (!(scale > 0.f) || !(scale < 1e30f))
+    return tv_set_error(TV_ERR_ARG, "%s: scale must be a positive finite number", fn);
+  if (s->B == 0) return TV_OK;
+  TV_REQUIRE(logits, fn);
+  TV_REQUIRE(status, fn);
+  if (n_tok > 0) {
+    TV_REQUIRE(tokens, fn);
+    TV_REQUIRE(logprobs, fn);
+    if (nodes == nullptr && n_tok > s->D)
+      return tv_set_error(TV_ERR_ARG, "%s: nodes is null and n_tok = %d > D = %d", fn, n_tok, s->D);
+  }
+  if (n_top > 0) {
+    TV_REQUIRE(top_ids, fn);
+    TV_REQUIRE(top_logprobs, fn);
+  }
+  if ((uintptr_t)logits % (logits_dtype == TV_BF16 ? 2 : 4) != 0)
+    return tv_set_error(TV_ERR_ARG, "%s: logits must be aligned to their type", fn);
+  return tv_launch_logprobs(s, vocab, ld, logits_dtype, logits, n_tok, tokens, nodes, scale, n_top,
+                            lse, entropy, logprobs, top_ids, top_logprobs, target, status,
+                            (cudaStream_t)stream);
+}
+
+// ---- pages ----------------------------------------------------------------------------------------
+// Checks shared by the tv_pages_* calls: the shape has pools, the workspace is large enough.
+static int check_pages(const tv_shape* s, const char* fn, void* workspace, size_t ws_bytes) {
+  if (s->page_tokens == 0)
+    return tv_set_error(TV_ERR_SHAPE, "%s: the shape has no page pools (page_tokens = 0)", fn);
+  if (s->B == 0) return TV_OK;
+  TV_REQUIRE(workspace, fn);
+  if (((uintptr_t)workspace) % 256 != 0)
+    return tv_set_error(TV_ERR_ARG, "%s: workspace must be 256-byte aligned", fn);
+  const size_t need = tv_pages_workspace(s);
+  if (ws_bytes < need)
+    return tv_set_error(TV_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", fn, ws_bytes,
+                        need);
+  return TV_OK;
+}
+
+// The pools of the active layers, null and alignment checks made (copies move 16 bytes at a time).
+static int page_pools(const tv_shape* s, const char* fn, void* rawK, void* rawV, void* c4K,
+                      void* c4V, void* c128K, void* c128V, void* pools[6]) {
+  TV_REQUIRE(rawK, fn);
+  TV_REQUIRE(rawV, fn);
+  if (has_c4(s)) {
+    TV_REQUIRE(c4K, fn);
+    TV_REQUIRE(c4V, fn);
+  }
+  if (has_c128(s)) {
+    TV_REQUIRE(c128K, fn);
+    TV_REQUIRE(c128V, fn);
+  }
+  void* const p[6] = {rawK, rawV, has_c4(s) ? c4K : nullptr, has_c4(s) ? c4V : nullptr,
+                      has_c128(s) ? c128K : nullptr, has_c128(s) ? c128V : nullptr};
+  uintptr_t bits = 0;
+  for (int i = 0; i < 6; ++i) {
+    pools[i] = p[i];
+    bits |= (uintptr_t)p[i];
+  }
+  if (bits & 15u) return tv_set_error(TV_ERR_ARG, "%s: the pools must be 16-byte aligned", fn);
+  return TV_OK;
+}
+
+extern "C" size_t tv_pages_workspace_size(const tv_shape* s) {
+  if (check_shape(s, "tv_pages_workspace_size") != TV_OK || s->B == 0 || s->page_tokens == 0)
+    return 0;
+  return tv_pages_workspace(s);
+}
+
+extern "C" int tv_pages_fork(const tv_shape* s, const int32_t* source, const int32_t* keep,
+                             int32_t* L, int32_t* page_refs, void* rawK, void* rawV, void* c4K,
+                             void* c4V, void* c128K, void* c128V, void* k_idx, int32_t d_idx,
+                             void* workspace, size_t ws_bytes, int32_t* status,
+                             tv_stream_t stream) {
+  const char* fn = "tv_pages_fork";
+  if (int rc = check_shape(s, fn)) return rc;
+  if (int rc = check_pages(s, fn, workspace, ws_bytes)) return rc;
+  if (k_idx != nullptr) {
+    if (!has_c4(s)) return tv_set_error(TV_ERR_ARG, "%s: k_idx needs C4 in comp_mask", fn);
+    if (d_idx < 8 || d_idx > 256 || d_idx % 8 != 0)
+      return tv_set_error(TV_ERR_SHAPE, "%s: d_idx = %d is not a multiple of 8 in 8..256", fn, d_idx);
+    if ((uintptr_t)k_idx & 15u)
+      return tv_set_error(TV_ERR_ARG, "%s: k_idx must be 16-byte aligned", fn);
+  }
+  if (s->B == 0) return TV_OK;
+  TV_REQUIRE(source, fn);
+  TV_REQUIRE(L, fn);
+  TV_REQUIRE(page_refs, fn);
+  TV_REQUIRE(status, fn);
+  void* pools[6];
+  if (int rc = page_pools(s, fn, rawK, rawV, c4K, c4V, c128K, c128V, pools)) return rc;
+  return tv_launch_fork(s, source, keep, L, page_refs, pools, k_idx, d_idx, workspace, status,
+                        (cudaStream_t)stream);
+}
+
+extern "C" int tv_pages_reserve(const tv_shape* s, const int32_t* need, const int32_t* L,
+                                int32_t* page_refs, void* workspace, size_t ws_bytes,
+                                int32_t* status, tv_stream_t stream) {
+  const char* fn = "tv_pages_reserve";
+  if (int rc = check_shape(s, fn)) return rc;
+  if (int rc = check_pages(s, fn, workspace, ws_bytes)) return rc;
+  if (s->B == 0) return TV_OK;
+  TV_REQUIRE(need, fn);
+  TV_REQUIRE(L, fn);
+  TV_REQUIRE(page_refs, fn);
+  TV_REQUIRE(status, fn);
+  return tv_launch_reserve(s, need, L, page_refs, workspace, status, (cudaStream_t)stream);
+}
+
+extern "C" int tv_pages_compact(const tv_shape* s, const int32_t* L, int32_t* page_refs, void* rawK,
+                                void* rawV, void* c4K, void* c4V, void* c128K, void* c128V,
+                                int32_t* remap, int32_t* n_live, void* workspace, size_t ws_bytes,
+                                int32_t* status, tv_stream_t stream) {
+  const char* fn = "tv_pages_compact";
+  if (int rc = check_shape(s, fn)) return rc;
+  if (int rc = check_pages(s, fn, workspace, ws_bytes)) return rc;
+  if (s->B == 0) return TV_OK;
+  TV_REQUIRE(L, fn);
+  TV_REQUIRE(page_refs, fn);
+  TV_REQUIRE(remap, fn);
+  TV_REQUIRE(n_live, fn);
+  TV_REQUIRE(status, fn);
+  void* pools[6];
+  if (int rc = page_pools(s, fn, rawK, rawV, c4K, c4V, c128K, c128V, pools)) return rc;
+  return tv_launch_compact(s, L, page_refs, pools, remap, n_live, workspace, status,
                            (cudaStream_t)stream);
 }

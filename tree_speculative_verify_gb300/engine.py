@@ -43,11 +43,14 @@ class DeviceState:
     L: torch.Tensor
     k_idx: torch.Tensor = None    # [B][c4_cap][64] bf16 indexer keys (sparse C4 path only)
     page_table: torch.Tensor = None   # [B][max_pages] int32 (paged pools only)
+    page_refs: torch.Tensor = None    # [n_pool_pages] int32 holders (managed pools only)
+    page_ws: torch.Tensor = None      # workspace of the tv_pages_* calls (managed pools only)
 
     def clone(self):
         return DeviceState(*(t.clone() for t in (self.rawK, self.rawV, self.c4K, self.c4V,
                                                  self.c128K, self.c128V, self.L)),
-                           k_idx=self.k_idx, page_table=self.page_table)
+                           k_idx=self.k_idx, page_table=self.page_table,
+                           page_refs=self.page_refs, page_ws=self.page_ws)
 
 
 @dataclass
@@ -80,6 +83,13 @@ class RoundBuffers:
     workspace: torch.Tensor
     q_idx: torch.Tensor = None    # [B][64] bf16 indexer queries (sparse C4 path only)
     idx_ws: torch.Tensor = None   # indexer score workspace
+    need: torch.Tensor = None     # [B] int32 positions to reserve per round (managed pools only)
+    logits: torch.Tensor = None   # [B][D][vocab] the model's logits (scored rounds, alloc_scores)
+    logits_lse: torch.Tensor = None     # [B][D] fp32
+    entropy: torch.Tensor = None        # [B][D] fp32, nats
+    draft_logprobs: torch.Tensor = None  # [B][D] fp32, every draft token under its parent
+    top_ids: torch.Tensor = None        # [B][D][n_top] int32
+    top_logprobs: torch.Tensor = None   # [B][D][n_top] fp32
 
 
 def alloc_state(wl, device="cuda"):
@@ -133,6 +143,60 @@ def alloc_paged(wl, page_tokens, attn_kernel=_lib.TV_ATTN_AUTO, spare_pages=None
     return shape, st
 
 
+def alloc_pool(wl, page_tokens, n_pool_pages, attn_kernel=_lib.TV_ATTN_AUTO, stage_chain=0,
+               device="cuda"):
+    """Page pools whose pages tv_pages_fork, tv_pages_reserve and tv_pages_compact manage (see
+    include/treeverify.h): like ``alloc_paged``, but only the pages that the committed prefixes
+    cover are mapped (in order, from page 0) and ``page_refs`` counts the holders of every page;
+    ``verify_round`` reserves each round's pages.  Returns (shape, state)."""
+    P, n_pool = int(page_tokens), int(n_pool_pages)
+    max_pages = -(-wl.raw_cap // P)
+    table = torch.full((wl.B, max_pages), -1, dtype=torch.int32)
+    used = 0
+    for b in range(wl.B):
+        n = -(-int(wl.L[b]) // P)
+        table[b, :n] = torch.arange(used, used + n, dtype=torch.int32)
+        used += n
+    if used > n_pool:
+        raise ValueError(f"the prefixes need {used} pages, the pool has {n_pool}")
+    refs = torch.zeros(n_pool, dtype=torch.int32)
+    refs[:used] = 1
+    dt = wl.torch_dtype
+    z = lambda rows: torch.zeros((n_pool, max(rows, 1), wl.d), dtype=dt, device=device)
+    rawK, rawV = z(P), z(P)
+    for b in range(wl.B):
+        L = int(wl.L[b])
+        for g in range(-(-L // P)):
+            lo, hi = g * P, min((g + 1) * P, L)
+            rawK[int(table[b, g]), : hi - lo] = wl.rawK[b, lo:hi].to(device)
+            rawV[int(table[b, g]), : hi - lo] = wl.rawV[b, lo:hi].to(device)
+    k_idx = None
+    if wl.k_idx is not None:
+        k_idx = torch.zeros((wl.B, max_pages * P // 4, wl.k_idx.shape[2]), dtype=wl.k_idx.dtype,
+                            device=device)
+        k_idx[:, : wl.k_idx.shape[1]] = wl.k_idx.to(device)
+    st = DeviceState(rawK=rawK, rawV=rawV, c4K=z(P // 4), c4V=z(P // 4), c128K=z(P // 128),
+                     c128V=z(P // 128), L=torch.as_tensor(wl.L, dtype=torch.int32).to(device),
+                     k_idx=k_idx, page_table=table.to(device), page_refs=refs.to(device))
+    shape = shape_for(wl, attn_kernel, stage_chain=stage_chain)
+    shape.raw_cap, shape.c4_cap, shape.c128_cap = max_pages * P, max_pages * P // 4, max_pages * P // 128
+    shape.page_tokens, shape.max_pages, shape.n_pool_pages = P, max_pages, n_pool
+    shape.page_table = st.page_table.data_ptr()
+    st.page_ws = torch.empty(_lib.tv_pages_workspace_size(shape), dtype=torch.uint8, device=device)
+    return shape, st
+
+
+def alloc_scores(rb, shape, vocab, n_top=8, dtype=torch.bfloat16, device="cuda"):
+    """Adds the buffers of a scored round to ``rb``: the logits, which the caller's model fills
+    before the acceptance, and what ``score`` makes of them."""
+    B, D = shape.B, shape.D
+    f = lambda *s: torch.zeros(s, dtype=torch.float32, device=device)
+    rb.logits = torch.zeros((B, D, vocab), dtype=dtype, device=device)
+    rb.logits_lse, rb.entropy, rb.draft_logprobs = f(B, D), f(B, D), f(B, D)
+    rb.top_ids = torch.zeros((B, D, n_top), dtype=torch.int32, device=device)
+    rb.top_logprobs = f(B, D, n_top)
+
+
 def alloc_round(wl, shape, device="cuda"):
     dt = wl.torch_dtype
     B, D, H, d = wl.B, wl.D, wl.H, wl.d
@@ -163,7 +227,8 @@ def alloc_round(wl, shape, device="cuda"):
         workspace=torch.empty(max(ws, 256), dtype=torch.uint8, device=device),
         q_idx=None if wl.q_idx is None else wl.q_idx.to(device),
         idx_ws=None if wl.q_idx is None else torch.empty(
-            max(_lib.tv_indexer_workspace_size(shape), 256), dtype=torch.uint8, device=device))
+            max(_lib.tv_indexer_workspace_size(shape), 256), dtype=torch.uint8, device=device),
+        need=torch.full((B,), D, **i32) if shape.page_tokens else None)
 
 
 def prefill(shape, st, rb, stream=None):
@@ -207,14 +272,47 @@ def refresh(shape, st, rb, stream=None):
                            st.c4V, st.c128K, st.c128V, st.L, rb.committed, rb.status, stream)
 
 
-def verify_round(shape, st, rb, scale=None, stream=None, commit=True, select=False):
+def score(shape, rb, inv_temperature=1.0, stream=None):
+    """From ``rb.logits`` to the round's target tokens, the alternatives of every node, the draft
+    tokens' log probabilities under their parents, and the entropies."""
+    _lib.tv_token_logprobs(shape, rb.logits, rb.draft, rb.parents, inv_temperature, rb.logits_lse,
+                           rb.entropy, rb.draft_logprobs, rb.top_ids, rb.top_logprobs, rb.target,
+                           rb.status, stream)
+
+
+def reserve(shape, st, rb, need=None, stream=None):
+    """Pages for the next ``need`` positions of every request (default: the round's D)."""
+    _lib.tv_pages_reserve(shape, rb.need if need is None else need, st.L, st.page_refs, st.page_ws,
+                          rb.status, stream)
+
+
+def fork(shape, st, rb, source, keep=None, stream=None):
+    """Releases, truncates and branches the slots of a managed pool: ``source[b]`` is b (stays), -1
+    (released) or the slot that b becomes a copy of; ``keep`` truncates (see tv_pages_fork)."""
+    _lib.tv_pages_fork(shape, source, keep, st.L, st.page_refs, st.rawK, st.rawV, st.c4K, st.c4V,
+                       st.c128K, st.c128V, st.k_idx, st.page_ws, rb.status, stream)
+
+
+def compact(shape, st, rb, remap, n_live, stream=None):
+    """Moves the live pages of a managed pool into its ``n_live`` lowest pages."""
+    _lib.tv_pages_compact(shape, st.L, st.page_refs, st.rawK, st.rawV, st.c4K, st.c4V, st.c128K,
+                          st.c128V, remap, n_live, st.page_ws, rb.status, stream)
+
+
+def verify_round(shape, st, rb, scale=None, stream=None, commit=True, select=False, scored=False):
     """One target-verify round: plan, scratch pad, attention, acceptance, refresh; with
-    ``select`` the indexer first picks the sparse path's C4 entries on the device."""
+    ``select`` the indexer first picks the sparse path's C4 entries on the device, with ``scored``
+    the target tokens come from ``rb.logits`` (else the caller has filled ``rb.target``).  On a
+    managed pool the round's pages are reserved first."""
+    if st.page_refs is not None:
+        reserve(shape, st, rb, None, stream)
     if select:
         indexer(shape, st, rb, stream)
     plan(shape, st, rb, stream)
     branch_compress(shape, st, rb, stream)
     attention(shape, st, rb, scale, stream)
+    if scored:
+        score(shape, rb, 1.0, stream)
     accept(shape, st, rb, stream)
     if commit:
         refresh(shape, st, rb, stream)
@@ -226,6 +324,8 @@ def draft_decode(shape, st, rb, scale=None, stream=None):
     attends to the prefix and its own ancestors, with the scratch pad isolating blocks closed
     inside the tree -- the verify round's plan, scratch-pad and attention calls on the draft
     step's tree, without acceptance or commit (nothing is accepted until the target verifies)."""
+    if st.page_refs is not None:
+        reserve(shape, st, rb, None, stream)
     plan(shape, st, rb, stream)
     branch_compress(shape, st, rb, stream)
     attention(shape, st, rb, scale, stream)
@@ -243,17 +343,18 @@ class RoundGraph:
     may change between replays.
     """
 
-    def __init__(self, shape, st, rb, scale=None, commit=True, prologue=None, select=False):
+    def __init__(self, shape, st, rb, scale=None, commit=True, prologue=None, select=False,
+                 scored=False):
         # one eager round first, without the commit (the persistent state is left as it was):
         # the library's once-per-device set-up happens outside the capture
-        verify_round(shape, st, rb, scale, None, False, select)
+        verify_round(shape, st, rb, scale, None, False, select, scored)
         torch.cuda.synchronize()
         self.graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(self.graph):
             stream = torch.cuda.current_stream()
             if prologue is not None:
                 prologue()
-            verify_round(shape, st, rb, scale, stream, commit, select)
+            verify_round(shape, st, rb, scale, stream, commit, select, scored)
 
     def replay(self):
         self.graph.replay()
