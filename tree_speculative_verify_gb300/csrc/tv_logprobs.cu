@@ -8,13 +8,14 @@
 // grows; the partial triples are joined over the CTA, and over the CTAs of a cluster that share a
 // row when there are few rows.
 //
-// The alternatives come out of the same pass.  K distinct threads whose largest logits are >= t
-// show that the K-th largest logit of the row is >= t, so a logit below t is no alternative: after
-// the first tile of the row (and again after 2, 4, 8, ... tiles) such a t is taken from the
-// threads' running maxima, and only logits >= t, a few per tile, go to a candidate list in shared
-// memory.  At the end the list is ranked by counting: a key's place is the number of larger keys
-// (a key is the logit's order, then the lower id, so keys differ).  A list that overflows (rows of
-// many equal logits, ascending rows) is replaced by one scan of the row per alternative.
+// The alternatives.  K distinct threads whose largest logits are >= t show that the K-th largest
+// logit is >= t, so a logit below t is no alternative.  In the pass a thread only notes its largest
+// logit, the tile that holds it, and the largest of its other tiles; at the end t is taken from
+// the threads' largest logits, the few threads at or above t look at that one tile again, and where
+// a second tile reaches t a warp looks at all of the thread's vectors.  The logits found, little
+// more than K, are ranked by counting: a key's place is the number of larger keys (a key is the
+// logit's order, then the lower id, so keys differ).  Rows of so many equal logits that the list
+// overflows take one scan per alternative instead.
 #include <cooperative_groups.h>
 #include <float.h>
 
@@ -28,13 +29,14 @@ using sm100::fma_f32x2;
 using sm100::pack_f32x2;
 using sm100::unpack_f32x2;
 
-constexpr int kLpThreads = 256;
+constexpr int kLpThreads = 128;
 constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kLpUnroll = 4;                        // 16-byte vectors per thread and tile
 constexpr int kLpTile = kLpThreads * kLpUnroll;     // vectors per tile
+constexpr int kLpStages = 4;                        // tiles in flight
 constexpr int kLpMaxTop = 32;
 constexpr int kLpCand = 1024;                       // candidate list
-constexpr int kLpMaxRanks = 8;
+constexpr int kLpMaxRanks = 16;
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct LogprobArgs {
@@ -180,26 +182,32 @@ struct Row {
 
 __device__ __forceinline__ uint64_t max_u64(uint64_t a, uint64_t b) { return a > b ? a : b; }
 
-// Shared memory of one CTA.  part and top are read by the other CTAs of the cluster.
+// Shared memory of one CTA.  Of rank 0's, the other CTAs of the cluster write part and peer.
 struct LpShared {
+  uint4 ring[kLpStages][kLpUnroll][kLpThreads];   // tiles in flight; a thread reads only its own
   Partial warp_part[kLpWarps];
-  Partial part;                    // the CTA's share of the row
-  uint64_t top[kLpMaxTop];         // its largest keys, descending (0: none)
-  uint32_t bound[2][kLpWarps][2];
-  int count, kept;
+  Partial part[kLpMaxRanks];       // the CTAs' shares of the row
+  uint64_t top[kLpMaxTop];         // largest keys, descending (0: none)
+  uint32_t bound[kLpWarps][2];
+  int count, columns;
   uint64_t scan[kLpWarps];
   uint64_t cand[kLpCand];
-  uint64_t sel[kLpCand];
+  uint64_t peer[kLpMaxRanks * kLpMaxTop];   // the CTAs' top lists
+  uint64_t peer_bound;
+  uint8_t column[kLpThreads];      // threads with more than one tile to look at again
 };
+static_assert(kLpMaxRanks * kLpMaxTop <= kLpCand, "every CTA's keys fit into cand");
 
 // Lower bound (as an order) of the K-th largest logit that the CTA has seen, from the threads'
-// largest ones: either K threads of one warp are at or above it, or ceil(K / 8) of every warp.
-__device__ __forceinline__ uint32_t kth_bound(LpShared& sm, int parity, float m, int K) {
+// largest ones m: either K threads of one warp are at or above it, or ceil(K / warps) of every
+// warp.  The order of the lowest finite value where there are fewer.
+__device__ __forceinline__ uint32_t kth_bound(LpShared& sm, float m, int K) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int r = (K + kLpWarps - 1) / kLpWarps;
   uint32_t o = order_of(m);
   uint32_t kth = 0u, rth = 0u;
-  const int rounds = K <= 4 ? K : r;
+  const int rounds = K <= kLpWarps ? K : r;
+#pragma unroll 1
   for (int i = 1; i <= rounds; ++i) {
     const uint32_t w = __reduce_max_sync(0xffffffffu, o);
     if (i == r) rth = w;
@@ -208,20 +216,21 @@ __device__ __forceinline__ uint32_t kth_bound(LpShared& sm, int parity, float m,
     if (lane == __ffs(at) - 1) o = 0u;
   }
   if (lane == 0) {
-    sm.bound[parity][warp][0] = kth;
-    sm.bound[parity][warp][1] = rth;
+    sm.bound[warp][0] = kth;
+    sm.bound[warp][1] = rth;
   }
   __syncthreads();
   uint32_t one = 0u, every = 0xffffffffu;
 #pragma unroll
   for (int w = 0; w < kLpWarps; ++w) {
-    one = max(one, sm.bound[parity][w][0]);
-    every = min(every, sm.bound[parity][w][1]);
+    one = max(one, sm.bound[w][0]);
+    every = min(every, sm.bound[w][1]);
   }
   uint32_t t = max(one, every);
-  if (t < kOrderLowest && K > 4) {
-    // some warp has too few logits (a short or masked stretch): the K-th of one warp after all
+  if (t < kOrderLowest && K > kLpWarps) {
+    // some warp has too few logits (a short or masked row): the K-th of one warp after all
     o = order_of(m);
+#pragma unroll 1
     for (int i = 1; i < K; ++i) {
       const uint32_t w = __reduce_max_sync(0xffffffffu, o);
       if (w < kOrderLowest) break;
@@ -230,12 +239,28 @@ __device__ __forceinline__ uint32_t kth_bound(LpShared& sm, int parity, float m,
     }
     o = __reduce_max_sync(0xffffffffu, o);
     __syncthreads();
-    if (lane == 0) sm.bound[parity][warp][0] = o;
+    if (lane == 0) sm.bound[warp][0] = o;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kLpWarps; ++w) t = max(t, sm.bound[parity][w][0]);
+    for (int w = 0; w < kLpWarps; ++w) t = max(t, sm.bound[w][0]);
   }
   return max(t, kOrderLowest);
+}
+
+// Appends the logits of vector i that are >= bound to the candidate list.
+template <typename T>
+__device__ __forceinline__ void list_vector(LpShared& sm, const Row<T>& row, int i, int hi,
+                                            float bound) {
+  const uint4 q = row.edge(i, hi);
+  if (Row<T>::largest(q) < bound) return;
+  float x[Row<T>::kVec];
+  Row<T>::unpack(q, x);
+#pragma unroll
+  for (int j = 0; j < Row<T>::kVec; ++j)
+    if (x[j] >= bound) {
+      const int at = atomicAdd(&sm.count, 1);
+      if (at < kLpCand) sm.cand[at] = key_of(x[j], row.id(i, j));
+    }
 }
 
 // The CTA's K largest keys by one scan of its vectors [lo, hi) per key, into sm.top.
@@ -266,7 +291,7 @@ __device__ __noinline__ void scan_top(LpShared& sm, const Row<T>& row, int lo, i
 }
 
 // Places of the n keys of `list` among each other: out[place] = key for the places below K.
-__device__ __forceinline__ void rank_keys(const uint64_t* list, int n, int K, uint64_t* out) {
+__device__ __noinline__ void rank_keys(const uint64_t* list, int n, int K, uint64_t* out) {
   for (int i = threadIdx.x; i < n; i += kLpThreads) {
     const uint64_t key = list[i];
     int place = 0;
@@ -276,10 +301,28 @@ __device__ __forceinline__ void rank_keys(const uint64_t* list, int n, int K, ui
   }
 }
 
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// Joins the partials held by the lanes of a warp (every lane gets the result).
+template <int kLanes>
+__device__ __forceinline__ Partial warp_join(Partial p, ExpScale k) {
+  const uint32_t top = __reduce_max_sync(0xffffffffu, order_of(p.m));
+  rebase(p, logit_of_order(top), k);
+#pragma unroll
+  for (int o = kLanes / 2; o > 0; o >>= 1) {
+    p.s += __shfl_xor_sync(0xffffffffu, p.s, o);
+    p.t += __shfl_xor_sync(0xffffffffu, p.t, o);
+  }
+  return p;
+}
+
 template <typename T, bool kCluster>
 __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const T* __restrict__ logits,
                                                               const LogprobArgs a, int ranks) {
-  __shared__ LpShared sm;
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  LpShared& sm = *reinterpret_cast<LpShared*>(smem_raw);
   const int rank = kCluster ? (int)cg::this_cluster().block_rank() : 0;
   const int64_t r = kCluster ? blockIdx.x / ranks : blockIdx.x;
   const int b = (int)(r / a.D), v = (int)(r - (int64_t)b * a.D);
@@ -292,35 +335,73 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const T* __restric
   const int per = kCluster ? (row.n_vec + ranks - 1) / ranks : row.n_vec;
   const int lo = min(row.n_vec, rank * per), hi = min(row.n_vec, lo + per);
 
-  if (tid == 0) sm.count = sm.kept = 0;
-  if (tid < K) sm.top[tid] = 0ull;
-  uint4 next[kLpUnroll];
-  auto fetch = [&](int i0) {
-    if (i0 > 0 && i0 + kLpTile <= hi && i0 + kLpTile < row.n_vec) {   // no edge in the tile
+  // a tile's copies: whole vectors asynchronously, the row's ends and what lies past hi at once
+  const T* src = row.p + ((lo + tid) * kVec - row.skew);
+  const uint32_t ring = sm100::smem_u32(&sm.ring[0][0][tid]);
+  constexpr uint32_t kStageBytes = sizeof(sm.ring[0]);
+  const int inner_hi = min(hi, row.n_vec - 1);
+  auto fetch = [&](int t) {
+    const int i0 = lo + t * kLpTile;
+    const uint32_t slot = ring + t % kLpStages * kStageBytes;
+    const T* at = src + (int64_t)t * (kLpTile * kVec);
+    if (i0 > 0 && i0 + kLpTile <= inner_hi) {
 #pragma unroll
-      for (int u = 0; u < kLpUnroll; ++u) next[u] = row.whole(i0 + u * kLpThreads + tid);
+      for (int u = 0; u < kLpUnroll; ++u)
+        cp_async_16(slot + u * kLpThreads * 16, at + u * kLpThreads * kVec);
     } else {
-#pragma unroll
-      for (int u = 0; u < kLpUnroll; ++u) next[u] = row.edge(i0 + u * kLpThreads + tid, hi);
+#pragma unroll 1
+      for (int u = 0; u < kLpUnroll; ++u) {
+        const int i = i0 + u * kLpThreads + tid;
+        if (i > 0 && i < inner_hi)
+          cp_async_16(slot + u * kLpThreads * 16, at + u * kLpThreads * kVec);
+        else
+          sm.ring[t % kLpStages][u][tid] = row.edge(i, hi);
+      }
     }
   };
+  const int tiles = (hi - lo + kLpTile - 1) / kLpTile;
+#pragma unroll 1
+  for (int t = 0; t < kLpStages - 1; ++t) {
+    if (t < tiles) fetch(t);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  if constexpr (kCluster) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  // the first given tokens of this row, so that their logits arrive under the others
+  const bool first = rank == 0 && tid < a.n_tok;
+  int given_node = -1, given_tok = -1;
+  float given = 0.f;
+  if (first) {
+    const int64_t at = (int64_t)b * a.n_tok + tid;
+    given_node = a.nodes ? a.nodes[at] : tid;
+    given_tok = a.tokens[at];
+    if (given_node == v && given_tok >= 0 && given_tok < a.vocab) given = load_f(row.p + given_tok);
+  }
+  if (tid == 0) sm.count = sm.columns = 0;
+  if (tid < K) sm.top[tid] = 0ull;
+
   Partial p = {-INFINITY, 0.f, 0.f};
-  float bound = 0.f;
-  int parity = 0, refresh = 1;
-  fetch(lo);
-  for (int t = 0, i0 = lo; i0 < hi; ++t, i0 += kLpTile) {
+  float second = -INFINITY;   // largest logit outside the tile of the largest
+  int at_tile = 0;
+#pragma unroll 1
+  for (int t = 0; t < tiles; ++t) {
+    if (t + kLpStages - 1 < tiles) fetch(t + kLpStages - 1);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    asm volatile("cp.async.wait_group %0;" ::"n"(kLpStages - 1) : "memory");
+    const uint4(*tile)[kLpThreads] = sm.ring[t % kLpStages];
     uint4 w[kLpUnroll];
-    float vmax[kLpUnroll];
-#pragma unroll
-    for (int u = 0; u < kLpUnroll; ++u) w[u] = next[u];
-    if (i0 + kLpTile < hi) fetch(i0 + kLpTile);
-    float m = p.m;
+    float m = -INFINITY;
 #pragma unroll
     for (int u = 0; u < kLpUnroll; ++u) {
-      vmax[u] = Row<T>::largest(w[u]);
-      m = fmaxf(m, vmax[u]);
+      w[u] = tile[u][tid];
+      m = fmaxf(m, Row<T>::largest(w[u]));
     }
-    rebase(p, m, ks);
+    if (m > p.m) {
+      second = p.m;
+      at_tile = t;
+      rebase(p, m, ks);
+    } else {
+      second = fmaxf(second, m);
+    }
     const float base = p.m == -INFINITY ? 0.f : p.m;
     const uint64_t neg = pack_f32x2(-base, -base), c2 = pack_f32x2(ks.c, ks.c);
     uint64_t s2 = pack_f32x2(0.f, 0.f), t2 = s2;
@@ -330,9 +411,8 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const T* __restric
       Row<T>::unpack(w[u], x);
 #pragma unroll
       for (int j = 0; j < kVec; j += 2) {
-        float d0, d1, y0, y1;
-        unpack_f32x2(add_f32x2(pack_f32x2(x[j], x[j + 1]), neg), d0, d1);
-        const uint64_t d = pack_f32x2(max_nan(d0, ks.dmin), max_nan(d1, ks.dmin));
+        const uint64_t d = add_f32x2(pack_f32x2(x[j], x[j + 1]), neg);
+        float y0, y1;
         unpack_f32x2(mul_f32x2(d, c2), y0, y1);
         const uint64_t e = pack_f32x2(exp2_approx(y0), exp2_approx(y1));
         s2 = add_f32x2(s2, e);
@@ -343,72 +423,89 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const T* __restric
     unpack_f32x2(s2, s0, s1);
     unpack_f32x2(t2, t0, t1);
     p.s += s0 + s1;
-    p.t += t0 + t1;
-    // candidates; the first tile sets the bound before it looks at its own logits
-    if (t == 0) bound = logit_of_order(kth_bound(sm, 0, p.m, K));
-#pragma unroll
-    for (int u = 0; u < kLpUnroll; ++u) {
-      if (vmax[u] >= bound) {
+    float dt = t0 + t1;
+    if (!(dt == dt)) {   // a masked logit: -inf times 0; the differences are bounded below instead
+      dt = 0.f;
+#pragma unroll 1
+      for (int u = 0; u < kLpUnroll; ++u) {
         float x[kVec];
-        Row<T>::unpack(w[u], x);
+        Row<T>::unpack(tile[u][tid], x);
 #pragma unroll
-        for (int j = 0; j < kVec; ++j)
-          if (x[j] >= bound) {
-            const int at = atomicAdd(&sm.count, 1);
-            if (at < kLpCand) sm.cand[at] = key_of(x[j], row.id(i0 + u * kLpThreads + tid, j));
-          }
+        for (int j = 0; j < kVec; ++j) {
+          const float d = max_nan(x[j] - base, ks.dmin);
+          dt += d * exp2_approx(d * ks.c);
+        }
       }
     }
-    if (t == refresh) {
-      parity ^= 1;
-      bound = logit_of_order(kth_bound(sm, parity, p.m, K));
-      refresh = 2 * refresh + 1;   // after 2, 4, 8, ... tiles
-    }
+    p.t += dt;
   }
   // the CTA's sums
   const float largest = p.m;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const Partial q = {__shfl_xor_sync(0xffffffffu, p.m, o), __shfl_xor_sync(0xffffffffu, p.s, o),
-                       __shfl_xor_sync(0xffffffffu, p.t, o)};
-    p = join(p, q, ks);
-  }
+  p = warp_join<32>(p, ks);
   if (lane == 0) sm.warp_part[warp] = p;
-  // the final bound leaves little of the list (its barrier also publishes the list and the sums)
-  const uint32_t final_bound = kth_bound(sm, parity ^ 1, largest, K);
-  p = sm.warp_part[0];
-#pragma unroll
-  for (int w = 1; w < kLpWarps; ++w) p = join(p, sm.warp_part[w], ks);
-  if (tid == 0) sm.part = p;
-  const int n = sm.count;
-  if (n > kLpCand) {
-    scan_top(sm, row, lo, hi, K);
-  } else {
-    for (int i = tid; i < n; i += kLpThreads) {
-      const uint64_t key = sm.cand[i];
-      if ((uint32_t)(key >> 32) >= final_bound) sm.sel[atomicAdd(&sm.kept, 1)] = key;
-    }
-    __syncthreads();
-    rank_keys(sm.sel, sm.kept, K, sm.top);
+  const float bound = logit_of_order(kth_bound(sm, largest, K));   // (its barrier: warp_part)
+  p = warp_join<kLpWarps>(sm.warp_part[lane % kLpWarps], ks);
+  if (second >= bound) {
+    sm.column[atomicAdd(&sm.columns, 1)] = (uint8_t)tid;
+  } else if (largest >= bound) {
+#pragma unroll 1
+    for (int u = 0; u < kLpUnroll; ++u)
+      list_vector(sm, row, lo + at_tile * kLpTile + u * kLpThreads + tid, hi, bound);
   }
   __syncthreads();
+  const int columns = sm.columns;
+#pragma unroll 1
+  for (int k = warp; k < columns; k += kLpWarps) {
+    if (*(volatile int*)&sm.count > kLpCand) break;   // too many equal logits
+    for (int i = lo + sm.column[k] + lane * kLpThreads; i < hi; i += 32 * kLpThreads)
+      list_vector(sm, row, i, hi, bound);
+  }
+  __syncthreads();
+  const int n = sm.count;
+  if (n > kLpCand)
+    scan_top(sm, row, lo, hi, K);
+  else
+    rank_keys(sm.cand, n, K, sm.top);
+  __syncthreads();
   if constexpr (kCluster) {
-    // rank 0 joins the CTAs' sums and keys
+    // every CTA leaves its sums and keys in rank 0's shared memory, which joins them
     auto cluster = cg::this_cluster();
-    cluster.sync();
-    if (rank == 0) {
-      for (int i = tid; i < ranks * K; i += kLpThreads) {
-        const int q = i / K;
-        sm.sel[i] = cluster.map_shared_rank(&sm, q)->top[i - q * K];
-      }
-      for (int q = 1; q < ranks; ++q) p = join(p, cluster.map_shared_rank(&sm, q)->part, ks);
-    }
-    cluster.sync();   // every CTA's shared memory has been read
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");   // rank 0 has started
+    LpShared* to = cluster.map_shared_rank(&sm, 0);
+    if (tid == 0) to->part[rank] = p;
+    if (tid < K) to->peer[rank * K + tid] = sm.top[tid];
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     if (rank != 0) return;
-    if (tid < K) sm.top[tid] = 0ull;
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    const Partial q = {-INFINITY, 0.f, 0.f};
+    p = warp_join<kLpMaxRanks>(lane % kLpMaxRanks < ranks ? sm.part[lane % kLpMaxRanks] : q, ks);
+    // the K-th largest of all keys is at least any CTA's K-th, and at least the least of the CTAs'
+    // ceil(K / ranks)-th
+    if (warp == 0) {
+      const int r_th = (K + ranks - 1) / ranks;
+      uint64_t one = lane < ranks ? sm.peer[lane * K + K - 1] : 0ull;
+      uint64_t every = lane < ranks ? sm.peer[lane * K + r_th - 1] : ~0ull;
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) {
+        const uint64_t x = __shfl_xor_sync(0xffffffffu, one, o);
+        const uint64_t y = __shfl_xor_sync(0xffffffffu, every, o);
+        one = x > one ? x : one;
+        every = y < every ? y : every;
+      }
+      if (lane == 0) {
+        sm.peer_bound = one > every ? one : every;
+        sm.count = 0;
+      }
+    }
     __syncthreads();
-    // (0 stands for no key: its place is behind the others, and equal places hold equal zeros)
-    rank_keys(sm.sel, ranks * K, K, sm.top);
+    if (tid < K) sm.top[tid] = 0ull;
+    const uint64_t least = sm.peer_bound;
+    for (int i = tid; i < ranks * K; i += kLpThreads) {
+      const uint64_t key = sm.peer[i];
+      if (key != 0ull && key >= least) sm.cand[atomicAdd(&sm.count, 1)] = key;
+    }
+    __syncthreads();
+    rank_keys(sm.cand, sm.count, K, sm.top);
     __syncthreads();
   }
 
@@ -438,7 +535,9 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const T* __restric
   // given tokens: this row takes those of its node, and row 0 those without a node or a token
   for (int i = tid; i < a.n_tok; i += kLpThreads) {
     const int64_t at = (int64_t)b * a.n_tok + i;
-    const int node = a.nodes ? a.nodes[at] : i, tok = a.tokens[at];
+    const bool early = i == tid && first;
+    const int node = early ? given_node : a.nodes ? a.nodes[at] : i;
+    const int tok = early ? given_tok : a.tokens[at];
     const bool wrong = node >= a.D || tok >= a.vocab;
     if (node < 0 || tok < 0 || wrong) {
       if (v == 0) {
@@ -446,9 +545,32 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const T* __restric
         if (wrong) record_error(a.status, TV_ERR_ARG);
       }
     } else if (node == v) {
-      a.logprobs[at] = log_prob(load_f(row.p + tok));
+      a.logprobs[at] = log_prob(early ? given : load_f(row.p + tok));
     }
   }
+}
+
+template <typename T, bool kCluster>
+static cudaError_t launch_kernel(const T* logits, const LogprobArgs& a, int64_t rows, int ranks,
+                                 cudaStream_t stream) {
+  auto kernel = logprobs_kernel<T, kCluster>;
+  const int smem = (int)sizeof(LpShared);
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess && ranks > 8)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(rows * ranks));
+  cfg.blockDim = dim3(kLpThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ranks;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = kCluster ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, logits, a, ranks);
 }
 
 template <typename T>
@@ -457,19 +579,9 @@ static cudaError_t launch_logprobs(const T* logits, const LogprobArgs& a, int64_
   // CTAs per row: enough for two per SM, each with a tile's worth of vectors
   const int64_t vecs = (int64_t)a.vocab * sizeof(T) / 16;
   int ranks = 1;
-  while (ranks < kLpMaxRanks && rows * ranks < 2 * 152 && vecs / (2 * ranks) >= kLpThreads) ranks *= 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(rows * ranks));
-  cfg.blockDim = dim3(kLpThreads);
-  cfg.stream = stream;
-  if (ranks == 1) return cudaLaunchKernelEx(&cfg, logprobs_kernel<T, false>, logits, a, 1);
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = ranks;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, logprobs_kernel<T, true>, logits, a, ranks);
+  while (ranks < kLpMaxRanks && rows * ranks < 2 * 152 && vecs / (2 * ranks) >= kLpTile / 2) ranks *= 2;
+  return ranks == 1 ? launch_kernel<T, false>(logits, a, rows, 1, stream)
+                    : launch_kernel<T, true>(logits, a, rows, ranks, stream);
 }
 
 }  // namespace tv
