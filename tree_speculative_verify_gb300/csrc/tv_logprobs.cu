@@ -9,10 +9,10 @@
 // row when there are few rows.
 //
 // The alternatives.  K distinct threads whose largest logits are >= t show that the K-th largest
-// logit is >= t, so a logit below t is no alternative.  In the pass a thread only notes its largest
-// logit, the tile that holds it, and the largest of its other tiles; at the end t is taken from
-// the threads' largest logits, the few threads at or above t look at that one tile again, and where
-// a second tile reaches t a warp looks at all of the thread's vectors.  The logits found, little
+// logit is >= t, so a logit below t is no alternative.  In the pass a thread only notes its two
+// largest tiles and the largest logit of its other tiles; at the end t is taken from the threads'
+// largest logits and the few tiles that reach t are looked at again, a vector per thread (all
+// vectors of a thread where a third tile reaches t).  The logits found, little
 // more than K, are ranked by counting: a key's place is the number of larger keys (a key is the
 // logit's order, then the lower id, so keys differ).  Rows of so many equal logits that the list
 // overflows take one scan per alternative instead.
@@ -29,15 +29,13 @@ using sm100::fma_f32x2;
 using sm100::pack_f32x2;
 using sm100::unpack_f32x2;
 
-constexpr int kLpThreads = 128;
-constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kLpUnroll = 4;                        // 16-byte vectors per thread and tile
-constexpr int kLpTile = kLpThreads * kLpUnroll;     // vectors per tile
-constexpr int kLpStages = 4;                        // tiles in flight
+constexpr int kLpStages = 3;                        // tiles in flight
 constexpr int kLpMaxTop = 32;
-constexpr int kLpCand = 1024;                       // candidate list
+constexpr int kLpCand = 512;                        // candidate list
 constexpr int kLpMaxRanks = 16;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
 
 struct LogprobArgs {
   int D, vocab, n_tok, n_top;
@@ -54,16 +52,19 @@ struct LogprobArgs {
   int32_t* status;
 };
 
-// Partial sums of a set of logits: their maximum (-inf: none above -inf yet), and S and T relative
-// to it.  A NaN or +inf logit makes S NaN.
+// Exponents are taken in base 2: with c = scale log2 e, a logit x contributes 2^{x c - m c}.  In the
+// pass that is one fused multiply-add with the rounded product b = fl(m c), and the sums are
+// relative to 2^b; the residual m c - b, at most 2^-24 |m c|, is taken out of ln S at the end.  Where
+// |m c| is so large that the residual is no longer small ("far": a largest logit beyond thousands)
+// the exponent is (x - m) c instead and the sums are relative to m itself.  Exponents below
+// kMinExp count as it: 2^-256 is 0 here, and -inf stays out of the products.
+constexpr float kMinExp = -256.f;
+constexpr float kFar = 1e4f;
+
+// Partial sums of a set of logits: their maximum m (-inf: none above -inf yet), S, and T = sum of
+// exponent * 2^exponent.  A NaN or +inf logit makes S NaN.
 struct Partial {
   float m, s, t;
-};
-
-// Exponent scale, and the difference below which e^{scale d} is taken as 0 (2^-256; it also keeps
-// -inf out of the products d e^{scale d}).
-struct ExpScale {
-  float c, dmin;
 };
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -76,27 +77,23 @@ __device__ __forceinline__ float max_nan(float a, float b) {   // NaN if either 
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
   return y;
 }
-__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
+__device__ __forceinline__ bool is_far(float m, float c) { return !(fabsf(m * c) < kFar); }
 
 // p relative to a maximum m >= p.m
-__device__ __forceinline__ void rebase(Partial& p, float m, ExpScale k) {
+__device__ __forceinline__ void rebase(Partial& p, float m, float c) {
   if (m > p.m) {
-    const float d = fmaxf(p.m - m, k.dmin);
-    const float f = exp2_approx(d * k.c);
-    p.t = (p.t + d * p.s) * f;
+    const float d = is_far(m, c) || is_far(p.m, c) ? (p.m - m) * c : p.m * c - m * c;
+    const float e = fmaxf(d, kMinExp), f = exp2_approx(e);
+    p.t = (p.t + e * p.s) * f;
     p.s *= f;
     p.m = m;
   }
 }
 
-__device__ __forceinline__ Partial join(Partial a, Partial b, ExpScale k) {
+__device__ __forceinline__ Partial join(Partial a, Partial b, float c) {
   const float m = fmaxf(a.m, b.m);
-  rebase(a, m, k);
-  rebase(b, m, k);
+  rebase(a, m, c);
+  rebase(b, m, c);
   return {m, a.s + b.s, a.t + b.t};
 }
 
@@ -126,25 +123,28 @@ struct Row {
     skew = (int)(((uintptr_t)row & 15u) / sizeof(T));
     n_vec = (skew + v + kVec - 1) / kVec;
   }
+  // vectors [first_whole, end_whole) lie inside the row
+  __device__ __forceinline__ int first_whole() const { return skew == 0 ? 0 : 1; }
+  __device__ __forceinline__ int end_whole() const { return (skew + vocab) / kVec; }
   __device__ __forceinline__ int id(int i, int j) const { return i * kVec - skew + j; }
   __device__ __forceinline__ uint4 whole(int i) const {
     return *reinterpret_cast<const uint4*>(p + (i * kVec - skew));
   }
-  // -inf where the vector reaches past the row or `hi`
-  __device__ __forceinline__ uint4 edge(int i, int hi) const {
+  // any vector; -inf where it reaches past the row
+  __device__ __forceinline__ uint4 load(int i) const {
+    if (i >= first_whole() && i < end_whole()) return whole(i);
     const int e0 = i * kVec - skew;
-    if (i < hi && e0 >= 0 && e0 + kVec <= vocab) return whole(i);
     uint32_t u[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       if constexpr (sizeof(T) == 2) {
         const int e = e0 + 2 * q;
-        const uint32_t lo = i < hi && e >= 0 && e < vocab ? bits(e) : 0xff80u;
-        const uint32_t up = i < hi && e + 1 >= 0 && e + 1 < vocab ? bits(e + 1) : 0xff80u;
+        const uint32_t lo = e >= 0 && e < vocab ? bits(e) : 0xff80u;
+        const uint32_t up = e + 1 >= 0 && e + 1 < vocab ? bits(e + 1) : 0xff80u;
         u[q] = lo | up << 16;
       } else {
         const int e = e0 + q;
-        u[q] = i < hi && e >= 0 && e < vocab ? bits(e) : 0xff800000u;
+        u[q] = e >= 0 && e < vocab ? bits(e) : 0xff800000u;
       }
     }
     return make_uint4(u[0], u[1], u[2], u[3]);
@@ -167,112 +167,121 @@ struct Row {
       }
     }
   }
-  // largest value (NaN ignored)
-  __device__ static __forceinline__ float largest(const uint4& w) {
+  // largest value of n vectors (NaN ignored)
+  template <int n>
+  __device__ static __forceinline__ float largest(const uint4 (&w)[n]) {
     if constexpr (sizeof(T) == 2) {
       auto h = [](uint32_t u) { return *reinterpret_cast<const __nv_bfloat162*>(&u); };
-      const __nv_bfloat162 m = __hmax2(__hmax2(h(w.x), h(w.y)), __hmax2(h(w.z), h(w.w)));
-      return fmaxf(__low2float(m), __high2float(m));
+      __nv_bfloat162 m[n];
+#pragma unroll
+      for (int k = 0; k < n; ++k)
+        m[k] = __hmax2(__hmax2(h(w[k].x), h(w[k].y)), __hmax2(h(w[k].z), h(w[k].w)));
+#pragma unroll
+      for (int k = 1; k < n; ++k) m[0] = __hmax2(m[0], m[k]);
+      return fmaxf(__low2float(m[0]), __high2float(m[0]));
     } else {
-      return fmaxf(fmaxf(__uint_as_float(w.x), __uint_as_float(w.y)),
-                   fmaxf(__uint_as_float(w.z), __uint_as_float(w.w)));
+      float m[n];
+#pragma unroll
+      for (int k = 0; k < n; ++k)
+        m[k] = fmaxf(sm100::max3f(__uint_as_float(w[k].x), __uint_as_float(w[k].y),
+                                  __uint_as_float(w[k].z)), __uint_as_float(w[k].w));
+#pragma unroll
+      for (int k = 1; k < n; ++k) m[0] = fmaxf(m[0], m[k]);
+      return m[0];
     }
   }
 };
 
 __device__ __forceinline__ uint64_t max_u64(uint64_t a, uint64_t b) { return a > b ? a : b; }
 
-// Shared memory of one CTA.  Of rank 0's, the other CTAs of the cluster write part and peer.
+// Shared memory of one CTA.  The lists of the end share the space of the tiles, which are done by
+// then: what a CTA takes decides how many rows run at once on an SM.
+template <int kThreads, bool kCluster>
 struct LpShared {
-  uint4 ring[kLpStages][kLpUnroll][kLpThreads];   // tiles in flight; a thread reads only its own
-  Partial warp_part[kLpWarps];
-  Partial part[kLpMaxRanks];       // the CTAs' shares of the row
+  static constexpr int kWarps = kThreads / 32;
+  struct Lists {
+    uint64_t cand[kLpCand];
+    int hit[2 * kThreads];         // tile * kThreads + thread: a thread's tile to look at again
+    uint16_t column[kThreads];     // threads with more than two of them
+  };
+  union {
+    uint4 ring[kLpStages][kLpUnroll][kThreads];   // tiles in flight; a thread reads only its own
+    Lists list;
+  };
+  Partial warp_part[kWarps];
   uint64_t top[kLpMaxTop];         // largest keys, descending (0: none)
-  uint32_t bound[kLpWarps][2];
-  int count, columns;
-  uint64_t scan[kLpWarps];
-  uint64_t cand[kLpCand];
-  uint64_t peer[kLpMaxRanks * kLpMaxTop];   // the CTAs' top lists
+  uint32_t largest[32];            // the warps' largest threads (kth_bound)
+  int count, hits, columns;
+  uint64_t scan[kWarps];
+  // rank 0's, written by the CTAs of the cluster: their shares of the row and their top lists
+  Partial part[kCluster ? kLpMaxRanks : 1];
+  uint64_t peer[kCluster ? kLpMaxRanks * kLpMaxTop : 1];
   uint64_t peer_bound;
-  uint8_t column[kLpThreads];      // threads with more than one tile to look at again
 };
 static_assert(kLpMaxRanks * kLpMaxTop <= kLpCand, "every CTA's keys fit into cand");
 
-// Lower bound (as an order) of the K-th largest logit that the CTA has seen, from the threads'
-// largest ones m: either K threads of one warp are at or above it, or ceil(K / warps) of every
-// warp.  The order of the lowest finite value where there are fewer.
-__device__ __forceinline__ uint32_t kth_bound(LpShared& sm, float m, int K) {
+// Lower bound (as an order) of the K-th largest logit that the CTA has seen: the K-th largest among
+// the 32 / warps (at most K) largest threads of every warp, m being a thread's largest logit.  The
+// order of the lowest finite value where those are fewer than K.
+template <int kThreads, bool kCluster>
+__device__ __forceinline__ uint32_t kth_bound(LpShared<kThreads, kCluster>& sm, float m, int K) {
+  constexpr int kWarps = kThreads / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int r = (K + kLpWarps - 1) / kLpWarps;
+  constexpr int per = 32 / kWarps;
   uint32_t o = order_of(m);
-  uint32_t kth = 0u, rth = 0u;
-  const int rounds = K <= kLpWarps ? K : r;
 #pragma unroll 1
-  for (int i = 1; i <= rounds; ++i) {
-    const uint32_t w = __reduce_max_sync(0xffffffffu, o);
-    if (i == r) rth = w;
-    if (i == K) kth = w;
-    const uint32_t at = __ballot_sync(0xffffffffu, o == w);
-    if (lane == __ffs(at) - 1) o = 0u;
-  }
-  if (lane == 0) {
-    sm.bound[warp][0] = kth;
-    sm.bound[warp][1] = rth;
-  }
-  __syncthreads();
-  uint32_t one = 0u, every = 0xffffffffu;
-#pragma unroll
-  for (int w = 0; w < kLpWarps; ++w) {
-    one = max(one, sm.bound[w][0]);
-    every = min(every, sm.bound[w][1]);
-  }
-  uint32_t t = max(one, every);
-  if (t < kOrderLowest && K > kLpWarps) {
-    // some warp has too few logits (a short or masked row): the K-th of one warp after all
-    o = order_of(m);
-#pragma unroll 1
-    for (int i = 1; i < K; ++i) {
-      const uint32_t w = __reduce_max_sync(0xffffffffu, o);
-      if (w < kOrderLowest) break;
+  for (int i = 0; i < per; ++i) {
+    uint32_t w = 0u;
+    if (i < K) {
+      w = __reduce_max_sync(0xffffffffu, o);
       const uint32_t at = __ballot_sync(0xffffffffu, o == w);
       if (lane == __ffs(at) - 1) o = 0u;
     }
-    o = __reduce_max_sync(0xffffffffu, o);
-    __syncthreads();
-    if (lane == 0) sm.bound[warp][0] = o;
-    __syncthreads();
+    if (lane == 0) sm.largest[i * kWarps + warp] = w;
+  }
+  __syncthreads();
+  const uint32_t v = sm.largest[lane];
+  uint32_t t;
+  if (K == 1) {
+    t = __reduce_max_sync(0xffffffffu, v);
+  } else {
+    int place = 0;
 #pragma unroll
-    for (int w = 0; w < kLpWarps; ++w) t = max(t, sm.bound[w][0]);
+    for (int j = 0; j < 32; ++j) {
+      const uint32_t x = __shfl_sync(0xffffffffu, v, j);
+      place += x > v || (x == v && j < lane) ? 1 : 0;
+    }
+    t = __reduce_max_sync(0xffffffffu, place == K - 1 ? v : 0u);
   }
   return max(t, kOrderLowest);
 }
 
-// Appends the logits of vector i that are >= bound to the candidate list.
-template <typename T>
-__device__ __forceinline__ void list_vector(LpShared& sm, const Row<T>& row, int i, int hi,
+// Appends the logits >= bound of vector i to the candidate list.
+template <typename T, int kThreads, bool kCluster>
+__device__ __forceinline__ void list_vector(LpShared<kThreads, kCluster>& sm, const Row<T>& row, int i,
                                             float bound) {
-  const uint4 q = row.edge(i, hi);
+  const uint4 q[1] = {row.load(i)};
   if (Row<T>::largest(q) < bound) return;
   float x[Row<T>::kVec];
-  Row<T>::unpack(q, x);
+  Row<T>::unpack(q[0], x);
 #pragma unroll
   for (int j = 0; j < Row<T>::kVec; ++j)
     if (x[j] >= bound) {
       const int at = atomicAdd(&sm.count, 1);
-      if (at < kLpCand) sm.cand[at] = key_of(x[j], row.id(i, j));
+      if (at < kLpCand) sm.list.cand[at] = key_of(x[j], row.id(i, j));
     }
 }
 
 // The CTA's K largest keys by one scan of its vectors [lo, hi) per key, into sm.top.
-template <typename T>
-__device__ __noinline__ void scan_top(LpShared& sm, const Row<T>& row, int lo, int hi, int K) {
+template <typename T, int kThreads, bool kCluster>
+__device__ __noinline__ void scan_top(LpShared<kThreads, kCluster>& sm, const Row<T>& row, int lo, int hi, int K) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint64_t last = ~0ull;
   for (int k = 0; k < K; ++k) {
     uint64_t best = 0ull;
-    for (int i = lo + threadIdx.x; i < hi; i += kLpThreads) {
+    for (int i = lo + threadIdx.x; i < hi; i += kThreads) {
       float x[Row<T>::kVec];
-      Row<T>::unpack(row.edge(i, hi), x);
+      Row<T>::unpack(row.load(i), x);
 #pragma unroll
       for (int j = 0; j < Row<T>::kVec; ++j) {
         const uint64_t key = key_of(x[j], row.id(i, j));
@@ -284,15 +293,16 @@ __device__ __noinline__ void scan_top(LpShared& sm, const Row<T>& row, int lo, i
     __syncthreads();
     if (lane == 0) sm.scan[warp] = best;
     __syncthreads();
-    for (int w = 0; w < kLpWarps; ++w) best = max_u64(best, sm.scan[w]);
+    for (int w = 0; w < kThreads / 32; ++w) best = max_u64(best, sm.scan[w]);
     if (threadIdx.x == 0) sm.top[k] = best;
     last = best;
   }
 }
 
 // Places of the n keys of `list` among each other: out[place] = key for the places below K.
+template <int kThreads>
 __device__ __noinline__ void rank_keys(const uint64_t* list, int n, int K, uint64_t* out) {
-  for (int i = threadIdx.x; i < n; i += kLpThreads) {
+  for (int i = threadIdx.x; i < n; i += kThreads) {
     const uint64_t key = list[i];
     int place = 0;
 #pragma unroll 8
@@ -305,11 +315,18 @@ __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
+__device__ __forceinline__ uint4 ld_shared_16(uint32_t src) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(src));
+  return v;
+}
+
 // Joins the partials held by the lanes of a warp (every lane gets the result).
 template <int kLanes>
-__device__ __forceinline__ Partial warp_join(Partial p, ExpScale k) {
+__device__ __forceinline__ Partial warp_join(Partial p, float c) {
   const uint32_t top = __reduce_max_sync(0xffffffffu, order_of(p.m));
-  rebase(p, logit_of_order(top), k);
+  rebase(p, logit_of_order(top), c);
 #pragma unroll
   for (int o = kLanes / 2; o > 0; o >>= 1) {
     p.s += __shfl_xor_sync(0xffffffffu, p.s, o);
@@ -318,53 +335,57 @@ __device__ __forceinline__ Partial warp_join(Partial p, ExpScale k) {
   return p;
 }
 
-template <typename T, bool kCluster>
-__global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const T* __restrict__ logits,
-                                                              const LogprobArgs a, int ranks) {
+template <typename T, int kThreads, bool kCluster>
+__global__ void __launch_bounds__(kThreads) logprobs_kernel(const T* __restrict__ logits,
+                                                            const LogprobArgs a, int ranks) {
+  constexpr int kWarps = kThreads / 32;
+  constexpr int kTile = kThreads * kLpUnroll;   // vectors per tile
   extern __shared__ __align__(16) unsigned char smem_raw[];
-  LpShared& sm = *reinterpret_cast<LpShared*>(smem_raw);
+  LpShared<kThreads, kCluster>& sm = *reinterpret_cast<LpShared<kThreads, kCluster>*>(smem_raw);
   const int rank = kCluster ? (int)cg::this_cluster().block_rank() : 0;
-  const int64_t r = kCluster ? blockIdx.x / ranks : blockIdx.x;
-  const int b = (int)(r / a.D), v = (int)(r - (int64_t)b * a.D);
+  const int r32 = kCluster ? blockIdx.x / ranks : blockIdx.x;   // rows: at most 2^21
+  const int b = r32 / a.D, v = r32 - b * a.D;
+  const int64_t r = r32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const Row<T> row(logits + r * a.ld, a.vocab);
   constexpr int kVec = Row<T>::kVec;
-  const ExpScale ks = {a.scale * kLog2e, -256.f / (a.scale * kLog2e)};
+  // (made to look different from thread to thread, so that it lives in an ordinary register: the
+  // packed instructions of the pass would fetch it from the uniform ones every time)
+  const float c = fmaf(__int2float_rn(tid), 0.f, a.scale * kLog2e);
   const int K = a.n_top > 1 ? a.n_top : 1;
-  // the CTA's vectors
+  // The CTA's vectors [lo, hi): its whole ones make `rows` rows of one vector per thread, which are
+  // streamed in tiles of kLpUnroll rows; what is left (less than a row, and the ends of the vocabulary)
+  // counts as two rows and a tile in front of them.
   const int per = kCluster ? (row.n_vec + ranks - 1) / ranks : row.n_vec;
   const int lo = min(row.n_vec, rank * per), hi = min(row.n_vec, lo + per);
+  const int whole_lo = max(lo, min(hi, row.first_whole()));
+  const int rows = max(0, min(hi, row.end_whole()) - whole_lo) / kThreads;
+  const int head = whole_lo - lo, rest = whole_lo + rows * kThreads;   // left over: [lo, whole_lo), [rest, hi)
+  // vector of row r (0, 1: left over) of a thread, -1: none
+  auto vector_of = [&](int r, int thread) {
+    if (r >= 2) return r - 2 < rows ? whole_lo + (r - 2) * kThreads + thread : -1;
+    const int j = r * kThreads + thread;
+    return j < head ? lo + j : rest + j - head < hi ? rest + j - head : -1;
+  };
+  const int tiles = (rows + kLpUnroll - 1) / kLpUnroll;
 
-  // a tile's copies: whole vectors asynchronously, the row's ends and what lies past hi at once
-  const T* src = row.p + ((lo + tid) * kVec - row.skew);
+  // a tile's copies into its stage
   const uint32_t ring = sm100::smem_u32(&sm.ring[0][0][tid]);
   constexpr uint32_t kStageBytes = sizeof(sm.ring[0]);
-  const int inner_hi = min(hi, row.n_vec - 1);
-  auto fetch = [&](int t) {
-    const int i0 = lo + t * kLpTile;
-    const uint32_t slot = ring + t % kLpStages * kStageBytes;
-    const T* at = src + (int64_t)t * (kLpTile * kVec);
-    if (i0 > 0 && i0 + kLpTile <= inner_hi) {
+  const T* next_src = row.p + ((whole_lo + tid) * kVec - row.skew);
+  int next_rows = rows;
+  uint32_t next_slot = ring;
+  auto fetch = [&] {
 #pragma unroll
-      for (int u = 0; u < kLpUnroll; ++u)
-        cp_async_16(slot + u * kLpThreads * 16, at + u * kLpThreads * kVec);
-    } else {
-#pragma unroll 1
-      for (int u = 0; u < kLpUnroll; ++u) {
-        const int i = i0 + u * kLpThreads + tid;
-        if (i > 0 && i < inner_hi)
-          cp_async_16(slot + u * kLpThreads * 16, at + u * kLpThreads * kVec);
-        else
-          sm.ring[t % kLpStages][u][tid] = row.edge(i, hi);
-      }
-    }
-  };
-  const int tiles = (hi - lo + kLpTile - 1) / kLpTile;
-#pragma unroll 1
-  for (int t = 0; t < kLpStages - 1; ++t) {
-    if (t < tiles) fetch(t);
+    for (int u = 0; u < kLpUnroll; ++u)
+      if (u < next_rows) cp_async_16(next_slot + u * kThreads * 16, next_src + u * kThreads * kVec);
     asm volatile("cp.async.commit_group;" ::: "memory");
-  }
+    next_rows -= kLpUnroll;
+    next_src += kTile * kVec;
+    next_slot = next_slot == ring + (kLpStages - 1) * kStageBytes ? ring : next_slot + kStageBytes;
+  };
+#pragma unroll 1
+  for (int t = 0; t < kLpStages - 1; ++t) fetch();
   if constexpr (kCluster) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   // the first given tokens of this row, so that their logits arrive under the others
   const bool first = rank == 0 && tid < a.n_tok;
@@ -376,109 +397,144 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const T* __restric
     given_tok = a.tokens[at];
     if (given_node == v && given_tok >= 0 && given_tok < a.vocab) given = load_f(row.p + given_tok);
   }
-  if (tid == 0) sm.count = sm.columns = 0;
+  if (tid == 0) sm.count = sm.hits = sm.columns = 0;
   if (tid < K) sm.top[tid] = 0ull;
 
+  const uint64_t c2 = pack_f32x2(c, c);
   Partial p = {-INFINITY, 0.f, 0.f};
-  float second = -INFINITY;   // largest logit outside the tile of the largest
-  int at_tile = 0;
-#pragma unroll 1
-  for (int t = 0; t < tiles; ++t) {
-    if (t + kLpStages - 1 < tiles) fetch(t + kLpStages - 1);
-    asm volatile("cp.async.commit_group;" ::: "memory");
-    asm volatile("cp.async.wait_group %0;" ::"n"(kLpStages - 1) : "memory");
-    const uint4(*tile)[kLpThreads] = sm.ring[t % kLpStages];
-    uint4 w[kLpUnroll];
-    float m = -INFINITY;
-#pragma unroll
-    for (int u = 0; u < kLpUnroll; ++u) {
-      w[u] = tile[u][tid];
-      m = fmaxf(m, Row<T>::largest(w[u]));
+  // largest logits of the three largest tiles (the first: p.m), and which the first two are
+  float second = -INFINITY, third = -INFINITY;
+  int tile1 = 0, tile2 = 0;
+  auto note_tile = [&](float m, int t) {
+    third = fmaxf(third, fminf(second, m));
+    if (m > second) {
+      tile2 = m > p.m ? tile1 : t;
+      second = fminf(p.m, m);
     }
     if (m > p.m) {
-      second = p.m;
-      at_tile = t;
-      rebase(p, m, ks);
-    } else {
-      second = fmaxf(second, m);
+      tile1 = t;
+      rebase(p, m, c);
     }
-    const float base = p.m == -INFINITY ? 0.f : p.m;
-    const uint64_t neg = pack_f32x2(-base, -base), c2 = pack_f32x2(ks.c, ks.c);
+  };
+  // adds a vector's logits to the sums, exponents bounded: any logits, any maximum
+  auto add_vector = [&](const uint4& w, float& s, float& t) {
+    const bool far = is_far(p.m, c);
+    const float base = p.m == -INFINITY ? 0.f : p.m, shift = -(p.m * c);
+    float x[kVec];
+    Row<T>::unpack(w, x);
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) {
+      const float y = max_nan(far ? (x[j] - base) * c : fmaf(x[j], c, shift), kMinExp);
+      const float e = exp2_approx(y);
+      s += e;
+      t += y * e;
+    }
+  };
+  {
+    const int i0 = vector_of(0, tid), i1 = vector_of(1, tid);
+    if (i0 >= 0) {
+      const uint4 w[2] = {row.load(i0), row.load(i1 >= 0 ? i1 : i0)};
+      note_tile(Row<T>::largest(w), 0);
+      add_vector(w[0], p.s, p.t);
+      if (i1 >= 0) add_vector(w[1], p.s, p.t);
+    }
+  }
+  uint32_t slot = ring;
+  int left = rows;
+#pragma unroll 1
+  for (int t = 1; t <= tiles; ++t, left -= kLpUnroll) {
+    fetch();
+    asm volatile("cp.async.wait_group %0;" ::"n"(kLpStages - 1) : "memory");
+    uint4 w[kLpUnroll];
+#pragma unroll
+    for (int u = 0; u < kLpUnroll; ++u)   // (a row that is not there: the first one again, not added)
+      w[u] = ld_shared_16(slot + (u < left ? u : 0) * kThreads * 16);
+    note_tile(Row<T>::largest(w), t);
+    const float shift = -(p.m * c);
+    const uint64_t shift2 = pack_f32x2(shift, shift);
     uint64_t s2 = pack_f32x2(0.f, 0.f), t2 = s2;
 #pragma unroll
     for (int u = 0; u < kLpUnroll; ++u) {
+      if (u >= left) break;
       float x[kVec];
       Row<T>::unpack(w[u], x);
 #pragma unroll
       for (int j = 0; j < kVec; j += 2) {
-        const uint64_t d = add_f32x2(pack_f32x2(x[j], x[j + 1]), neg);
+        const uint64_t y = fma_f32x2(pack_f32x2(x[j], x[j + 1]), c2, shift2);
         float y0, y1;
-        unpack_f32x2(mul_f32x2(d, c2), y0, y1);
+        unpack_f32x2(y, y0, y1);
         const uint64_t e = pack_f32x2(exp2_approx(y0), exp2_approx(y1));
         s2 = add_f32x2(s2, e);
-        t2 = fma_f32x2(d, e, t2);
+        t2 = fma_f32x2(y, e, t2);
       }
     }
-    float s0, s1, t0, t1;
-    unpack_f32x2(s2, s0, s1);
-    unpack_f32x2(t2, t0, t1);
-    p.s += s0 + s1;
-    float dt = t0 + t1;
-    if (!(dt == dt)) {   // a masked logit: -inf times 0; the differences are bounded below instead
-      dt = 0.f;
+    float ds, dt, s1, t1;
+    unpack_f32x2(s2, ds, s1);
+    unpack_f32x2(t2, dt, t1);
+    ds += s1;
+    dt += t1;
+    if (!(dt == dt) || is_far(p.m, c)) {
+      // a masked logit (-inf times 0) or far exponents: the same sums with bounded exponents
+      ds = dt = 0.f;
 #pragma unroll 1
-      for (int u = 0; u < kLpUnroll; ++u) {
-        float x[kVec];
-        Row<T>::unpack(tile[u][tid], x);
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) {
-          const float d = max_nan(x[j] - base, ks.dmin);
-          dt += d * exp2_approx(d * ks.c);
-        }
-      }
+      for (int u = 0; u < min(left, kLpUnroll); ++u)
+        add_vector(ld_shared_16(slot + u * kThreads * 16), ds, dt);
     }
+    p.s += ds;
     p.t += dt;
+    slot = slot == ring + (kLpStages - 1) * kStageBytes ? ring : slot + kStageBytes;
   }
   // the CTA's sums
   const float largest = p.m;
-  p = warp_join<32>(p, ks);
+  p = warp_join<32>(p, c);
   if (lane == 0) sm.warp_part[warp] = p;
   const float bound = logit_of_order(kth_bound(sm, largest, K));   // (its barrier: warp_part)
-  p = warp_join<kLpWarps>(sm.warp_part[lane % kLpWarps], ks);
-  if (second >= bound) {
-    sm.column[atomicAdd(&sm.columns, 1)] = (uint8_t)tid;
+  p = warp_join<kWarps>(sm.warp_part[lane % kWarps], c);
+  if (third >= bound) {
+    sm.list.column[atomicAdd(&sm.columns, 1)] = (uint16_t)tid;
   } else if (largest >= bound) {
-#pragma unroll 1
-    for (int u = 0; u < kLpUnroll; ++u)
-      list_vector(sm, row, lo + at_tile * kLpTile + u * kLpThreads + tid, hi, bound);
+    const int two = second >= bound ? 1 : 0, at = atomicAdd(&sm.hits, 1 + two);
+    sm.list.hit[at] = tile1 * kThreads + tid;
+    if (two) sm.list.hit[at + 1] = tile2 * kThreads + tid;
   }
   __syncthreads();
-  const int columns = sm.columns;
+  const int looks = sm.hits * kLpUnroll, columns = sm.columns;
 #pragma unroll 1
-  for (int k = warp; k < columns; k += kLpWarps) {
-    if (*(volatile int*)&sm.count > kLpCand) break;   // too many equal logits
-    for (int i = lo + sm.column[k] + lane * kLpThreads; i < hi; i += 32 * kLpThreads)
-      list_vector(sm, row, i, hi, bound);
+  for (int k = tid; k < looks + columns * kThreads; k += kThreads) {
+    // a row of a tile, or (whole CTA) the rows of a thread
+    if (k < looks) {
+      const int hit = sm.list.hit[k / kLpUnroll], u = k % kLpUnroll, tile = hit / kThreads;
+      const int r = tile == 0 ? u : 2 + (tile - 1) * kLpUnroll + u;
+      const int i = tile == 0 && u >= 2 ? -1 : vector_of(r, hit % kThreads);
+      if (i >= 0) list_vector(sm, row, i, bound);
+    } else {
+      if (*(volatile int*)&sm.count > kLpCand) break;   // too many equal logits
+      const int q = k - looks, thread = sm.list.column[q / kThreads];
+      for (int r = q % kThreads; r < rows + 2; r += kThreads) {
+        const int i = vector_of(r, thread);
+        if (i >= 0) list_vector(sm, row, i, bound);
+      }
+    }
   }
   __syncthreads();
   const int n = sm.count;
   if (n > kLpCand)
     scan_top(sm, row, lo, hi, K);
   else
-    rank_keys(sm.cand, n, K, sm.top);
+    rank_keys<kThreads>(sm.list.cand, n, K, sm.top);
   __syncthreads();
   if constexpr (kCluster) {
     // every CTA leaves its sums and keys in rank 0's shared memory, which joins them
     auto cluster = cg::this_cluster();
     asm volatile("barrier.cluster.wait.aligned;" ::: "memory");   // rank 0 has started
-    LpShared* to = cluster.map_shared_rank(&sm, 0);
+    LpShared<kThreads, kCluster>* to = cluster.map_shared_rank(&sm, 0);
     if (tid == 0) to->part[rank] = p;
     if (tid < K) to->peer[rank * K + tid] = sm.top[tid];
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     if (rank != 0) return;
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     const Partial q = {-INFINITY, 0.f, 0.f};
-    p = warp_join<kLpMaxRanks>(lane % kLpMaxRanks < ranks ? sm.part[lane % kLpMaxRanks] : q, ks);
+    p = warp_join<kLpMaxRanks>(lane % kLpMaxRanks < ranks ? sm.part[lane % kLpMaxRanks] : q, c);
     // the K-th largest of all keys is at least any CTA's K-th, and at least the least of the CTAs'
     // ceil(K / ranks)-th
     if (warp == 0) {
@@ -500,19 +556,21 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const T* __restric
     __syncthreads();
     if (tid < K) sm.top[tid] = 0ull;
     const uint64_t least = sm.peer_bound;
-    for (int i = tid; i < ranks * K; i += kLpThreads) {
+    for (int i = tid; i < ranks * K; i += kThreads) {
       const uint64_t key = sm.peer[i];
-      if (key != 0ull && key >= least) sm.cand[atomicAdd(&sm.count, 1)] = key;
+      if (key != 0ull && key >= least) sm.list.cand[atomicAdd(&sm.count, 1)] = key;
     }
     __syncthreads();
-    rank_keys(sm.cand, sm.count, K, sm.top);
+    rank_keys<kThreads>(sm.list.cand, sm.count, K, sm.top);
     __syncthreads();
   }
 
   const bool bad = !(p.s == p.s) || p.m == INFINITY;   // a NaN or +inf among the logits
   const bool none = !bad && p.m == -INFINITY;
   const float nan = __int_as_float(0x7fffffff);
-  const float log_s = logf(p.s);   // -inf for an empty row
+  // ln S relative to m: the rounding of m c taken out (-inf for an empty row)
+  const float residual = is_far(p.m, c) ? 0.f : fmaf(p.m, c, -(p.m * c));
+  const float ln_s = logf(p.s), log_s = ln_s - residual * kLn2;
   auto log_prob = [&](float x) {
     return bad ? nan : x == -INFINITY ? x : (x - p.m) * a.scale - log_s;
   };
@@ -520,7 +578,7 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const T* __restric
     if (bad) record_error(a.status, TV_ERR_VALUE);
     if (a.lse) a.lse[r] = bad ? nan : none ? -INFINITY : p.m * a.scale + log_s;
     if (a.entropy)
-      a.entropy[r] = bad ? nan : none ? 0.f : fmaxf(log_s - a.scale * (p.t / p.s), 0.f);
+      a.entropy[r] = bad ? nan : none ? 0.f : fmaxf(ln_s - kLn2 * (p.t / p.s), 0.f);
   }
   if (tid < K) {
     const uint64_t key = bad ? 0ull : sm.top[tid];
@@ -533,7 +591,7 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const T* __restric
     }
   }
   // given tokens: this row takes those of its node, and row 0 those without a node or a token
-  for (int i = tid; i < a.n_tok; i += kLpThreads) {
+  for (int i = tid; i < a.n_tok; i += kThreads) {
     const int64_t at = (int64_t)b * a.n_tok + i;
     const bool early = i == tid && first;
     const int node = early ? given_node : a.nodes ? a.nodes[at] : i;
@@ -550,18 +608,18 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const T* __restric
   }
 }
 
-template <typename T, bool kCluster>
+template <typename T, int kThreads, bool kCluster>
 static cudaError_t launch_kernel(const T* logits, const LogprobArgs& a, int64_t rows, int ranks,
                                  cudaStream_t stream) {
-  auto kernel = logprobs_kernel<T, kCluster>;
-  const int smem = (int)sizeof(LpShared);
+  auto kernel = logprobs_kernel<T, kThreads, kCluster>;
+  const int smem = (int)sizeof(LpShared<kThreads, kCluster>);
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e == cudaSuccess && ranks > 8)
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(rows * ranks));
-  cfg.blockDim = dim3(kLpThreads);
+  cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -576,12 +634,18 @@ static cudaError_t launch_kernel(const T* logits, const LogprobArgs& a, int64_t 
 template <typename T>
 static cudaError_t launch_logprobs(const T* logits, const LogprobArgs& a, int64_t rows,
                                    cudaStream_t stream) {
-  // CTAs per row: enough for two per SM, each with a tile's worth of vectors
   const int64_t vecs = (int64_t)a.vocab * sizeof(T) / 16;
+  // a cluster per row while all CTAs of all rows have an SM of their own (two rows' worth of clusters
+  // per SM already cost more than they give: 120 rows of 50001 bf16 logits take 8.1 us as one CTA
+  // each, 9.6 us as two), each with at least a row of vectors
   int ranks = 1;
-  while (ranks < kLpMaxRanks && rows * ranks < 2 * 152 && vecs / (2 * ranks) >= kLpTile / 2) ranks *= 2;
-  return ranks == 1 ? launch_kernel<T, false>(logits, a, rows, 1, stream)
-                    : launch_kernel<T, true>(logits, a, rows, ranks, stream);
+  while (ranks < kLpMaxRanks && rows * ranks * 2 <= 152 && vecs / (2 * ranks) >= 256) ranks *= 2;
+  if (ranks > 1) return launch_kernel<T, 256, true>(logits, a, rows, ranks, stream);
+  // many rows fill the SMs with small CTAs, whose ends cost less (512 rows of 2048 bf16 logits: 6.1
+  // us with 128 threads, 7.3 us with 256); fewer rows want more loads in flight per row (256 rows of
+  // 128000 fp32 logits: 31.5 and 25.3 us)
+  return rows >= 512 ? launch_kernel<T, 128, false>(logits, a, rows, 1, stream)
+                     : launch_kernel<T, 256, false>(logits, a, rows, 1, stream);
 }
 
 }  // namespace tv
