@@ -27,6 +27,7 @@ TV_TAIL_WINDOW, TV_TAIL_REMAINDER = 0, 1
 TV_COMP_C4, TV_COMP_C128 = 1, 2
 TV_F32, TV_BF16 = 0, 1
 TV_ATTN_AUTO, TV_ATTN_SIMT, TV_ATTN_TCGEN05 = 0, 1, 2
+_LOGIT_TYPES = {torch.float32: TV_F32, torch.bfloat16: TV_BF16}
 
 EXPORTS = (
     "tv_version", "tv_status_string", "tv_last_error_string", "tv_workspace_size",
@@ -246,30 +247,44 @@ def tv_indexer_topk(shape, d_idx, q_idx, k_idx, L, sel, workspace, status, strea
     _check("tv_indexer_topk", rc)
 
 
-# The calls below check their tensors' types and sizes, and pass plain integers: their kernels are
-# short, so the binding's own time counts.
-def _a(t, dtype, numel, name):
-    """Device address of a contiguous tensor of the given type with at least numel elements on the
-    current device (None: a null pointer)."""
-    if t is None:
+# The calls below check their tensors' types, sizes and device, and pass plain integers: their kernels
+# are short, so the binding's own time counts (a tensor takes 0.35 us, the current stream's handle
+# 0.1 us against 2.9 us through a torch.cuda.Stream).
+def _here():
+    """The current device's index (None without a CUDA device: every tensor is then refused)."""
+    try:
+        return torch.cuda.current_device()
+    except (RuntimeError, AssertionError):
         return None
+
+
+def _refuse(t, dtype, numel, name, dev):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor or None")
     if not t.is_cuda:
         raise ValueError(f"{name}: tensor arguments must live on the CUDA device")
-    if t.get_device() != torch.cuda.current_device():
+    if t.get_device() != dev:
         raise ValueError(f"{name}: the tensor lives on another device than the current one")
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: tensor arguments must be contiguous")
-    if t.numel() < numel:
-        raise ValueError(f"{name}: {t.numel()} elements, {numel} needed")
+    raise ValueError(f"{name}: {t.numel()} elements, {numel} needed")
+
+
+def _a(t, dtype, numel, name, dev):
+    """Device address of a contiguous tensor of the given type with at least numel elements on
+    device dev (None: a null pointer)."""
+    if t is None:
+        return None
+    if (not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype is not dtype
+            or not t.is_contiguous() or t.numel() < numel):
+        _refuse(t, dtype, numel, name, dev)
     return t.data_ptr()
 
 
-def _s(stream):
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+def _s(stream, dev):
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def tv_token_logprobs(shape, logits, tokens, nodes, scale, lse, entropy, logprobs, top_ids,
@@ -277,31 +292,29 @@ def tv_token_logprobs(shape, logits, tokens, nodes, scale, lse, entropy, logprob
     """``logits``: [B][D][vocab] fp32 or bf16 with unit last stride; the rows may lie further apart
     than the vocabulary (a slice of a padded buffer).  ``tokens``, ``nodes`` and ``logprobs``: [B][n_tok]
     or None; ``top_ids`` and ``top_logprobs``: [B][D][n_top] or None."""
-    B, D = shape.B, shape.D
+    lib, dev, B, D = _lib or load(), _here(), shape.B, shape.D
     if logits.dim() != 3 or logits.shape[0] != B or logits.shape[1] != D:
         raise ValueError(f"logits: expected [{B}][{D}][vocab], got {tuple(logits.shape)}")
-    if not logits.is_cuda or logits.get_device() != torch.cuda.current_device():
+    if not logits.is_cuda or logits.get_device() != dev:
         raise ValueError("logits: the tensor must live on the current CUDA device")
-    dtype = {torch.float32: TV_F32, torch.bfloat16: TV_BF16}.get(logits.dtype)
+    dtype = _LOGIT_TYPES.get(logits.dtype)
     if dtype is None:
         raise TypeError(f"logits: expected float32 or bfloat16, got {logits.dtype}")
     vocab, (sB, ld, unit) = logits.shape[2], logits.stride()
     if D == 1:
         ld = sB if B > 1 else vocab
-    if B * D == 1:
-        ld = vocab
     if (unit != 1 and vocab > 1) or ld < vocab or (B > 1 and sB != D * ld):
         raise ValueError(f"logits: rows must be contiguous and evenly spaced, strides {logits.stride()}")
     n_tok = 0 if tokens is None else tokens.shape[-1]
     n_top = 0 if top_ids is None else top_ids.shape[-1]
-    rows, i32, f32 = B * D, torch.int32, torch.float32
-    rc = load().tv_token_logprobs(
+    rows, given, i32, f32 = B * D, B * n_tok, torch.int32, torch.float32
+    rc = lib.tv_token_logprobs(
         ctypes.byref(shape), vocab, ld, dtype, logits.data_ptr(), n_tok,
-        _a(tokens, i32, B * n_tok, "tokens"), _a(nodes, i32, B * n_tok, "nodes"), scale, n_top,
-        _a(lse, f32, rows, "lse"), _a(entropy, f32, rows, "entropy"),
-        _a(logprobs, f32, B * n_tok, "logprobs"), _a(top_ids, i32, rows * n_top, "top_ids"),
-        _a(top_logprobs, f32, rows * n_top, "top_logprobs"), _a(target, i32, rows, "target"),
-        _a(status, i32, 1, "status"), _s(stream))
+        _a(tokens, i32, given, "tokens", dev), _a(nodes, i32, given, "nodes", dev), scale, n_top,
+        _a(lse, f32, rows, "lse", dev), _a(entropy, f32, rows, "entropy", dev),
+        _a(logprobs, f32, given, "logprobs", dev), _a(top_ids, i32, rows * n_top, "top_ids", dev),
+        _a(top_logprobs, f32, rows * n_top, "top_logprobs", dev), _a(target, i32, rows, "target", dev),
+        _a(status, i32, 1, "status", dev), _s(stream, dev))
     if rc:
         _check("tv_token_logprobs", rc)
 
@@ -310,59 +323,57 @@ def tv_pages_workspace_size(shape):
     return int(load().tv_pages_workspace_size(ctypes.byref(shape)))
 
 
-def _pools(shape, rawK, rawV, c4K, c4V, c128K, c128V):
+def _pools(shape, rawK, rawV, c4K, c4V, c128K, c128V, dev):
     dt = torch.bfloat16 if shape.dtype == TV_BF16 else torch.float32
-    n = shape.n_pool_pages * shape.page_tokens * shape.d
-    n4 = n // 4 if shape.comp_mask & TV_COMP_C4 else 0
-    n128 = n // 128 if shape.comp_mask & TV_COMP_C128 else 0
-    return (_a(rawK, dt, n, "rawK"), _a(rawV, dt, n, "rawV"), _a(c4K, dt, n4, "c4K"),
-            _a(c4V, dt, n4, "c4V"), _a(c128K, dt, n128, "c128K"), _a(c128V, dt, n128, "c128V"))
+    mask, n = shape.comp_mask, shape.n_pool_pages * shape.page_tokens * shape.d
+    n4, n128 = n // 4 if mask & TV_COMP_C4 else 0, n // 128 if mask & TV_COMP_C128 else 0
+    return (_a(rawK, dt, n, "rawK", dev), _a(rawV, dt, n, "rawV", dev), _a(c4K, dt, n4, "c4K", dev),
+            _a(c4V, dt, n4, "c4V", dev), _a(c128K, dt, n128, "c128K", dev),
+            _a(c128V, dt, n128, "c128V", dev))
 
 
-def _workspace(workspace):
-    if workspace is None:
-        return None, 0
-    return (_a(workspace, workspace.dtype, 0, "workspace"),
-            workspace.numel() * workspace.element_size())
+def _pages(shape, L, page_refs, workspace, dev):
+    """Addresses of what all tv_pages_* calls take, and the workspace's size."""
+    i32 = torch.int32
+    ws = None if workspace is None else _a(workspace, workspace.dtype, 0, "workspace", dev)
+    ws_bytes = 0 if ws is None else workspace.numel() * workspace.element_size()
+    return (_a(L, i32, shape.B, "L", dev), _a(page_refs, i32, shape.n_pool_pages, "page_refs", dev),
+            ws, ws_bytes)
 
 
 def tv_pages_fork(shape, source, keep, L, page_refs, rawK, rawV, c4K, c4V, c128K, c128V, k_idx,
                   workspace, status, stream=None):
     """``k_idx``: [B][c4_cap][d_idx] bf16 indexer keys, or None."""
-    B, i32 = shape.B, torch.int32
+    lib, dev, B, i32 = _lib or load(), _here(), shape.B, torch.int32
     d_idx = 0 if k_idx is None else k_idx.shape[-1]
-    ws, ws_bytes = _workspace(workspace)
-    rc = load().tv_pages_fork(
-        ctypes.byref(shape), _a(source, i32, B, "source"), _a(keep, i32, B, "keep"),
-        _a(L, i32, B, "L"), _a(page_refs, i32, shape.n_pool_pages, "page_refs"),
-        *_pools(shape, rawK, rawV, c4K, c4V, c128K, c128V),
-        _a(k_idx, torch.bfloat16, B * shape.c4_cap * d_idx, "k_idx"), d_idx, ws, ws_bytes,
-        _a(status, i32, 1, "status"), _s(stream))
+    L, page_refs, ws, ws_bytes = _pages(shape, L, page_refs, workspace, dev)
+    rc = lib.tv_pages_fork(
+        ctypes.byref(shape), _a(source, i32, B, "source", dev), _a(keep, i32, B, "keep", dev), L,
+        page_refs, *_pools(shape, rawK, rawV, c4K, c4V, c128K, c128V, dev),
+        _a(k_idx, torch.bfloat16, B * shape.c4_cap * d_idx, "k_idx", dev), d_idx, ws, ws_bytes,
+        _a(status, i32, 1, "status", dev), _s(stream, dev))
     if rc:
         _check("tv_pages_fork", rc)
 
 
 def tv_pages_reserve(shape, need, L, page_refs, workspace, status, stream=None):
-    B, i32 = shape.B, torch.int32
-    ws, ws_bytes = _workspace(workspace)
-    rc = load().tv_pages_reserve(
-        ctypes.byref(shape), _a(need, i32, B, "need"), _a(L, i32, B, "L"),
-        _a(page_refs, i32, shape.n_pool_pages, "page_refs"), ws, ws_bytes,
-        _a(status, i32, 1, "status"), _s(stream))
+    lib, dev, i32 = _lib or load(), _here(), torch.int32
+    L, page_refs, ws, ws_bytes = _pages(shape, L, page_refs, workspace, dev)
+    rc = lib.tv_pages_reserve(
+        ctypes.byref(shape), _a(need, i32, shape.B, "need", dev), L, page_refs, ws, ws_bytes,
+        _a(status, i32, 1, "status", dev), _s(stream, dev))
     if rc:
         _check("tv_pages_reserve", rc)
 
 
 def tv_pages_compact(shape, L, page_refs, rawK, rawV, c4K, c4V, c128K, c128V, remap, n_live,
                      workspace, status, stream=None):
-    B, i32 = shape.B, torch.int32
-    ws, ws_bytes = _workspace(workspace)
-    rc = load().tv_pages_compact(
-        ctypes.byref(shape), _a(L, i32, B, "L"),
-        _a(page_refs, i32, shape.n_pool_pages, "page_refs"),
-        *_pools(shape, rawK, rawV, c4K, c4V, c128K, c128V),
-        _a(remap, i32, shape.n_pool_pages, "remap"), _a(n_live, i32, 1, "n_live"), ws, ws_bytes,
-        _a(status, i32, 1, "status"), _s(stream))
+    lib, dev, i32 = _lib or load(), _here(), torch.int32
+    L, page_refs, ws, ws_bytes = _pages(shape, L, page_refs, workspace, dev)
+    rc = lib.tv_pages_compact(
+        ctypes.byref(shape), L, page_refs, *_pools(shape, rawK, rawV, c4K, c4V, c128K, c128V, dev),
+        _a(remap, i32, shape.n_pool_pages, "remap", dev), _a(n_live, i32, 1, "n_live", dev), ws,
+        ws_bytes, _a(status, i32, 1, "status", dev), _s(stream, dev))
     if rc:
         _check("tv_pages_compact", rc)
 

@@ -613,7 +613,9 @@ static cudaError_t launch_kernel(const T* logits, const LogprobArgs& a, int64_t 
                                  cudaStream_t stream) {
   auto kernel = logprobs_kernel<T, kThreads, kCluster>;
   const int smem = (int)sizeof(LpShared<kThreads, kCluster>);
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = cudaSuccess;
+  if (smem > 48 * 1024)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e == cudaSuccess && ranks > 8)
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
@@ -635,11 +637,12 @@ template <typename T>
 static cudaError_t launch_logprobs(const T* logits, const LogprobArgs& a, int64_t rows,
                                    cudaStream_t stream) {
   const int64_t vecs = (int64_t)a.vocab * sizeof(T) / 16;
-  // a cluster per row while all CTAs of all rows have an SM of their own (two rows' worth of clusters
-  // per SM already cost more than they give: 120 rows of 50001 bf16 logits take 8.1 us as one CTA
-  // each, 9.6 us as two), each with at least a row of vectors
+  // Long rows are shared by a cluster while little more than the SMs are taken: 6 rows of 200000 fp32
+  // logits 20.8 us as one CTA each, 10.2 us over 16; 48 rows 23.5 and 16.5 us (over 4); but 120 rows
+  // of 50001 bf16 logits 8.1 us, 9.6 us over 2.  Shorter shares than 2500 vectors do not pay for the
+  // cluster's barriers: 8 rows of 32000 bf16 logits 6.8 us, 7.5 us over 2.
   int ranks = 1;
-  while (ranks < kLpMaxRanks && rows * ranks * 2 <= 152 && vecs / (2 * ranks) >= 256) ranks *= 2;
+  while (ranks < kLpMaxRanks && rows * ranks * 2 <= 200 && vecs / (2 * ranks) >= 2500) ranks *= 2;
   if (ranks > 1) return launch_kernel<T, 256, true>(logits, a, rows, ranks, stream);
   // many rows fill the SMs with small CTAs, whose ends cost less (512 rows of 2048 bf16 logits: 6.1
   // us with 128 threads, 7.3 us with 256); fewer rows want more loads in flight per row (256 rows of
