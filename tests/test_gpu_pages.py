@@ -167,10 +167,11 @@ def test_reserve_windows():
     s.check([s.reserve([8] * 7)])
 
 
-@pytest.mark.parametrize("n_pool,B,G", [(3, 1, 2), (40, 6, 5), (700, 50, 8), (5000, 300, 6)])
+@pytest.mark.parametrize("n_pool,B,G", [(3, 1, 2), (40, 6, 5), (700, 50, 8), (5000, 300, 6), (8193, 300, 6),
+                                        (700, 50, 800)])
 def test_compact_moves_the_upper_live_pages(n_pool, B, G):
     P, rng = 512, np.random.default_rng(n_pool)
-    L = [int(x) for x in rng.integers(0, G * P + 1, size=B)]
+    L = [int(x) for x in rng.integers(0, min(G, 8) * P + 1, size=B)]
     while sum(-(-n // P) for n in L) > 0.8 * n_pool:
         L[int(np.argmax(L))] = int(rng.integers(0, 2 * P))
     table = _random_table(rng, B, G, n_pool, L, P)
@@ -197,10 +198,13 @@ def test_compact_reports_an_inconsistent_table():
     s.check([-1])
 
 
-@pytest.mark.parametrize("seed", range(4))
-def test_random_histories(seed):
+@pytest.mark.parametrize("seed,wide", [(0, 0), (1, 0), (2, 0), (3, 0), (4, 1), (5, 1)])
+def test_random_histories(seed, wide):
+    # (wide: a table of more entries than one CTA plans, so that the cluster does)
     rng = np.random.default_rng(seed)
     B, G, P, n = int(rng.integers(3, 40)), int(rng.integers(2, 7)), 512, 90
+    if wide:
+        G = 40000 // B
     s = Pool([[-1] * G for _ in range(B)], [0] * B, n, P, keys=16, seed=seed)
     for _ in range(25):
         op, codes = int(rng.integers(4)), []
@@ -214,7 +218,7 @@ def test_random_histories(seed):
             s.L.copy_(torch.tensor(s.o["L"], dtype=torch.int32))
         elif op == 2:
             src = [int(x) if rng.random() < 0.4 else b for b, x in enumerate(rng.integers(-1, B, size=B))]
-            keep = [int(x) for x in rng.integers(-900, G * P, size=B)] if rng.random() < 0.5 else None
+            keep = [int(x) for x in rng.integers(-900, min(G, 7) * P, size=B)] if rng.random() < 0.5 else None
             codes.append(s.fork(src, keep))
         else:
             codes.append(s.compact())

@@ -336,12 +336,13 @@ __device__ __forceinline__ Partial warp_join(Partial p, float c) {
 }
 
 template <typename T, int kThreads, bool kCluster>
-__global__ void __launch_bounds__(kThreads) logprobs_kernel(const T* __restrict__ logits,
+__global__ void __launch_bounds__(kThreads) logprobs_kernel(const T* logits,
                                                             const LogprobArgs a, int ranks) {
   constexpr int kWarps = kThreads / 32;
   constexpr int kTile = kThreads * kLpUnroll;   // vectors per tile
   extern __shared__ __align__(16) unsigned char smem_raw[];
   LpShared<kThreads, kCluster>& sm = *reinterpret_cast<LpShared<kThreads, kCluster>*>(smem_raw);
+  pdl_wait();   // nothing is read before the kernel in front has completed
   const int rank = kCluster ? (int)cg::this_cluster().block_rank() : 0;
   const int r32 = kCluster ? blockIdx.x / ranks : blockIdx.x;   // rows: at most 2^21
   const int b = r32 / a.D, v = r32 - b * a.D;
@@ -624,12 +625,14 @@ static cudaError_t launch_kernel(const T* logits, const LogprobArgs& a, int64_t 
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = ranks;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ranks;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = kCluster ? 1 : 0;
+  cfg.numAttrs = kCluster ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, logits, a, ranks);
 }
 

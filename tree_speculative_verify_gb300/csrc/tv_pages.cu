@@ -2,12 +2,14 @@
 // compaction.  include/treeverify.h gives the rules; here is how they run.
 //
 // The state is small and its steps depend on one another (who still holds a page decides which
-// pages are free, that decides who gets which), so each call plans on one cluster of eight CTAs,
-// with a cluster barrier between the steps; requests and pages are split over the CTAs in
-// contiguous ranges, so that counts in range order give the order of requests and pages, and with
-// it results that do not depend on timing.  The reference counts change by integer atomics only.
-// The plan leaves a list of copies in the workspace; a second kernel, its programmatic dependent,
-// moves the rows.
+// pages are free, that decides who gets which), so a call is a chain of round trips, and what it
+// takes is latency.  It is planned by one CTA with the counts in shared memory, or, for pools and
+// batches that are too large for that, by a cluster of eight on the arrays in global memory, with a
+// cluster barrier between the steps; requests and pages are split over the CTAs in contiguous
+// ranges, so that counts in range order give the order of requests and pages, and with it results
+// that do not depend on timing.  The reference counts change by integer atomics only.  The plan
+// leaves a list of copies in the workspace; a second kernel, its programmatic dependent, moves the
+// rows.
 #include <cooperative_groups.h>
 
 #include "tv_common.cuh"
@@ -15,8 +17,10 @@
 namespace tv {
 namespace cg = cooperative_groups;
 
-constexpr int kPlanRanks = 8;
-constexpr int kPlanThreads = 512;
+constexpr int kPlanRanks = 8;         // CTAs of a cluster plan
+constexpr int kPlanThreads = 1024;
+// A single CTA plans up to this many pages, requests and table entries.
+constexpr int kOnePages = 8192, kOneRequests = 2048, kOneEntries = 32768;
 constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kCopyThreads = 256;
 constexpr int kCopyUnroll = 8;
@@ -85,11 +89,47 @@ __device__ __forceinline__ bool in_pool(const PlanArgs& a, int page) {
 struct Range {
   int lo, hi;
 };
+template <int kRanks>
 __device__ __forceinline__ Range share_of(int n, int rank) {
-  const int per = (n + kPlanRanks - 1) / kPlanRanks;
+  const int per = (n + kRanks - 1) / kRanks;
   const int lo = min(n, rank * per);
   return {lo, min(n, lo + per)};
 }
+
+template <int kRanks>
+__device__ __forceinline__ int plan_rank() {
+  return kRanks == 1 ? 0 : (int)cg::this_cluster().block_rank();
+}
+template <int kRanks>
+__device__ __forceinline__ void plan_sync() {
+  if constexpr (kRanks == 1)
+    __syncthreads();
+  else
+    cg::this_cluster().sync();
+}
+
+// Index of a table entry: 32 bits where a single CTA plans (at most kOneEntries).
+template <int kRanks>
+struct EntryIndex {
+  using type = int64_t;
+};
+template <>
+struct EntryIndex<1> {
+  using type = int32_t;
+};
+
+// The plan's arrays: a single CTA's in shared memory (n ints each, in order), a cluster's the
+// global ones.
+struct SharedInts {
+  int32_t* next;
+  template <int kRanks>
+  __device__ __forceinline__ int32_t* take(int32_t* global, int n) {
+    if constexpr (kRanks != 1) return global;
+    int32_t* p = next;
+    next += n;
+    return p;
+  }
+};
 
 // Exclusive prefix of v over the CTA's threads; *total: the sum.
 __device__ __forceinline__ int block_prefix(int v, int* total) {
@@ -104,15 +144,16 @@ __device__ __forceinline__ int block_prefix(int v, int* total) {
   __syncthreads();   // the last call's readers are done
   if (lane == 31) s_warp[warp] = x;
   __syncthreads();
-  int before = 0, sum = 0;
+  // every warp scans the warps' sums
+  const int c = lane < kPlanWarps ? s_warp[lane] : 0;
+  int y = c;
 #pragma unroll
-  for (int w = 0; w < kPlanWarps; ++w) {
-    const int c = s_warp[w];
-    before += w < warp ? c : 0;
-    sum += c;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int z = __shfl_up_sync(0xffffffffu, y, o);
+    if (lane >= o) y += z;
   }
-  *total = sum;
-  return before + x - v;
+  *total = __shfl_sync(0xffffffffu, y, 31);
+  return __shfl_sync(0xffffffffu, y - c, warp) + x - v;
 }
 
 // Sum of f(i) over the CTA's share r, by all its threads.
@@ -138,19 +179,21 @@ __device__ __forceinline__ void block_place(Range r, int start, F f, G g) {
   }
 }
 
-// Leaves the CTA's sums in the workspace, waits for the cluster, and returns the sums over the
-// CTAs before this one and over all of them.
+// The sums of s0 and s1 over the CTAs before this one and over all of them (with several CTAs: left
+// in the workspace, and a wait for the cluster).
 struct Sums {
   int before[2], all[2];
 };
-__device__ __forceinline__ Sums cluster_sums(const PlanArgs& a, int rank, int s0, int s1) {
+template <int kRanks>
+__device__ __forceinline__ Sums plan_sums(const PlanArgs& a, int rank, int s0, int s1) {
+  if constexpr (kRanks == 1) return {{0, 0}, {s0, s1}};
   if (threadIdx.x == 0) {
     a.w.rank_sum[2 * rank] = s0;
     a.w.rank_sum[2 * rank + 1] = s1;
   }
-  cg::this_cluster().sync();
+  plan_sync<kRanks>();
   Sums s = {{0, 0}, {0, 0}};
-  for (int q = 0; q < kPlanRanks; ++q)
+  for (int q = 0; q < kRanks; ++q)
     for (int k = 0; k < 2; ++k) {
       const int c = a.w.rank_sum[2 * q + k];
       if (q < rank) s.before[k] += c;
@@ -160,43 +203,69 @@ __device__ __forceinline__ Sums cluster_sums(const PlanArgs& a, int rank, int s0
 }
 
 // Whether the call's requests can all have their pages; if so, the lowest free pages are listed in
-// order (cluster-wide: the list is complete after the closing barrier).  `want`: pages that the
-// CTA's requests need; *start: the list position of the CTA's first one.
-__device__ __forceinline__ bool list_free_pages(const PlanArgs& a, int rank, int want, int* start) {
-  const Range pages = share_of(a.n_pool, rank);
-  auto is_free = [&](int p) { return a.refs[p] == 0 ? 1 : 0; };
-  const Sums s = cluster_sums(a, rank, want, block_count(pages, is_free));
+// order (complete after the closing barrier).  `want`: pages that the CTA's requests need; *start:
+// the list position of the CTA's first one; *total: all CTAs' together.
+template <int kRanks>
+__device__ __forceinline__ bool list_free_pages(const PlanArgs& a, int rank, const int32_t* refs,
+                                                int32_t* list, int want, int* start, int* total) {
+  const Range pages = share_of<kRanks>(a.n_pool, rank);
+  auto is_free = [&](int p) { return refs[p] == 0 ? 1 : 0; };
+  const Sums s = plan_sums<kRanks>(a, rank, want, block_count(pages, is_free));
   *start = s.before[0];
-  const int total = s.all[0];
-  const bool ok = total <= s.all[1];
-  if (ok && s.before[1] < total)
+  *total = s.all[0];
+  const bool ok = s.all[0] <= s.all[1];
+  if (ok && s.before[1] < s.all[0])
     block_place(pages, s.before[1], is_free, [&](int p, int at) {
-      if (at < total) a.w.list[at] = p;
+      if (at < s.all[0]) list[at] = p;
     });
-  cg::this_cluster().sync();
+  plan_sync<kRanks>();
   if (!ok && rank == 0 && threadIdx.x == 0) record_error(a.status, TV_ERR_CAPACITY);
   return ok;
 }
 
 // ---- fork: release, truncate, share ------------------------------------------------------------
-__global__ void __cluster_dims__(kPlanRanks, 1, 1) __launch_bounds__(kPlanThreads)
-    fork_plan_kernel(const PlanArgs a, int32_t* L, const int32_t* __restrict__ source,
-                     const int32_t* __restrict__ keep) {
-  pdl_launch_dependents();   // the copy kernel waits for this grid before it reads the plan
-  const int rank = (int)cg::this_cluster().block_rank();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const Range mine = share_of(a.B, rank);
-  const int P = a.page_tokens, G = a.max_pages;
-  const PageWorkspace& w = a.w;
+// Shared memory of a single CTA: counts and free list of the pages, four numbers per request.
+static size_t fork_smem(const tv_shape* s) {
+  return ((size_t)2 * s->n_pool_pages + (size_t)4 * s->B) * 4;
+}
 
-  // 1. what every request does, its new length, whether the source has the pages for it
-  for (int b = mine.lo + warp; b < mine.hi; b += kPlanWarps) {
+template <int kRanks>
+__global__ void __launch_bounds__(kPlanThreads)
+    fork_plan_kernel(const PlanArgs a, int32_t* L, const int32_t* source,
+                     const int32_t* keep) {
+  pdl_wait();
+  pdl_launch_dependents();   // the copy kernel waits for this grid before it reads the plan
+  extern __shared__ __align__(16) int32_t smem_ints[];
+  const int rank = plan_rank<kRanks>(), tid = threadIdx.x;
+  const Range mine = share_of<kRanks>(a.B, rank);
+  const int P = a.page_tokens, G = a.max_pages;
+  SharedInts ints = {smem_ints};
+  int32_t* refs = ints.take<kRanks>(a.refs, a.n_pool);
+  int32_t* list = ints.take<kRanks>(a.w.list, a.n_pool);
+  int32_t* act = ints.take<kRanks>(a.w.act, a.B);
+  int32_t* new_len = ints.take<kRanks>(a.w.len, a.B);
+  int32_t* pages = ints.take<kRanks>(a.w.pages, a.B);
+  int32_t* from = ints.take<kRanks>(a.w.from, a.B);
+  // f(request, position) over the table entries of the CTA's requests that change
+  using Entry = typename EntryIndex<kRanks>::type;
+  auto entries = [&](auto f) {
+    const Entry hi = (Entry)mine.hi * G;
+    for (Entry e = (Entry)mine.lo * G + tid; e < hi; e += kPlanThreads) {
+      const int b = (int)(e / G);
+      if (act[b] != kKeep) f(b, (int)(e - (Entry)b * G), e);
+    }
+  };
+
+  // 1. what every request does and its new length
+  if constexpr (kRanks == 1)
+    for (int p = tid; p < a.n_pool; p += kPlanThreads) refs[p] = a.refs[p];
+  for (int b = mine.lo + tid; b < mine.hi; b += kPlanThreads) {
     const int s = source[b];
-    int act = kKeep, len = 0, pages = 0, from = -1;
+    int what = kKeep, len = 0;
     if (s == -1) {
-      act = kRelease;
+      what = kRelease;
     } else if (s < 0 || s >= a.B || source[s] != s) {
-      if (lane == 0) record_error(a.status, TV_ERR_ARG);
+      record_error(a.status, TV_ERR_ARG);
     } else {
       const int Ls = L[s];
       len = Ls;
@@ -205,142 +274,151 @@ __global__ void __cluster_dims__(kPlanRanks, 1, 1) __launch_bounds__(kPlanThread
         if (ks >= 0) len = min(len, ks);
         if (kb >= 0) len = min(len, kb);
       }
-      if (s != b || len < Ls) act = s != b ? kFork : kTruncate;
-      if (act != kKeep) {
-        bool ok = Ls >= 0 && Ls <= a.raw_cap;
-        if (!ok && lane == 0) record_error(a.status, TV_ERR_CAPACITY);
-        if (ok) {
-          const int n = (len + P - 1) / P;
-          bool mapped = true;
-          for (int g = lane; g < n; g += 32) mapped &= in_pool(a, a.table[(int64_t)s * G + g]);
-          ok = __all_sync(0xffffffffu, mapped);
-          if (!ok && lane == 0) record_error(a.status, TV_ERR_ARG);
-        }
-        if (!ok) {
-          act = kKeep;
-        } else if (len % P != 0) {
-          // the partial last page: a fork gets a copy, a truncated request does if others hold it
-          from = a.table[(int64_t)s * G + len / P];
-          pages = act == kFork || a.refs[from] > 1 ? 1 : 0;
-        }
+      if (s != b || len < Ls) what = s != b ? kFork : kTruncate;
+      if (what != kKeep && (Ls < 0 || Ls > a.raw_cap)) {
+        record_error(a.status, TV_ERR_CAPACITY);
+        what = kKeep;
       }
     }
-    if (lane == 0) {
-      w.act[b] = act;
-      w.len[b] = len;
-      w.pages[b] = pages;
-      w.from[b] = from;
-    }
+    act[b] = what;
+    new_len[b] = len;
+    pages[b] = 0;   // here: whether a page is missing among the source's
   }
-  cg::this_cluster().sync();
+  __syncthreads();
+  entries([&](int b, int g, Entry) {
+    if (act[b] != kRelease && (int64_t)g * P < new_len[b] &&
+        !in_pool(a, a.table[(int64_t)source[b] * G + g]))
+      pages[b] = 1;
+  });
+  __syncthreads();
+  for (int b = mine.lo + tid; b < mine.hi; b += kPlanThreads) {
+    const int len = new_len[b];
+    int need = 0, src = -1;
+    if (pages[b]) {
+      record_error(a.status, TV_ERR_ARG);
+      act[b] = kKeep;
+    } else if ((act[b] == kTruncate || act[b] == kFork) && len % P != 0) {
+      // the partial last page: a fork gets a copy, a truncated request does if others hold it
+      src = a.table[(int64_t)source[b] * G + len / P];
+      need = act[b] == kFork || refs[src] > 1 ? 1 : 0;
+    }
+    pages[b] = need;
+    from[b] = src;
+  }
+  plan_sync<kRanks>();
 
   // 2. the reference counts: entries that go, full pages that gain a holder (sign -1: undone)
   auto count = [&](int sign) {
-    for (int b = mine.lo + warp; b < mine.hi; b += kPlanWarps) {
-      const int act = w.act[b];
-      if (act == kKeep) continue;
-      const int len = w.len[b], full = len / P, held = (len + P - 1) / P;
-      const int s = source[b];
-      for (int g = lane; g < G; g += 32) {
-        if (act != kTruncate || g >= held) {
-          const int p = a.table[(int64_t)b * G + g];
-          if (in_pool(a, p)) atomicAdd(&a.refs[p], -sign);
-        }
-        if (act == kFork && g < full) atomicAdd(&a.refs[a.table[(int64_t)s * G + g]], sign);
+    entries([&](int b, int g, Entry e) {
+      const int len = new_len[b];
+      if (act[b] != kTruncate || (int64_t)g * P >= len) {
+        const int p = a.table[e];
+        if (in_pool(a, p)) atomicAdd(&refs[p], -sign);
       }
-    }
+      if (act[b] == kFork && g < len / P)
+        atomicAdd(&refs[a.table[(int64_t)source[b] * G + g]], sign);
+    });
   };
   count(1);
-  cg::this_cluster().sync();
+  plan_sync<kRanks>();
 
   // 3. new pages for the partial last pages, in the order of the requests
-  auto pages_of = [&](int b) { return w.pages[b]; };
-  int start;
-  const bool ok = list_free_pages(a, rank, block_count(mine, pages_of), &start);
-  if (!ok) {   // nothing changes
-    if (rank == 0 && tid == 0) w.n_jobs[0] = 0;
-    count(-1);
+  auto pages_of = [&](int b) { return pages[b]; };
+  int start, total;
+  const bool ok = list_free_pages<kRanks>(a, rank, refs, list, block_count(mine, pages_of), &start,
+                                          &total);
+  if (rank == 0 && tid == 0) a.w.n_jobs[0] = ok ? total : 0;
+  if (!ok) {   // nothing changes (a single CTA has only changed its own copy of the counts)
+    if constexpr (kRanks != 1) count(-1);
     __syncthreads();
-    for (int b = mine.lo + tid; b < mine.hi; b += kPlanThreads) w.act[b] = kKeep;
+    for (int b = mine.lo + tid; b < mine.hi; b += kPlanThreads) a.w.act[b] = kKeep;
     return;
   }
   block_place(mine, start, pages_of, [&](int b, int at) {
-    const int page = w.list[at], src = w.from[b];
-    w.jobs[at] = {src, page, w.len[b] % P, 0};
-    a.refs[page] = 1;
-    if (w.act[b] == kTruncate) atomicAdd(&a.refs[src], -1);
-    w.from[b] = page;
+    const int page = list[at], src = from[b];
+    a.w.jobs[at] = {src, page, new_len[b] % P, 0};
+    refs[page] = 1;
+    if (act[b] == kTruncate) atomicAdd(&refs[src], -1);
+    from[b] = page;
   });
-  __syncthreads();   // the new pages of this CTA's requests are in w.from
+  __syncthreads();   // the new pages of this CTA's requests are in from
 
-  // 4. the table and the lengths.  A fork reads full pages of its source, which no other request
-  //    writes: a source changes at most its last partial page and what lies behind it.
-  for (int b = mine.lo + warp; b < mine.hi; b += kPlanWarps) {
-    const int act = w.act[b];
-    if (act == kKeep) continue;
-    const int len = w.len[b], full = len / P, tail = len % P != 0 ? full : -1;
-    const int s = source[b], pages = w.pages[b], page = w.from[b];
-    for (int g = lane; g < G; g += 32) {
-      int32_t* e = &a.table[(int64_t)b * G + g];
-      if (act == kRelease)
-        *e = -1;
-      else if (g < full) {
-        if (act == kFork) *e = a.table[(int64_t)s * G + g];
-      } else if (g == tail) {
-        if (pages) *e = page;
-      } else {
-        *e = -1;
-      }
+  // 4. the table, the lengths, the counts.  A fork reads full pages of its source, which no other
+  //    request writes: a source changes at most its last partial page and what lies behind it.
+  entries([&](int b, int g, Entry e) {
+    const int len = new_len[b], full = len / P;
+    if (act[b] != kRelease && g < full) {
+      if (act[b] == kFork) a.table[e] = a.table[(int64_t)source[b] * G + g];
+    } else if (act[b] != kRelease && g == full && len % P != 0) {
+      if (pages[b]) a.table[e] = from[b];
+    } else {
+      a.table[e] = -1;
     }
-    if (lane == 0) L[b] = len;
+  });
+  for (int b = mine.lo + tid; b < mine.hi; b += kPlanThreads) {
+    if (act[b] != kKeep) L[b] = new_len[b];
+    if constexpr (kRanks == 1) {   // for the copies of the indexer keys
+      a.w.act[b] = act[b];
+      a.w.len[b] = new_len[b];
+    }
   }
-  // the number of copies: the last CTA's list position after its own
-  int total;
-  {
-    int n = 0;
-    for (int b = mine.lo + tid; b < mine.hi; b += kPlanThreads) n += w.pages[b];
-    block_prefix(n, &total);
-  }
-  if (rank == kPlanRanks - 1 && tid == 0) w.n_jobs[0] = start + total;
+  if constexpr (kRanks == 1)
+    for (int p = tid; p < a.n_pool; p += kPlanThreads) a.refs[p] = refs[p];
 }
 
 // ---- reserve: the pages of the next tokens -------------------------------------------------------
-__global__ void __cluster_dims__(kPlanRanks, 1, 1) __launch_bounds__(kPlanThreads)
-    reserve_kernel(const PlanArgs a, const int32_t* __restrict__ need) {
-  const int rank = (int)cg::this_cluster().block_rank();
-  const Range mine = share_of(a.B, rank);
+static size_t reserve_smem(const tv_shape* s) {
+  return ((size_t)2 * s->n_pool_pages + (size_t)s->B) * 4;
+}
+
+template <int kRanks>
+__global__ void __launch_bounds__(kPlanThreads)
+    reserve_kernel(const PlanArgs a, const int32_t* need) {
+  pdl_wait();
+  extern __shared__ __align__(16) int32_t smem_ints[];
+  const int rank = plan_rank<kRanks>(), tid = threadIdx.x;
+  const Range mine = share_of<kRanks>(a.B, rank);
   const int P = a.page_tokens, G = a.max_pages;
+  SharedInts ints = {smem_ints};
+  int32_t* refs = ints.take<kRanks>(a.refs, a.n_pool);
+  int32_t* list = ints.take<kRanks>(a.w.list, a.n_pool);
+  int32_t* pages = ints.take<kRanks>(a.w.pages, a.B);
+  if constexpr (kRanks == 1)
+    for (int p = tid; p < a.n_pool; p += kPlanThreads) refs[p] = a.refs[p];
   // unmapped pages of the positions L .. L + need - 1
-  for (int b = mine.lo + threadIdx.x; b < mine.hi; b += kPlanThreads) {
+  for (int b = mine.lo + tid; b < mine.hi; b += kPlanThreads) {
     const int n = need[b], L = a.L[b];
-    int pages = 0;
+    int missing = 0;
     if (n > 0) {
       if (L < 0) {
         record_error(a.status, TV_ERR_ARG);
       } else if ((int64_t)L + n > a.raw_cap) {
         record_error(a.status, TV_ERR_CAPACITY);
       } else {
+#pragma unroll 4
         for (int g = L / P; g <= (L + n - 1) / P; ++g) {
           const int p = a.table[(int64_t)b * G + g];
           if (p == -1)
-            ++pages;
+            ++missing;
           else if (!in_pool(a, p))
             record_error(a.status, TV_ERR_ARG);
         }
       }
     }
-    a.w.pages[b] = pages;
+    pages[b] = missing;
   }
   __syncthreads();
-  auto pages_of = [&](int b) { return a.w.pages[b]; };
-  int start;
-  if (!list_free_pages(a, rank, block_count(mine, pages_of), &start)) return;
+  auto pages_of = [&](int b) { return pages[b]; };
+  int start, total;
+  if (!list_free_pages<kRanks>(a, rank, refs, list, block_count(mine, pages_of), &start, &total))
+    return;
+  if (total == 0) return;
   block_place(mine, start, pages_of, [&](int b, int at) {
     const int L = a.L[b], n = need[b];
     for (int g = L / P; g <= (L + n - 1) / P; ++g) {
       int32_t* e = &a.table[(int64_t)b * G + g];
       if (*e != -1) continue;
-      const int page = a.w.list[at++];
+      const int page = list[at++];
       *e = page;
       a.refs[page] = 1;
     }
@@ -348,52 +426,68 @@ __global__ void __cluster_dims__(kPlanRanks, 1, 1) __launch_bounds__(kPlanThread
 }
 
 // ---- compaction ----------------------------------------------------------------------------------
-__global__ void __cluster_dims__(kPlanRanks, 1, 1) __launch_bounds__(kPlanThreads)
-    compact_plan_kernel(const PlanArgs a, int32_t* __restrict__ remap,
-                        int32_t* __restrict__ n_live_out) {
+static size_t compact_smem(const tv_shape* s) { return (size_t)5 * s->n_pool_pages * 4; }
+
+template <int kRanks>
+__global__ void __launch_bounds__(kPlanThreads)
+    compact_plan_kernel(const PlanArgs a, int32_t* remap_out, int32_t* n_live_out) {
   pdl_launch_dependents();
-  auto cluster = cg::this_cluster();
-  const int rank = (int)cluster.block_rank();
+  extern __shared__ __align__(16) int32_t smem_ints[];
+  const int rank = plan_rank<kRanks>();
   const int tid = threadIdx.x, all = rank * kPlanThreads + tid;
-  constexpr int kAll = kPlanRanks * kPlanThreads;
-  const Range mine = share_of(a.n_pool, rank);
+  constexpr int kAll = kRanks * kPlanThreads;
+  const Range mine = share_of<kRanks>(a.n_pool, rank);
   const int P = a.page_tokens, G = a.max_pages;
-  const int64_t entries = (int64_t)a.B * G;
-  const PageWorkspace& w = a.w;
+  using Entry = typename EntryIndex<kRanks>::type;
+  const Entry entries = (Entry)a.B * G;
+  SharedInts ints = {smem_ints};
+  const int32_t* refs = a.refs;
+  int32_t* tokens = ints.take<kRanks>(a.w.tokens, a.n_pool);
+  int32_t* holders = ints.take<kRanks>(a.w.holders, a.n_pool);
+  int32_t* list = ints.take<kRanks>(a.w.list, a.n_pool);
+  int32_t* remap = ints.take<kRanks>(remap_out, a.n_pool);
+  if constexpr (kRanks == 1) {
+    int32_t* copy = ints.take<1>(nullptr, a.n_pool);
+    for (int p = tid; p < a.n_pool; p += kPlanThreads) copy[p] = a.refs[p];
+    refs = copy;
+  }
 
   // 1. every page's holders in the table and the most tokens that one of them has in it
-  for (int p = mine.lo + tid; p < mine.hi; p += kPlanThreads) w.tokens[p] = w.holders[p] = 0;
-  cluster.sync();
-  for (int64_t e = all; e < entries; e += kAll) {
+  for (int p = mine.lo + tid; p < mine.hi; p += kPlanThreads) tokens[p] = holders[p] = 0;
+  plan_sync<kRanks>();
+  for (Entry e = all; e < entries; e += kAll) {
     const int p = a.table[e];
     if (p == -1) continue;
     if (!in_pool(a, p)) {
       record_error(a.status, TV_ERR_ARG);
       continue;
     }
-    const int b = (int)(e / G), g = (int)(e - (int64_t)b * G);
+    const int b = (int)(e / G), g = (int)(e - (Entry)b * G);
     const int64_t left = (int64_t)a.L[b] - (int64_t)g * P;
-    atomicMax(&w.tokens[p], (int)(left < 0 ? 0 : left > P ? P : left));
-    atomicAdd(&w.holders[p], 1);
+    atomicMax(&tokens[p], (int)(left < 0 ? 0 : left > P ? P : left));
+    atomicAdd(&holders[p], 1);
   }
-  cluster.sync();
+  plan_sync<kRanks>();
 
   // 2. live pages in order; those at n_live and above take the holes below it, in order
-  auto live = [&](int p) { return a.refs[p] > 0 || w.holders[p] > 0 ? 1 : 0; };
-  const Sums s = cluster_sums(a, rank, block_count(mine, live), 0);
+  auto live = [&](int p) { return refs[p] > 0 || holders[p] > 0 ? 1 : 0; };
+  const Sums s = plan_sums<kRanks>(a, rank, block_count(mine, live), 0);
   const int n_live = s.all[0];
-  // live pages below n_live: complete in the shares before the one that holds n_live
-  int before = s.before[0];
+  int low_live;   // live pages below n_live
   {
-    int low = 0, total;
+    int low = 0;
     for (int p = mine.lo + tid; p < min(mine.hi, n_live); p += kPlanThreads) low += live(p);
-    block_prefix(low, &total);
-    if (tid == 0) w.rank_sum[2 * kPlanRanks + rank] = total;
+    block_prefix(low, &low_live);
+    if constexpr (kRanks != 1) {
+      int32_t* sums = a.w.rank_sum + 2 * kRanks;
+      if (tid == 0) sums[rank] = low_live;
+      plan_sync<kRanks>();
+      low_live = 0;
+      for (int q = 0; q < kRanks; ++q) low_live += sums[q];
+    }
   }
-  cluster.sync();
-  int low_live = 0;
-  for (int q = 0; q < kPlanRanks; ++q) low_live += w.rank_sum[2 * kPlanRanks + q];
   const int moves = n_live - low_live;
+  int before = s.before[0];
   for (int p0 = mine.lo; p0 < mine.hi; p0 += kPlanThreads) {
     const int p = p0 + tid;
     const int is = p < mine.hi ? live(p) : 0;
@@ -401,37 +495,38 @@ __global__ void __cluster_dims__(kPlanRanks, 1, 1) __launch_bounds__(kPlanThread
     const int at = before + block_prefix(is, &total);   // live pages before p
     before += total;
     if (p >= mine.hi) continue;
-    const int refs = a.refs[p];
-    if (refs < w.holders[p]) record_error(a.status, TV_ERR_ARG);
+    if (refs[p] < holders[p]) record_error(a.status, TV_ERR_ARG);
     if (p < n_live) {
       remap[p] = is ? p : -1;
-      if (!is) w.list[p - at] = p;
+      if (!is) list[p - at] = p;
     } else if (is) {
       // a page that somebody besides the table holds moves whole
-      w.jobs[at - low_live] = {p, -1, refs > w.holders[p] ? P : w.tokens[p], 0};
+      a.w.jobs[at - low_live] = {p, -1, refs[p] > holders[p] ? P : tokens[p], 0};
     } else {
       remap[p] = -1;
     }
   }
-  cluster.sync();
+  plan_sync<kRanks>();
   for (int i = all; i < moves; i += kAll) {
-    const int src = w.jobs[i].src, dst = w.list[i];
-    w.jobs[i].dst = dst;
+    const int src = a.w.jobs[i].src, dst = list[i];
+    a.w.jobs[i].dst = dst;
     remap[src] = dst;
-    a.refs[dst] = a.refs[src];
+    a.refs[dst] = refs[src];
     a.refs[src] = 0;
   }
   if (all == 0) {
     n_live_out[0] = n_live;
-    w.n_jobs[0] = moves;
+    a.w.n_jobs[0] = moves;
   }
-  cluster.sync();
+  plan_sync<kRanks>();
 
   // 3. the table follows
-  for (int64_t e = all; e < entries; e += kAll) {
+  for (Entry e = all; e < entries; e += kAll) {
     const int p = a.table[e];
-    if (in_pool(a, p)) a.table[e] = remap[p];
+    if (in_pool(a, p) && remap[p] != p) a.table[e] = remap[p];
   }
+  if constexpr (kRanks == 1)
+    for (int p = tid; p < a.n_pool; p += kPlanThreads) remap_out[p] = remap[p];
 }
 
 // ---- the copies ------------------------------------------------------------------------------------
@@ -549,6 +644,33 @@ static int launch_copy(const char* fn, const tv_shape* s, const PlanArgs& p, voi
   return e == cudaSuccess ? tv_check_launch(fn) : launch_error(fn, e);
 }
 
+// Launches a plan: one CTA where the state is small enough (a serving batch's fork 5 us against 11 us on
+// the cluster), else the cluster.
+template <typename... KArgs, typename... Args>
+static int launch_plan(const char* fn, const tv_shape* s, void (*one)(KArgs...),
+                       void (*cluster)(KArgs...), size_t smem, cudaStream_t stream, Args... args) {
+  const bool single = s->n_pool_pages <= kOnePages && s->B <= kOneRequests &&
+                      (int64_t)s->B * s->max_pages <= kOneEntries;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(single ? 1 : kPlanRanks);
+  cfg.blockDim = dim3(kPlanThreads);
+  cfg.dynamicSmemBytes = single ? smem : 0;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kPlanRanks;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = single ? 1 : 2;
+  cudaError_t e = cudaSuccess;
+  if (single && smem > 48 * 1024)
+    e = cudaFuncSetAttribute(one, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, single ? one : cluster, KArgs(args)...);
+  return e == cudaSuccess ? tv_check_launch(fn) : launch_error(fn, e);
+}
+
 }  // namespace tv
 
 size_t tv_pages_workspace(const tv_shape* s) { return tv::page_workspace(s, nullptr, nullptr); }
@@ -558,16 +680,17 @@ int tv_launch_fork(const tv_shape* s, const int32_t* source, const int32_t* keep
                    int32_t* status, cudaStream_t stream) {
   const char* fn = "tv_pages_fork";
   const tv::PlanArgs a = tv::plan_args(s, L, refs, workspace, status);
-  tv::fork_plan_kernel<<<tv::kPlanRanks, tv::kPlanThreads, 0, stream>>>(a, L, source, keep);
-  if (int rc = tv_check_launch(fn)) return rc;
+  if (int rc = tv::launch_plan(fn, s, tv::fork_plan_kernel<1>, tv::fork_plan_kernel<tv::kPlanRanks>,
+                               tv::fork_smem(s), stream, a, L, source, keep))
+    return rc;
   return tv::launch_copy(fn, s, a, pools, keys, d_idx, source, stream);
 }
 
 int tv_launch_reserve(const tv_shape* s, const int32_t* need, const int32_t* L, int32_t* refs,
                       void* workspace, int32_t* status, cudaStream_t stream) {
   const tv::PlanArgs a = tv::plan_args(s, L, refs, workspace, status);
-  tv::reserve_kernel<<<tv::kPlanRanks, tv::kPlanThreads, 0, stream>>>(a, need);
-  return tv_check_launch("tv_pages_reserve");
+  return tv::launch_plan("tv_pages_reserve", s, tv::reserve_kernel<1>,
+                         tv::reserve_kernel<tv::kPlanRanks>, tv::reserve_smem(s), stream, a, need);
 }
 
 int tv_launch_compact(const tv_shape* s, const int32_t* L, int32_t* refs, void* const pools[6],
@@ -575,7 +698,9 @@ int tv_launch_compact(const tv_shape* s, const int32_t* L, int32_t* refs, void* 
                       cudaStream_t stream) {
   const char* fn = "tv_pages_compact";
   const tv::PlanArgs a = tv::plan_args(s, L, refs, workspace, status);
-  tv::compact_plan_kernel<<<tv::kPlanRanks, tv::kPlanThreads, 0, stream>>>(a, remap, n_live);
-  if (int rc = tv_check_launch(fn)) return rc;
+  if (int rc = tv::launch_plan(fn, s, tv::compact_plan_kernel<1>,
+                               tv::compact_plan_kernel<tv::kPlanRanks>, tv::compact_smem(s), stream,
+                               a, remap, n_live))
+    return rc;
   return tv::launch_copy(fn, s, a, pools, nullptr, 0, nullptr, stream);
 }
