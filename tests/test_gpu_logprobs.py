@@ -1,10 +1,10 @@
 """tv_token_logprobs on the GPU against the fp64 oracle.  Ids and targets are exact (they are decided
 on the stored logits); the fp32 values are held to the rounding of their formulas.
 
-Tolerances.  u = 2^-24.  A term e^{y}, y = scale (x - m), is formed as 2^{fl((x - m) c)}, c =
-fl(scale log2 e): the difference, the product and c each round by u relative to y, log2 e once more,
-so e^{y} is off by a factor within 4 u |y| + 2^-22 (two ulp of the exponential); weighted by the
-terms, the sum S is off by 4 u E|y| + 2^-22, E|y| = ln S - entropy <= ln V, plus its additions: one thread adds at most
+Tolerances.  u = 2^-24.  A term e^{y}, y = scale (x - m), is formed as 2^{fl((x - m) c)} or, the same
+to within one rounding, 2^{fl(x c - b)} with b = fl(m c) taken out again at the end; c = fl(scale
+log2 e): the difference, the product and c each round by u relative to y, log2 e once more, so e^{y}
+is off by a factor within 4 u |y| + 2^-22 (two ulp of the exponential); weighted by the terms, the sum S is off by 4 u E|y| + 2^-22, E|y| = ln S - entropy <= ln V, plus its additions: one thread adds at most
 V / 256 + 8 terms in a row, the joins at most 16 more sums with a factor each (u for the sum,
 2^-22 + 4 u for the factor's exponential).  ln S adds two ulp of itself.  So
   dS   = 4 u lnV + 2^-22 + (V / 256 + 24) u + 16 (2^-22 + 4 u) ... relative error of S and T
@@ -218,6 +218,21 @@ def test_peaked_rows_keep_small_probabilities():
     got, status = _run(x, tokens, nodes, 1.0, 3)
     assert status == 0
     _check(x, got, tokens, nodes, 1.0, 3)
+
+
+@pytest.mark.parametrize("scale", [1e-6, 0.01, 30.0, 1e6])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_extreme_temperatures(scale, dtype):
+    # flat and one-token distributions, the exponents' far form (largest logit times scale beyond
+    # thousands) and logits that straddle it
+    x = _logits(1, 3, 5003, dtype, 21).contiguous()
+    x[0, 1] += 300.0
+    x[0, 2] -= 5000.0
+    tokens = np.array([[0, 1, 2, 3, 4, 5]], dtype=np.int32)
+    nodes = np.array([[0, 0, 1, 1, 2, 2]], dtype=np.int32)
+    got, status = _run(x, tokens, nodes, scale, 6)
+    assert status == 0
+    _check(x, got, tokens, nodes, scale, 6)
 
 
 def test_rows_beyond_32_bit_offsets():

@@ -12,10 +12,10 @@
 // logit is >= t, so a logit below t is no alternative.  In the pass a thread only notes its two
 // largest tiles and the largest logit of its other tiles; at the end t is taken from the threads'
 // largest logits and the few tiles that reach t are looked at again, a vector per thread (all
-// vectors of a thread where a third tile reaches t).  The logits found, little
-// more than K, are ranked by counting: a key's place is the number of larger keys (a key is the
-// logit's order, then the lower id, so keys differ).  Rows of so many equal logits that the list
-// overflows take one scan per alternative instead.
+// vectors of a thread where a third tile reaches t).  The logits found, little more than K, are
+// ranked by counting: a key's place is the number of larger keys (a key is the logit's order, then
+// the lower id, so keys differ).  Rows of so many equal logits that the list overflows take one
+// scan per alternative instead.
 #include <cooperative_groups.h>
 #include <float.h>
 
@@ -82,19 +82,14 @@ __device__ __forceinline__ bool is_far(float m, float c) { return !(fabsf(m * c)
 // p relative to a maximum m >= p.m
 __device__ __forceinline__ void rebase(Partial& p, float m, float c) {
   if (m > p.m) {
-    const float d = is_far(m, c) || is_far(p.m, c) ? (p.m - m) * c : p.m * c - m * c;
+    // (the rounded products, not contracted: the sums are relative to them)
+    const float d = is_far(m, c) || is_far(p.m, c) ? (p.m - m) * c
+                                                   : __fmul_rn(p.m, c) - __fmul_rn(m, c);
     const float e = fmaxf(d, kMinExp), f = exp2_approx(e);
     p.t = (p.t + e * p.s) * f;
     p.s *= f;
     p.m = m;
   }
-}
-
-__device__ __forceinline__ Partial join(Partial a, Partial b, float c) {
-  const float m = fmaxf(a.m, b.m);
-  rebase(a, m, c);
-  rebase(b, m, c);
-  return {m, a.s + b.s, a.t + b.t};
 }
 
 // Order of a logit as an unsigned number; equal logits (and -0, +0) give equal numbers.
@@ -420,7 +415,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const T* logits,
   // adds a vector's logits to the sums, exponents bounded: any logits, any maximum
   auto add_vector = [&](const uint4& w, float& s, float& t) {
     const bool far = is_far(p.m, c);
-    const float base = p.m == -INFINITY ? 0.f : p.m, shift = -(p.m * c);
+    const float base = p.m == -INFINITY ? 0.f : p.m, shift = -__fmul_rn(p.m, c);
     float x[kVec];
     Row<T>::unpack(w, x);
 #pragma unroll
@@ -451,7 +446,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const T* logits,
     for (int u = 0; u < kLpUnroll; ++u)   // (a row that is not there: the first one again, not added)
       w[u] = ld_shared_16(slot + (u < left ? u : 0) * kThreads * 16);
     note_tile(Row<T>::largest(w), t);
-    const float shift = -(p.m * c);
+    const float shift = -__fmul_rn(p.m, c);
     const uint64_t shift2 = pack_f32x2(shift, shift);
     uint64_t s2 = pack_f32x2(0.f, 0.f), t2 = s2;
 #pragma unroll
@@ -570,7 +565,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const T* logits,
   const bool none = !bad && p.m == -INFINITY;
   const float nan = __int_as_float(0x7fffffff);
   // ln S relative to m: the rounding of m c taken out (-inf for an empty row)
-  const float residual = is_far(p.m, c) ? 0.f : fmaf(p.m, c, -(p.m * c));
+  const float residual = is_far(p.m, c) ? 0.f : fmaf(p.m, c, -__fmul_rn(p.m, c));
   const float ln_s = logf(p.s), log_s = ln_s - residual * kLn2;
   auto log_prob = [&](float x) {
     return bad ? nan : x == -INFINITY ? x : (x - p.m) * a.scale - log_s;

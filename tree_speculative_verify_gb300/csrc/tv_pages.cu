@@ -640,7 +640,7 @@ static int launch_copy(const char* fn, const tv_shape* s, const PlanArgs& p, voi
     a.len = p.w.len;
     a.source = source;
   }
-  const cudaError_t e = launch_pdl(page_copy_kernel, dim3(152 * 4), dim3(kCopyThreads), 0, stream, a);
+  const cudaError_t e = launch_pdl(page_copy_kernel, dim3(152 * 2), dim3(kCopyThreads), 0, stream, a);
   return e == cudaSuccess ? tv_check_launch(fn) : launch_error(fn, e);
 }
 
