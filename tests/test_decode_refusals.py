@@ -103,3 +103,30 @@ def test_binding_refuses_host_tensors(lib):
                                None, st)
     with pytest.raises(ValueError):
         _lib.tv_pages_reserve(_pages_shape(), st, st, st, None, st)
+    with pytest.raises(TypeError):
+        _lib.tv_pages_reserve(_pages_shape(), st, [1, 2], st, None, st)
+
+
+class _OnDevice:
+    """Stands in for a tensor of another device, which a machine with one device cannot make."""
+    is_cuda, dtype = True, torch.int32
+
+    def get_device(self):
+        return 1
+
+    def is_contiguous(self):
+        return True
+
+    def numel(self):
+        return 1 << 20
+
+    def data_ptr(self):
+        raise AssertionError("the address of a tensor on another device was taken")
+
+
+def test_binding_refuses_another_device(monkeypatch):
+    monkeypatch.setattr(_lib, "_here", lambda: 0)
+    monkeypatch.setattr(_lib.torch, "Tensor", _OnDevice)
+    t = _OnDevice()
+    with pytest.raises(ValueError, match="another device"):
+        _lib.tv_pages_reserve(_pages_shape(), t, t, t, t, t)

@@ -220,6 +220,27 @@ def test_peaked_rows_keep_small_probabilities():
     _check(x, got, tokens, nodes, 1.0, 3)
 
 
+@pytest.mark.parametrize("dtype,T", [(BF, 128), (F32, 256), (BF, 256)])
+def test_largest_logits_in_one_thread_s_reach(dtype, T):
+    # the pass gives thread i of T the vectors i, i + T, ...: all large logits in one of those columns,
+    # and more of them than the candidate list holds, so that neither the bound nor the second scan
+    # can keep the list short
+    kvec = 8 if dtype == BF else 4
+    V, rows = 80000, 1 if T == 256 else 600
+    x = torch.full((rows, 1, V), -3.0, dtype=dtype, device="cuda")
+    i = torch.arange(V, device="cuda")
+    col = (i // kvec) % T == 5
+    vals = torch.linspace(1.0, 200.0, int(col.sum()), device="cuda").to(dtype)
+    x[0, 0, col] = vals[torch.randperm(len(vals), generator=torch.Generator().manual_seed(2)).cuda()]
+    x[-1, 0, col] = vals
+    got, status = _run(x, n_top=32)
+    assert status == 0
+    pick = [0, rows - 1]
+    want = oracle.token_logprobs(x[pick].float().cpu().numpy(), n_top=32)
+    assert np.array_equal(got["top_ids"][pick], want["top_ids"])
+    assert np.array_equal(got["target"][pick], want["target"])
+
+
 @pytest.mark.parametrize("scale", [1e-6, 0.01, 30.0, 1e6])
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_extreme_temperatures(scale, dtype):

@@ -14,8 +14,9 @@
 // largest logits and the few tiles that reach t are looked at again, a vector per thread (all
 // vectors of a thread where a third tile reaches t).  The logits found, little more than K, are
 // ranked by counting: a key's place is the number of larger keys (a key is the logit's order, then
-// the lower id, so keys differ).  Rows of so many equal logits that the list overflows take one
-// scan per alternative instead.
+// the lower id, so keys differ).  Where many logits equal t and the list overflows, one more scan in
+// the order of the ids takes what lies above t and the first K of those equal to it; should what
+// lies above t alone overflow, one scan per alternative.
 #include <cooperative_groups.h>
 #include <float.h>
 
@@ -198,6 +199,7 @@ struct LpShared {
     uint64_t cand[kLpCand];
     int hit[2 * kThreads];         // tile * kThreads + thread: a thread's tile to look at again
     uint16_t column[kThreads];     // threads with more than two of them
+    uint64_t ties[kLpMaxTop];      // keys of the first logits equal to the bound
   };
   union {
     uint4 ring[kLpStages][kLpUnroll][kThreads];   // tiles in flight; a thread reads only its own
@@ -269,7 +271,8 @@ __device__ __forceinline__ void list_vector(LpShared<kThreads, kCluster>& sm, co
 
 // The CTA's K largest keys by one scan of its vectors [lo, hi) per key, into sm.top.
 template <typename T, int kThreads, bool kCluster>
-__device__ __noinline__ void scan_top(LpShared<kThreads, kCluster>& sm, const Row<T>& row, int lo, int hi, int K) {
+__device__ __noinline__ void scan_top(LpShared<kThreads, kCluster>& sm, const Row<T>& row, int lo,
+                                      int hi, int K) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint64_t last = ~0ull;
   for (int k = 0; k < K; ++k) {
@@ -292,6 +295,75 @@ __device__ __noinline__ void scan_top(LpShared<kThreads, kCluster>& sm, const Ro
     if (threadIdx.x == 0) sm.top[k] = best;
     last = best;
   }
+}
+
+// Rebuilds the candidate list after an overflow, with the K-th largest of all threads' largest logits
+// (m: this thread's) as the bound: the logits above it, and the K lowest ids of those equal to it.
+// Returns its length (more than kLpCand: it overflowed again).
+template <typename T, int kThreads, bool kCluster>
+__device__ __noinline__ int list_with_ties(LpShared<kThreads, kCluster>& sm, const Row<T>& row, int lo,
+                                           int hi, float m, int K) {
+  constexpr int kVec = Row<T>::kVec;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  __syncthreads();
+  uint32_t* orders = reinterpret_cast<uint32_t*>(sm.list.hit);
+  const uint32_t mine = order_of(m);
+  orders[tid] = mine;
+  if (tid == 0) sm.count = 0;
+  __syncthreads();
+  int place = 0;
+#pragma unroll 8
+  for (int q = 0; q < kThreads; ++q)
+    place += orders[q] > mine || (orders[q] == mine && q < tid) ? 1 : 0;
+  if (place == K - 1) sm.largest[0] = mine;
+  __syncthreads();
+  const float bound = logit_of_order(max(sm.largest[0], kOrderLowest));
+  int ties = 0;   // found so far, the same in every thread
+  for (int i0 = lo; i0 < hi; i0 += kThreads) {
+    const int i = i0 + tid;
+    uint32_t equal = 0u;   // bit j: element j of the thread's vector
+    if (i < hi) {
+      float x[kVec];
+      Row<T>::unpack(row.load(i), x);
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) {
+        if (x[j] == bound) equal |= 1u << j;
+        if (x[j] > bound) {
+          const int at = atomicAdd(&sm.count, 1);
+          if (at < kLpCand) sm.list.cand[at] = key_of(x[j], row.id(i, j));
+        }
+      }
+    }
+    if (ties >= K || !__syncthreads_or(equal != 0u)) continue;
+    // their places in the order of the ids: vectors ascend with the threads
+    const int n = __popc(equal);
+    int before = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) before += y;
+    }
+    if (lane == 31) sm.scan[warp] = before;
+    __syncthreads();
+    int at = ties + before - n;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      const int c = (int)sm.scan[w];
+      if (w < warp) at += c;
+      ties += c;
+    }
+#pragma unroll
+    for (int j = 0; j < kVec; ++j)
+      if (equal >> j & 1u) {
+        if (at < K) sm.list.ties[at] = key_of(bound, row.id(i, j));
+        ++at;
+      }
+    __syncthreads();   // the counts are read
+  }
+  __syncthreads();
+  const int above = sm.count, n = min(ties, K);
+  if (above + n <= kLpCand && tid < n) sm.list.cand[above + tid] = sm.list.ties[tid];
+  __syncthreads();
+  return above + n;
 }
 
 // Places of the n keys of `list` among each other: out[place] = key for the places below K.
@@ -513,7 +585,8 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const T* logits,
     }
   }
   __syncthreads();
-  const int n = sm.count;
+  int n = sm.count;
+  if (n > kLpCand) n = list_with_ties(sm, row, lo, hi, largest, K);
   if (n > kLpCand)
     scan_top(sm, row, lo, hi, K);
   else
