@@ -189,6 +189,23 @@ def test_compact_moves_the_upper_live_pages(n_pool, B, G):
     assert s.remap.tolist()[:int(s.n_live)] == list(range(int(s.n_live)))
 
 
+@pytest.mark.parametrize("n_pool", [400, 9000])
+def test_reserve_of_long_prompts(n_pool):
+    # windows of many pages, some of them mapped already, beside short ones
+    P, G, B = 512, 150, 40
+    rng = np.random.default_rng(n_pool)
+    L = [int(x) for x in rng.integers(0, 3 * P, size=B)]
+    table = _random_table(rng, B, G, 300, L, P)
+    for b in (3, 7):
+        table[b][9] = 301 + b
+    s = Pool(table, L, n_pool, P)
+    need = [int(x) for x in rng.integers(1, 9, size=B)]
+    need[3], need[5], need[7], need[33], need[39] = 40 * P, 5 * P, 33 * P + 1, 32 * P, 6 * P
+    s.check([s.reserve(need)])
+    need[3] = 150 * P
+    s.check([s.reserve(need)])       # past the capacity, and the others once more: nothing is missing
+
+
 def test_compact_reports_an_inconsistent_table():
     P = 512
     s = Pool([[5, 90], [3, -1]], [600, 20], 8, P)

@@ -19,8 +19,8 @@ namespace cg = cooperative_groups;
 
 constexpr int kPlanRanks = 8;         // CTAs of a cluster plan
 constexpr int kPlanThreads = 1024;
-// A single CTA plans up to this many pages, requests and table entries.
-constexpr int kOnePages = 8192, kOneRequests = 2048, kOneEntries = 32768;
+// A single CTA plans up to this many pages and steps (table entries; requests for a reserve).
+constexpr int kOnePages = 8192, kOneSteps = 4096;
 constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kCopyThreads = 256;
 constexpr int kCopyUnroll = 8;
@@ -108,7 +108,7 @@ __device__ __forceinline__ void plan_sync() {
     cg::this_cluster().sync();
 }
 
-// Index of a table entry: 32 bits where a single CTA plans (at most kOneEntries).
+// Index of a table entry: 32 bits where a single CTA plans (at most kOneSteps).
 template <int kRanks>
 struct EntryIndex {
   using type = int64_t;
@@ -368,61 +368,104 @@ __global__ void __launch_bounds__(kPlanThreads)
 
 // ---- reserve: the pages of the next tokens -------------------------------------------------------
 static size_t reserve_smem(const tv_shape* s) {
-  return ((size_t)2 * s->n_pool_pages + (size_t)s->B) * 4;
+  return ((size_t)2 * s->n_pool_pages + (size_t)2 * s->B) * 4;
 }
+
+// A round needs a page or two per request, which its thread looks at; a prompt's pages are looked at
+// by the thread's warp.
+constexpr int kShortWindow = 4;
 
 template <int kRanks>
 __global__ void __launch_bounds__(kPlanThreads)
     reserve_kernel(const PlanArgs a, const int32_t* need) {
   pdl_wait();
   extern __shared__ __align__(16) int32_t smem_ints[];
-  const int rank = plan_rank<kRanks>(), tid = threadIdx.x;
+  const int rank = plan_rank<kRanks>(), tid = threadIdx.x, lane = tid & 31;
   const Range mine = share_of<kRanks>(a.B, rank);
   const int P = a.page_tokens, G = a.max_pages;
   SharedInts ints = {smem_ints};
   int32_t* refs = ints.take<kRanks>(a.refs, a.n_pool);
   int32_t* list = ints.take<kRanks>(a.w.list, a.n_pool);
   int32_t* pages = ints.take<kRanks>(a.w.pages, a.B);
+  int32_t* first = ints.take<kRanks>(a.w.from, a.B);
   if constexpr (kRanks == 1)
     for (int p = tid; p < a.n_pool; p += kPlanThreads) refs[p] = a.refs[p];
-  // unmapped pages of the positions L .. L + need - 1
-  for (int b = mine.lo + tid; b < mine.hi; b += kPlanThreads) {
-    const int n = need[b], L = a.L[b];
-    int missing = 0;
-    if (n > 0) {
-      if (L < 0) {
-        record_error(a.status, TV_ERR_ARG);
-      } else if ((int64_t)L + n > a.raw_cap) {
-        record_error(a.status, TV_ERR_CAPACITY);
-      } else {
-#pragma unroll 4
-        for (int g = L / P; g <= (L + n - 1) / P; ++g) {
-          const int p = a.table[(int64_t)b * G + g];
-          if (p == -1)
-            ++missing;
-          else if (!in_pool(a, p))
-            record_error(a.status, TV_ERR_ARG);
+  // f(request, first page, last page, whole warp) for the CTA's requests; a warp's lanes pass their own
+  // windows (lo > hi: none), which are called one by one for the whole warp where they are long
+  auto windows = [&](int b, int lo, int hi, auto f) {
+    const bool is_long = hi - lo >= kShortWindow;
+    if (lo <= hi && !is_long) f(b, lo, hi, false);
+    for (unsigned m = __ballot_sync(0xffffffffu, is_long); m; m &= m - 1) {
+      const int q = __ffs(m) - 1;
+      f(__shfl_sync(0xffffffffu, b, q), __shfl_sync(0xffffffffu, lo, q),
+        __shfl_sync(0xffffffffu, hi, q), true);
+    }
+  };
+  // 1. unmapped pages of the positions L .. L + need - 1
+  const int steps = (mine.hi - mine.lo + kPlanThreads - 1) / kPlanThreads;
+  for (int k = 0; k < steps; ++k) {
+    const int b = mine.lo + k * kPlanThreads + tid;
+    int lo = 0, hi = -1;
+    if (b < mine.hi) {
+      const int n = need[b], L = a.L[b];
+      if (n > 0) {
+        if (L < 0) {
+          record_error(a.status, TV_ERR_ARG);
+        } else if ((int64_t)L + n > a.raw_cap) {
+          record_error(a.status, TV_ERR_CAPACITY);
+        } else {
+          lo = L / P;
+          hi = (L + n - 1) / P;
         }
       }
+      pages[b] = 0;
     }
-    pages[b] = missing;
+    windows(b, lo, hi, [&](int q, int g0, int g1, bool warp) {
+      int missing = 0;
+      for (int g = g0 + (warp ? lane : 0); g <= g1; g += warp ? 32 : 1) {
+        const int p = a.table[(int64_t)q * G + g];
+        if (p == -1)
+          ++missing;
+        else if (!in_pool(a, p))
+          record_error(a.status, TV_ERR_ARG);
+      }
+      if (warp) missing = __reduce_add_sync(0xffffffffu, missing);
+      if (b == q) pages[q] = missing;   // (the request's own thread)
+    });
   }
   __syncthreads();
+  // 2. the lowest free pages, in the order of requests and positions
   auto pages_of = [&](int b) { return pages[b]; };
   int start, total;
   if (!list_free_pages<kRanks>(a, rank, refs, list, block_count(mine, pages_of), &start, &total))
     return;
   if (total == 0) return;
-  block_place(mine, start, pages_of, [&](int b, int at) {
-    const int L = a.L[b], n = need[b];
-    for (int g = L / P; g <= (L + n - 1) / P; ++g) {
-      int32_t* e = &a.table[(int64_t)b * G + g];
-      if (*e != -1) continue;
-      const int page = list[at++];
-      *e = page;
-      a.refs[page] = 1;
+  block_place(mine, start, pages_of, [&](int b, int at) { first[b] = at; });
+  __syncthreads();
+  for (int k = 0; k < steps; ++k) {
+    const int b = mine.lo + k * kPlanThreads + tid;
+    int lo = 0, hi = -1;
+    if (b < mine.hi && pages[b] > 0) {
+      const int L = a.L[b];
+      lo = L / P;
+      hi = (L + need[b] - 1) / P;
     }
-  });
+    windows(b, lo, hi, [&](int q, int g0, int g1, bool warp) {
+      int at = first[q];
+      for (int g = g0; g <= g1; g += warp ? 32 : 1) {
+        const int mine_g = warp ? g + lane : g;
+        int32_t* e = &a.table[(int64_t)q * G + mine_g];
+        const bool missing = mine_g <= g1 && *e == -1;
+        const unsigned m = warp ? __ballot_sync(0xffffffffu, missing) : 0u;
+        if (missing) {
+          const int page = list[at + __popc(m & ((1u << lane) - 1u))];
+          *e = page;
+          a.refs[page] = 1;
+        }
+        at += warp ? __popc(m) : missing ? 1 : 0;
+      }
+    });
+  }
 }
 
 // ---- compaction ----------------------------------------------------------------------------------
@@ -644,13 +687,14 @@ static int launch_copy(const char* fn, const tv_shape* s, const PlanArgs& p, voi
   return e == cudaSuccess ? tv_check_launch(fn) : launch_error(fn, e);
 }
 
-// Launches a plan: one CTA where the state is small enough (a serving batch's fork 5 us against 11 us on
-// the cluster), else the cluster.
+// Launches a plan: one CTA where the state is small, else the cluster.  Measured (us, one CTA and
+// cluster; slots x pages per slot, pool): fork 64 x 9, 400: 6.8 and 11.3; 64 x 32, 2048: 9.0 and 11.0;
+// 256 x 32, 4096: 18.2 and 11.8.  compact 64 x 32, 2048: 6.3 and 10.6; 256 x 32, 4096: 10.9 and 10.4.
+// reserve 64 slots, 400 pages: 3.0 and 4.4; 1024 slots, 8192 pages: 3.9 and 4.5.
 template <typename... KArgs, typename... Args>
-static int launch_plan(const char* fn, const tv_shape* s, void (*one)(KArgs...),
+static int launch_plan(const char* fn, const tv_shape* s, int64_t steps, void (*one)(KArgs...),
                        void (*cluster)(KArgs...), size_t smem, cudaStream_t stream, Args... args) {
-  const bool single = s->n_pool_pages <= kOnePages && s->B <= kOneRequests &&
-                      (int64_t)s->B * s->max_pages <= kOneEntries;
+  const bool single = s->n_pool_pages <= kOnePages && steps <= kOneSteps;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(single ? 1 : kPlanRanks);
   cfg.blockDim = dim3(kPlanThreads);
@@ -680,8 +724,8 @@ int tv_launch_fork(const tv_shape* s, const int32_t* source, const int32_t* keep
                    int32_t* status, cudaStream_t stream) {
   const char* fn = "tv_pages_fork";
   const tv::PlanArgs a = tv::plan_args(s, L, refs, workspace, status);
-  if (int rc = tv::launch_plan(fn, s, tv::fork_plan_kernel<1>, tv::fork_plan_kernel<tv::kPlanRanks>,
-                               tv::fork_smem(s), stream, a, L, source, keep))
+  if (int rc = tv::launch_plan(fn, s, (int64_t)s->B * s->max_pages, tv::fork_plan_kernel<1>,
+                               tv::fork_plan_kernel<tv::kPlanRanks>, tv::fork_smem(s), stream, a, L, source, keep))
     return rc;
   return tv::launch_copy(fn, s, a, pools, keys, d_idx, source, stream);
 }
@@ -689,7 +733,7 @@ int tv_launch_fork(const tv_shape* s, const int32_t* source, const int32_t* keep
 int tv_launch_reserve(const tv_shape* s, const int32_t* need, const int32_t* L, int32_t* refs,
                       void* workspace, int32_t* status, cudaStream_t stream) {
   const tv::PlanArgs a = tv::plan_args(s, L, refs, workspace, status);
-  return tv::launch_plan("tv_pages_reserve", s, tv::reserve_kernel<1>,
+  return tv::launch_plan("tv_pages_reserve", s, s->B, tv::reserve_kernel<1>,
                          tv::reserve_kernel<tv::kPlanRanks>, tv::reserve_smem(s), stream, a, need);
 }
 
@@ -698,7 +742,7 @@ int tv_launch_compact(const tv_shape* s, const int32_t* L, int32_t* refs, void* 
                       cudaStream_t stream) {
   const char* fn = "tv_pages_compact";
   const tv::PlanArgs a = tv::plan_args(s, L, refs, workspace, status);
-  if (int rc = tv::launch_plan(fn, s, tv::compact_plan_kernel<1>,
+  if (int rc = tv::launch_plan(fn, s, (int64_t)s->B * s->max_pages, tv::compact_plan_kernel<1>,
                                tv::compact_plan_kernel<tv::kPlanRanks>, tv::compact_smem(s), stream,
                                a, remap, n_live))
     return rc;
