@@ -130,3 +130,18 @@ def test_binding_refuses_another_device(monkeypatch):
     t = _OnDevice()
     with pytest.raises(ValueError, match="another device"):
         _lib.tv_pages_reserve(_pages_shape(), t, t, t, t, t)
+
+
+def test_managed_pool_maps_what_the_prefixes_cover(lib):
+    from tree_speculative_verify_gb300 import engine, workloads
+    wl = workloads.make_workload("pool", B=3, D=4, H=2, d=64, W=128, tail_mode="window", ms=(4, 128),
+                                 dtype="f32", L=(100, 1300), k=2, steps=3, p_match=0.5, seed=3, kv_scale=0.5)
+    wl.L[:] = (0, 512, 1025)
+    shape, st = engine.alloc_pool(wl, 512, 6, device="cpu")
+    G = shape.max_pages
+    assert st.page_table.tolist() == [[-1] * G, [0] + [-1] * (G - 1), [1, 2, 3] + [-1] * (G - 3)]
+    assert st.page_refs.tolist() == [1, 1, 1, 1, 0, 0]
+    assert st.page_ws.numel() == lib.tv_pages_workspace_size(ctypes.byref(shape)) > 0
+    assert torch.equal(st.rawK[3, :1], wl.rawK[2, 1024:1025]) and not st.rawK[3, 1:].any()
+    with pytest.raises(ValueError):
+        engine.alloc_pool(wl, 512, 3, device="cpu")

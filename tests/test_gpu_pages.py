@@ -388,3 +388,46 @@ def test_round_without_free_pages_commits_nothing_it_has_no_page_for():
 
 def _lib_code(name):
     return next(c for c, n in _lib.TV_ERR.items() if n == name)
+
+
+def test_calls_right_behind_the_acceptance_walk_see_its_results():
+    # the walk allows the kernel behind it to start early and stores its results only after the
+    # attention in front of it has completed: whatever reads them must have waited for the walk
+    wl = workloads.serving(B=40, L=(2048, 2048))
+    shape, st = engine.alloc_pool(wl, 512, 400)
+    rb = engine.alloc_round(wl, shape)
+    engine.prefill(shape, st, rb)
+    engine.plan(shape, st, rb)
+    engine.branch_compress(shape, st, rb)
+    logits = torch.randn((40, 1, 40000), generator=torch.Generator(device="cuda").manual_seed(1),
+                         device="cuda")
+    one = _lib.make_shape(B=40, D=1, H=1, d=8, comp_mask=1)
+    lp, lse = (torch.empty((40, 1), device="cuda") for _ in range(2))
+    stay = torch.arange(40, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+
+    def walk():
+        for t in (rb.accept_len, rb.bonus):
+            t.zero_()
+        torch.cuda.synchronize()
+        engine.attention(shape, st, rb)
+        engine.accept(shape, st, rb)
+
+    walk()
+    engine.reserve(shape, st, rb, need=rb.accept_len)
+    torch.cuda.synchronize()
+    n = rb.accept_len.clone()
+    assert int(rb.status.item()) == 0 and int(n.min()) >= 1
+    assert bool((st.page_table[:, 4] >= 0).all())       # position 2048 lies on the fifth page
+    walk()
+    _lib.tv_token_logprobs(one, logits, rb.bonus.view(40, 1), None, 1.0, lse, None, lp, None, None, None,
+                           rb.status)
+    torch.cuda.synchronize()
+    want = torch.log_softmax(logits.double(), 2).gather(2, rb.bonus.long().view(40, 1, 1))[..., 0]
+    assert bool((rb.bonus != 0).any()) and float((lp - want).abs().max()) < 1e-4
+    walk()
+    engine.fork(shape, st, rb, stay, keep=rb.accept_len)
+    torch.cuda.synchronize()
+    assert int(rb.status.item()) == 0 and torch.equal(st.L, n)
+    refs = torch.bincount((st.page_table[st.page_table >= 0]).long(), minlength=400)
+    assert torch.equal(refs.int(), st.page_refs) and int((st.page_table >= 0).sum()) == 40
