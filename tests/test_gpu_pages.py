@@ -431,3 +431,26 @@ def test_calls_right_behind_the_acceptance_walk_see_its_results():
     assert int(rb.status.item()) == 0 and torch.equal(st.L, n)
     refs = torch.bincount((st.page_table[st.page_table >= 0]).long(), minlength=400)
     assert torch.equal(refs.int(), st.page_refs) and int((st.page_table >= 0).sum()) == 40
+
+
+def test_round_graph_on_a_managed_pool():
+    # replayed rounds map their pages, commit and move on like rounds called one by one
+    wl = workloads.serving(B=5, L=(500, 900))
+    runs = []
+    for graphed in (False, True):
+        shape, st = engine.alloc_pool(wl, 512, 24)
+        rb = engine.alloc_round(wl, shape)
+        engine.alloc_scores(rb, shape, workloads.VOCAB, n_top=2)
+        engine.prefill(shape, st, rb)
+        rb.logits.normal_(generator=torch.Generator(device="cuda").manual_seed(9))
+        graph = engine.RoundGraph(shape, st, rb, scored=True) if graphed else None
+        for _ in range(8):
+            graph.replay() if graphed else engine.verify_round(shape, st, rb, scored=True)
+        torch.cuda.synchronize()
+        assert int(rb.status.item()) == 0
+        view = st.page_table.long().clamp(min=0)
+        runs.append([st.L, st.page_table, st.page_refs, rb.O, rb.target, rb.top_ids, rb.committed]
+                    + [getattr(st, k)[view] for m in MS for k in MS[m]])
+    assert int((runs[0][0].cpu() - torch.as_tensor(wl.L)).min()) >= 8
+    for a, b in zip(*runs):
+        assert torch.equal(a, b)
