@@ -104,7 +104,8 @@ BF, F32 = torch.bfloat16, torch.float32
     (2, 8, 2049, 7, F32, 8, 8, 1.0), (3, 5, 4097, 2, BF, 20, 100, 1.0), (1, 1, 8191, 0, F32, 31, 3, 1.0),
     (1, 7, 16383, 0, BF, 32, 7, 1.3), (8, 8, 32000, 0, BF, 8, 8, 1.0), (2, 3, 50001, 2, BF, 5, 7, 1.25),
     (40, 8, 1024, 0, BF, 4, 8, 1.0), (1, 1, 131075, 0, BF, 32, 1, 1.0), (1, 2, 262144, 0, F32, 10, 1024, 0.6),
-    (200, 1, 3001, 0, BF, 2, 1, 1.0), (1, 6, 200000, 0, F32, 32, 6, 1.0),
+    (200, 1, 3001, 0, BF, 2, 1, 1.0), (1300, 1, 1501, 1, F32, 8, 1, 1.0),
+    (160, 8, 2600, 3, BF, 32, 8, 1.1), (1217, 1, 70, 0, F32, 5, 1, 1.0), (620, 1, 9001, 0, F32, 20, 1, 1.0), (1, 6, 200000, 0, F32, 32, 6, 1.0),
 ])
 def test_rows_match_oracle(B, D, V, pad, dtype, K, n_tok, scale):
     x = _logits(B, D, V, dtype, seed=V + B, pad=pad)
@@ -153,9 +154,10 @@ def test_masked_rows(V, dtype):
     assert (want["top_ids"][0, 1] >= 0).sum() == 1
 
 
-@pytest.mark.parametrize("dtype", [BF, F32])
-def test_ties_and_orders_that_defeat_a_threshold(dtype):
-    V = 20011
+@pytest.mark.parametrize("dtype,copies,V", [(BF, 1, 20011), (F32, 1, 20011), (BF, 60, 20011),
+                                            (BF, 140, 9011), (F32, 140, 5011)])
+def test_ties_and_orders_that_defeat_a_threshold(dtype, copies, V):
+    # (many copies of the rows: the thread counts that many rows take)
     x = torch.zeros((1, 9, V), dtype=dtype, device="cuda")
     ramp = torch.arange(V, device="cuda").float()
     x[0, 0] = 0.0                                        # all equal
@@ -169,10 +171,16 @@ def test_ties_and_orders_that_defeat_a_threshold(dtype):
     x[0, 6, 100:4000] = 2.0                              # a run of ties within one stretch
     x[0, 7] = torch.randint(0, 3, (V,), generator=torch.Generator().manual_seed(1)).to(dtype).cuda()
     x[0, 8] = torch.finfo(dtype).min
+    many = x.expand(copies, 9, V).contiguous()
     for K in (0, 1, 5, 32):
-        got, status = _run(x, n_top=K)
+        got, status = _run(many, n_top=K)
         assert status == 0
-        _check(x, got, n_top=K)
+        # copies start at other alignments: the same ids, and sums within the same tolerances
+        for b in sorted({0, copies // 2, copies - 1}):
+            _check(x, {k: v[b:b + 1] for k, v in got.items()}, n_top=K)
+        for k in ("target", "top_ids"):
+            if k in got:
+                assert np.array_equal(got[k], np.broadcast_to(got[k][:1], got[k].shape))
 
 
 def test_nan_and_inf_rows_are_reported_and_the_others_are_right():

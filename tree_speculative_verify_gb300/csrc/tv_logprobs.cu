@@ -207,7 +207,8 @@ struct LpShared {
   };
   Partial warp_part[kWarps];
   uint64_t top[kLpMaxTop];         // largest keys, descending (0: none)
-  uint32_t largest[32];            // the warps' largest threads (kth_bound)
+  alignas(16) uint32_t orders[kThreads];   // threads' largest logits (kth_bound)
+  uint32_t kth;
   int count, hits, columns;
   uint64_t scan[kWarps];
   // rank 0's, written by the CTAs of the cluster: their shares of the row and their top lists
@@ -217,38 +218,63 @@ struct LpShared {
 };
 static_assert(kLpMaxRanks * kLpMaxTop <= kLpCand, "every CTA's keys fit into cand");
 
-// Lower bound (as an order) of the K-th largest logit that the CTA has seen: the K-th largest among
-// the 32 / warps (at most K) largest threads of every warp, m being a thread's largest logit.  The
-// order of the lowest finite value where those are fewer than K.
+// The K-th largest of the threads' orders o: every thread counts its place among all.
+template <int kThreads, bool kCluster>
+__device__ __noinline__ uint32_t kth_of_all(LpShared<kThreads, kCluster>& sm, uint32_t o, int K) {
+  sm.orders[threadIdx.x] = o;
+  __syncthreads();
+  const uint4* all = reinterpret_cast<const uint4*>(sm.orders);
+  int place = 0;
+#pragma unroll 4
+  for (int j = 0; j < kThreads / 4; ++j) {
+    const uint4 x = all[j];
+    const int d = (int)threadIdx.x - 4 * j;   // equal orders: threads in front count
+    place += (x.x > o || (x.x == o && d > 0)) + (x.y > o || (x.y == o && d > 1)) +
+             (x.z > o || (x.z == o && d > 2)) + (x.w > o || (x.w == o && d > 3));
+  }
+  if (place == K - 1) sm.kth = o;
+  __syncthreads();
+  return sm.kth;
+}
+
+// Lower bound (as an order) of the K-th largest logit that the CTA has seen, m being a thread's
+// largest; the order of the lowest finite value where there are fewer.  It is the K-th largest among
+// the 32 / warps largest threads of every warp, which for K up to 32 / warps is the K-th largest
+// thread.  For more alternatives 128 threads count all of their places instead (512 rows of 32000
+// bf16 logits, 32 alternatives: 16.8 us without, 14.4 us with), 256 threads do not (256 rows of
+// 128000 fp32 logits, 20 alternatives: 25.1 us without, 27.6 us with).
 template <int kThreads, bool kCluster>
 __device__ __forceinline__ uint32_t kth_bound(LpShared<kThreads, kCluster>& sm, float m, int K) {
   constexpr int kWarps = kThreads / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   constexpr int per = 32 / kWarps;
-  uint32_t o = order_of(m);
-#pragma unroll 1
-  for (int i = 0; i < per; ++i) {
-    uint32_t w = 0u;
-    if (i < K) {
-      w = __reduce_max_sync(0xffffffffu, o);
-      const uint32_t at = __ballot_sync(0xffffffffu, o == w);
-      if (lane == __ffs(at) - 1) o = 0u;
-    }
-    if (lane == 0) sm.largest[i * kWarps + warp] = w;
-  }
-  __syncthreads();
-  const uint32_t v = sm.largest[lane];
-  uint32_t t;
-  if (K == 1) {
-    t = __reduce_max_sync(0xffffffffu, v);
+  uint32_t o = order_of(m), t;
+  if (kThreads <= 128 && K > per) {
+    t = kth_of_all(sm, o, K);
   } else {
-    int place = 0;
-#pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      const uint32_t x = __shfl_sync(0xffffffffu, v, j);
-      place += x > v || (x == v && j < lane) ? 1 : 0;
+#pragma unroll 1
+    for (int i = 0; i < per; ++i) {
+      uint32_t w = 0u;
+      if (i < K) {
+        w = __reduce_max_sync(0xffffffffu, o);
+        const uint32_t at = __ballot_sync(0xffffffffu, o == w);
+        if (lane == __ffs(at) - 1) o = 0u;
+      }
+      if (lane == 0) sm.orders[i * kWarps + warp] = w;
     }
-    t = __reduce_max_sync(0xffffffffu, place == K - 1 ? v : 0u);
+    __syncthreads();
+    const uint32_t v = sm.orders[lane];
+    if (K == 1) {
+      t = __reduce_max_sync(0xffffffffu, v);
+    } else {
+      int place = 0;
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        const uint32_t x = __shfl_sync(0xffffffffu, v, j);
+        place += x > v || (x == v && j < lane) ? 1 : 0;
+      }
+      t = __reduce_max_sync(0xffffffffu, place == K - 1 ? v : 0u);
+    }
   }
   return max(t, kOrderLowest);
 }
@@ -306,18 +332,8 @@ __device__ __noinline__ int list_with_ties(LpShared<kThreads, kCluster>& sm, con
   constexpr int kVec = Row<T>::kVec;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   __syncthreads();
-  uint32_t* orders = reinterpret_cast<uint32_t*>(sm.list.hit);
-  const uint32_t mine = order_of(m);
-  orders[tid] = mine;
   if (tid == 0) sm.count = 0;
-  __syncthreads();
-  int place = 0;
-#pragma unroll 8
-  for (int q = 0; q < kThreads; ++q)
-    place += orders[q] > mine || (orders[q] == mine && q < tid) ? 1 : 0;
-  if (place == K - 1) sm.largest[0] = mine;
-  __syncthreads();
-  const float bound = logit_of_order(max(sm.largest[0], kOrderLowest));
+  const float bound = logit_of_order(max(kth_of_all(sm, order_of(m), K), kOrderLowest));
   int ties = 0;   // found so far, the same in every thread
   for (int i0 = lo; i0 < hi; i0 += kThreads) {
     const int i = i0 + tid;
@@ -717,7 +733,10 @@ static cudaError_t launch_logprobs(const T* logits, const LogprobArgs& a, int64_
   if (ranks > 1) return launch_kernel<T, 256, true>(logits, a, rows, ranks, stream);
   // many rows fill the SMs with small CTAs, whose ends cost less (512 rows of 2048 bf16 logits: 6.1
   // us with 128 threads, 7.3 us with 256); fewer rows want more loads in flight per row (256 rows of
-  // 128000 fp32 logits: 31.5 and 25.3 us)
+  // 128000 fp32 logits: 31.5 and 25.3 us); very many short rows take two warps each (1372 rows of
+  // 2875 fp32 logits: 8.7 us with 64 threads, 11.4 us with 128; 4096 of 16000 bf16: 34.6 and 38.0;
+  // but 512 rows of 8000 bf16: 7.7 and 6.9)
+  if (rows >= 8 * 152 && vecs <= 2048) return launch_kernel<T, 64, false>(logits, a, rows, 1, stream);
   return rows >= 512 ? launch_kernel<T, 128, false>(logits, a, rows, 1, stream)
                      : launch_kernel<T, 256, false>(logits, a, rows, 1, stream);
 }
