@@ -454,3 +454,65 @@ def test_round_graph_on_a_managed_pool():
     assert int((runs[0][0].cpu() - torch.as_tensor(wl.L)).min()) >= 8
     for a, b in zip(*runs):
         assert torch.equal(a, b)
+
+
+def test_branch_on_the_sparse_path_selects_what_its_source_selects():
+    # the fork carries the indexer keys: with the same queries, tokens and tree the branch's round is
+    # its source's, from the device selection to the committed rows
+    wl = workloads.long_context(B=3, L=(9000, 12000), n_sel=512)
+    shape, st = engine.alloc_pool(wl, 2048, 24)
+    rb = engine.alloc_round(wl, shape)
+    engine.prefill(shape, st, rb)
+    for t in (rb.Q, rb.treeK, rb.treeV, rb.parents, rb.draft, rb.target, rb.q_idx):
+        t[2] = t[0]
+    before = st.k_idx.clone()
+    engine.fork(shape, st, rb, torch.tensor([0, 1, 0], dtype=torch.int32).cuda())
+    engine.verify_round(shape, st, rb, select=True)
+    torch.cuda.synchronize()
+    assert int(rb.status.item()) == 0
+    n = int(wl.L[0]) // 4
+    assert torch.equal(st.k_idx[2, :n], before[0, :n]) and torch.equal(st.k_idx[2, n:], before[2, n:])
+    for name in ("sel", "O", "lse", "accept_len", "path", "bonus", "committed"):
+        t = getattr(rb, name)
+        assert torch.equal(t[2], t[0]), name
+    assert int(st.L[2]) == int(st.L[0]) > int(wl.L[0])
+    table = st.page_table.long()
+    for m in MS:
+        for name in MS[m]:
+            rows = [getattr(st, name)[table[b].clamp(min=0)].reshape(-1, wl.d)[:int(st.L[0]) // m] for b in (0, 2)]
+            assert torch.equal(*rows), name
+
+
+def test_calls_on_two_streams_at_once():
+    # two pools, each with its own workspace, and two batches of logits, on two streams
+    P = 512
+    rng = np.random.default_rng(8)
+    pools = []
+    for k in range(2):
+        L = [int(x) for x in rng.integers(1, 3 * P, size=40)]
+        pools.append(Pool(_random_table(rng, 40, 5, 400, L, P), L, 400, P, d=64, seed=k))
+    x = [torch.randn((1, 30, 60000), generator=torch.Generator(device="cuda").manual_seed(k), device="cuda")
+         for k in range(2)]
+    f = lambda: torch.empty((1, 30), device="cuda")
+    out = [(f(), f(), torch.empty((1, 30, 9), dtype=torch.int32, device="cuda"),
+            torch.empty((1, 30, 9), device="cuda")) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    shape = _lib.make_shape(B=1, D=30, H=1, d=8, comp_mask=1)
+    src = [[b - b % 3 for b in range(40)], [b - b % 5 for b in range(40)]]
+    src_t = [torch.tensor(s, dtype=torch.int32).cuda() for s in src]
+    need = torch.full((40,), 700, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for k, s in enumerate(pools):
+            st = streams[k]
+            _lib.tv_pages_fork(s.shape, src_t[k], None, s.L, s.refs, *s.layers(), None, s.ws, s.status, st)
+            _lib.tv_token_logprobs(shape, x[k], None, None, 1.0, out[k][0], out[k][1], None, out[k][2],
+                                   out[k][3], None, s.status, st)
+            _lib.tv_pages_reserve(s.shape, need, s.L, s.refs, s.ws, s.status, st)
+            _lib.tv_pages_compact(s.shape, s.L, s.refs, *s.layers(), s.remap, s.n_live, s.ws, s.status, st)
+    torch.cuda.synchronize()
+    for k, s in enumerate(pools):
+        for _ in range(3):
+            codes = [pages.fork(s.o, P, src[k]), pages.reserve(s.o, P, [700] * 40), pages.compact(s.o, P)[0]]
+        s.check(codes)
+        assert torch.equal(out[k][2], torch.topk(x[k], 9, dim=2).indices.int())
