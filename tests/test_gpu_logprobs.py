@@ -365,3 +365,26 @@ def test_scored_round_feeds_the_acceptance_walk():
     want = oracle.token_logprobs(rb2.logits.float().cpu().numpy(), wl.draft, wl.parents)
     err = np.abs(rb2.draft_logprobs.cpu().numpy() - want["logprobs"]).max()
     assert err <= _dS(workloads.VOCAB) + 5 * U * (np.abs(want["logprobs"]).max() + 12)
+
+
+@pytest.mark.parametrize("V", [900, 20011, 400000])
+@pytest.mark.parametrize("scale,at", [(1.0, 6931.4487), (1.0, -6931.4487), (100.0, 69.31449),
+                                      (100.0, -69.31449), (0.001, 6931448.7)])
+def test_logits_on_both_sides_of_the_far_exponents(V, scale, at):
+    # comparable weights whose scaled logits lie a few tenths of a nat to either side of where the
+    # exponents take their far form (|logit * scale * log2 e| = 10^4): in one thread, in different
+    # threads and in different CTAs of a row (400000 logits), the larger one first and last
+    x = torch.full((1, 8, V), at - 300.0 / scale, dtype=F32, device="cuda")
+    near, far = at - 0.19 / scale, at + 0.23 / scale
+    gaps = (1, 4, 130, 4096 % V, V // 2, V - 9, 517, 8)
+    for r, gap in enumerate(gaps):
+        lo, hi = (near, far) if r % 2 else (far, near)
+        first = 4 if gap + 8 < V else 0
+        x[0, r, first] = lo
+        x[0, r, first + gap] = hi
+        x[0, r, (first + gap + 2) % V] = at + 0.01 / scale
+    tokens = np.array([[4, 5, 8, 4 + gaps[2], 4 + gaps[3], 4 + gaps[4], 0, 4]], dtype=np.int32)
+    nodes = np.array([[0, 0, 1, 2, 3, 4, 5, 7]], dtype=np.int32)
+    got, status = _run(x, tokens, nodes, scale, 3)
+    assert status == 0
+    _check(x, got, tokens, nodes, scale, 3)
