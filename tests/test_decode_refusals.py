@@ -145,3 +145,26 @@ def test_managed_pool_maps_what_the_prefixes_cover(lib):
     assert torch.equal(st.rawK[3, :1], wl.rawK[2, 1024:1025]) and not st.rawK[3, 1:].any()
     with pytest.raises(ValueError):
         engine.alloc_pool(wl, 512, 3, device="cpu")
+
+
+def test_copy_of_a_managed_pool_shares_nothing(lib):
+    from dataclasses import fields
+    from tree_speculative_verify_gb300 import engine, workloads
+    wl = workloads.make_workload("pool", B=2, D=4, H=2, d=64, W=128, tail_mode="window", ms=(4, 128),
+                                 dtype="f32", L=(100, 1300), k=2, steps=3, p_match=0.5, seed=3, kv_scale=0.5)
+    wl.k_idx = torch.randn((2, wl.cap4, 64)).bfloat16()
+    shape, st = engine.alloc_pool(wl, 512, 12, device="cpu")
+    with pytest.raises(ValueError, match="clone_pool"):
+        st.clone()
+    cshape, copy = engine.clone_pool(shape, st)
+    for f in fields(st):
+        a, b = getattr(st, f.name), getattr(copy, f.name)
+        assert a.untyped_storage().data_ptr() != b.untyped_storage().data_ptr(), f.name
+        if f.name != "page_ws":
+            assert torch.equal(a, b), f.name
+    assert shape.page_table == st.page_table.data_ptr()
+    assert cshape.page_table == copy.page_table.data_ptr()
+    assert all(getattr(shape, n) == getattr(cshape, n) for n, _ in shape._fields_ if n != "page_table")
+    # a state without counts keeps sharing what a round only reads
+    pshape, paged = engine.alloc_paged(wl, 512, device="cpu")
+    assert paged.clone().page_table is paged.page_table

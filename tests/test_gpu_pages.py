@@ -516,3 +516,28 @@ def test_calls_on_two_streams_at_once():
             codes = [pages.fork(s.o, P, src[k]), pages.reserve(s.o, P, [700] * 40), pages.compact(s.o, P)[0]]
         s.check(codes)
         assert torch.equal(out[k][2], torch.topk(x[k], 9, dim=2).indices.int())
+
+
+def test_copied_pool_goes_its_own_way():
+    # branching, compaction and rounds on one of the two leave the other's rounds as they are
+    wl = workloads.serving(B=4, L=(500, 1400))
+    shape, st = engine.alloc_pool(wl, 512, 30)
+    rb = engine.alloc_round(wl, shape)
+    engine.prefill(shape, st, rb)
+    cshape, copy = engine.clone_pool(shape, st)
+    want_shape, want = engine.clone_pool(shape, st)
+    wrb, crb = engine.alloc_round(wl, shape), engine.alloc_round(wl, shape)
+    engine.verify_round(want_shape, want, wrb)
+    remap = torch.empty(30, dtype=torch.int32, device="cuda")
+    n_live = torch.empty(1, dtype=torch.int32, device="cuda")
+    engine.fork(shape, st, rb, torch.tensor([0, -1, 0, 0], dtype=torch.int32).cuda())
+    engine.compact(shape, st, rb, remap, n_live)
+    engine.verify_round(shape, st, rb)
+    engine.verify_round(cshape, copy, crb)
+    torch.cuda.synchronize()
+    assert [int(r.status.item()) for r in (rb, wrb, crb)] == [0, 0, 0]
+    for name in ("L", "page_table", "page_refs", "rawK", "c4V", "c128K"):
+        assert torch.equal(getattr(copy, name), getattr(want, name)), name
+    for name in ("O", "lse", "committed"):
+        assert torch.equal(getattr(crb, name), getattr(wrb, name)), name
+    assert not torch.equal(st.page_table, copy.page_table)

@@ -10,7 +10,7 @@ library; PyTorch only allocates memory.
 """
 
 import math
-from dataclasses import dataclass
+from dataclasses import dataclass, fields
 
 import torch
 
@@ -47,10 +47,14 @@ class DeviceState:
     page_ws: torch.Tensor = None      # workspace of the tv_pages_* calls (managed pools only)
 
     def clone(self):
+        """A copy of the cache.  The indexer keys and the page table, which a round only reads, stay
+        shared; of a managed pool, whose calls write both, ``clone_pool`` makes the copy."""
+        if self.page_refs is not None:
+            raise ValueError("the copy of a managed pool needs a shape with its own page table: "
+                             "use engine.clone_pool(shape, state)")
         return DeviceState(*(t.clone() for t in (self.rawK, self.rawV, self.c4K, self.c4V,
                                                  self.c128K, self.c128V, self.L)),
-                           k_idx=self.k_idx, page_table=self.page_table,
-                           page_refs=self.page_refs, page_ws=self.page_ws)
+                           k_idx=self.k_idx, page_table=self.page_table)
 
 
 @dataclass
@@ -184,6 +188,15 @@ def alloc_pool(wl, page_tokens, n_pool_pages, attn_kernel=_lib.TV_ATTN_AUTO, sta
     shape.page_table = st.page_table.data_ptr()
     st.page_ws = torch.empty(_lib.tv_pages_workspace_size(shape), dtype=torch.uint8, device=device)
     return shape, st
+
+
+def clone_pool(shape, st):
+    """A copy of a managed pool that shares nothing with it: (shape, state)."""
+    copy = DeviceState(**{f.name: None if getattr(st, f.name) is None else getattr(st, f.name).clone()
+                          for f in fields(st)})
+    new = _lib.tv_shape.from_buffer_copy(shape)
+    new.page_table = copy.page_table.data_ptr()
+    return new, copy
 
 
 def alloc_scores(rb, shape, vocab, n_top=8, dtype=torch.bfloat16, device="cuda"):
