@@ -388,3 +388,40 @@ def test_logits_on_both_sides_of_the_far_exponents(V, scale, at):
     got, status = _run(x, tokens, nodes, scale, 3)
     assert status == 0
     _check(x, got, tokens, nodes, scale, 3)
+
+
+@pytest.mark.parametrize("B", [1, 12])
+def test_acceptance_walk_takes_the_targets_of_the_call_in_front(B):
+    # other logits before every round, and targets left over that no draft token equals: the walk
+    # follows what the call just in front of it has written, called one by one and replayed
+    wl = workloads.serving(B=B, L=(300, 900))
+    shape = engine.shape_for(wl)
+    st, rb = engine.alloc_state(wl), engine.alloc_round(wl, shape)
+    engine.prefill(shape, st, rb)
+    engine.alloc_scores(rb, shape, workloads.VOCAB, n_top=1)
+    L0 = st.L.clone()
+    graph = engine.RoundGraph(shape, st, rb, scored=True, prologue=lambda: st.L.copy_(L0))
+    rng = np.random.default_rng(B)
+    lengths = set()
+    for k in range(24):
+        want = rng.integers(0, workloads.VOCAB, size=(B, wl.D)).astype(np.int32)
+        for b in range(B):
+            for v in range(1, wl.D):       # half of the nodes lead on to one of their children
+                if rng.random() < 0.5:
+                    want[b, wl.parents[b, v]] = wl.draft[b, v]
+        logits = torch.zeros_like(rb.logits)
+        logits.scatter_(2, torch.as_tensor(want).cuda().long().unsqueeze(2), 9.0)
+        rb.logits.copy_(logits)
+        rb.target.fill_(-5)
+        st.L.copy_(L0)
+        torch.cuda.synchronize()
+        graph.replay() if k % 2 else engine.verify_round(shape, st, rb, scored=True)
+        torch.cuda.synchronize()
+        assert int(rb.status.item()) == 0
+        assert np.array_equal(rb.target.cpu().numpy(), want)
+        for b in range(B):
+            n, path, bonus = oracle.accept_walk(wl.parents[b], wl.draft[b], want[b])
+            assert int(rb.accept_len[b]) == n and int(rb.bonus[b]) == bonus
+            assert rb.path[b, :n].tolist() == list(path)[:n]
+            lengths.add(n)
+    assert len(lengths) > 1
