@@ -26,6 +26,11 @@
  *   writes anything, and before it completes.  A caller's kernel placed just before a call and
  *   itself allowing early starts (griddepcontrol.launch_dependents) must not write the call's
  *   inputs after that point.
+ *   Two calls read ahead of the call in front on contiguous caches: tv_branch_compress (L, parents,
+ *   treeK / treeV, raw rows) and tv_tree_verify_attn (L, Q, compressed entries, raw rows).  As in the
+ *   round's order, tv_build_ancestor_mask must come between the former and whatever last wrote what
+ *   it reads, and tv_branch_compress between the latter and the same.  With pages nothing is read
+ *   ahead, and no other call reads ahead.
  * - Errors found on the device (a malformed tree, a capacity overflow, a bad selection index,
  *   a wait that ran out) are written to the caller's int32 *status word with first-error-wins
  *   semantics (the word is only ever changed from 0 to a negative code); read it after the

@@ -541,3 +541,43 @@ def test_copied_pool_goes_its_own_way():
     for name in ("O", "lse", "committed"):
         assert torch.equal(getattr(crb, name), getattr(wrb, name)), name
     assert not torch.equal(st.page_table, copy.page_table)
+
+
+@pytest.mark.parametrize("call", ["fork", "reserve", "compact"])
+def test_scratch_pad_right_behind_a_pages_call_sees_its_results(call):
+    # no plan between them: the scratch pad reads lengths, page numbers and rows that the call in front
+    # writes, and stages rows on pages that it maps
+    wl = workloads.serving(B=24, L=(1021, 2046))
+    for k in range(6):
+        runs = []
+        for waits in (True, False):
+            shape, st = engine.alloc_pool(wl, 512, 200, stage_chain=1)
+            rb = engine.alloc_round(wl, shape)
+            engine.prefill(shape, st, rb)
+            remap = torch.empty(200, dtype=torch.int32, device="cuda")
+            n_live = torch.empty(1, dtype=torch.int32, device="cuda")
+            src = torch.arange(24, dtype=torch.int32, device="cuda")
+            keep = torch.tensor([509 + 3 * k + b for b in range(24)], dtype=torch.int32, device="cuda")
+            if call == "compact":      # two thirds of the slots go, the others' pages move down
+                drop = torch.where(src % 3 == 2, src, torch.full_like(src, -1))
+                engine.fork(shape, st, rb, drop)
+                rb.need.copy_(torch.where(drop >= 0, rb.need, 0))
+            if call != "reserve":
+                engine.reserve(shape, st, rb)
+            torch.cuda.synchronize()
+            if call == "fork":
+                engine.fork(shape, st, rb, torch.where(src % 4 == 3, src - 3, src), keep)
+            elif call == "reserve":
+                engine.reserve(shape, st, rb)
+            else:
+                engine.compact(shape, st, rb, remap, n_live)
+            if waits:
+                torch.cuda.synchronize()
+            engine.branch_compress(shape, st, rb)
+            torch.cuda.synchronize()
+            live = [b for b in range(24) if call != "compact" or b % 3 == 2]
+            table = st.page_table.long().clamp(min=0)
+            runs.append([t[live] for t in (rb.scrK4, rb.scrV4, rb.scrK128, rb.scrV128, st.L, st.page_table)]
+                        + [st.rawK[table[live]], st.c4K[table[live]]])
+        for a, b in zip(*runs):
+            assert torch.equal(a, b)

@@ -492,9 +492,9 @@ struct BranchSmem {
 template <typename T>
 __global__ void __cluster_dims__(kC128Ranks, 1, 1) __launch_bounds__(kThreads)
     branch_kernel(Paging pg, int D, int d, int comp_mask, int64_t raw_cap, T* rawK, T* rawV,
-                  int stage, int64_t c4_cap, T* c4K, T* c4V, const int32_t* __restrict__ L,
+                  int stage, int64_t c4_cap, T* c4K, T* c4V, const int32_t* L,
                   const T* __restrict__ treeK, const T* __restrict__ treeV,
-                  const int32_t* __restrict__ parents, const float* __restrict__ g4,
+                  const int32_t* parents, const float* __restrict__ g4,
                   const float* __restrict__ g128, T* scrK4, T* scrV4, T* scrK128, T* scrV128,
                   int32_t* status) {
   pdl_launch_dependents();   // the next kernel may start its prologue now
@@ -514,6 +514,10 @@ __global__ void __cluster_dims__(kC128Ranks, 1, 1) __launch_bounds__(kThreads)
   const int tid = threadIdx.x;
   const int rank = (int)cooperative_groups::this_cluster().block_rank();
   const bool has4 = comp_mask & TV_COMP_C4, has128 = comp_mask & TV_COMP_C128;
+  // with pages the kernel in front may be one that moves them or changes lengths (tv_pages_*), so
+  // nothing is read before it has completed (a paged round 164.0 -> 164.7 us); contiguous caches are
+  // read ahead, under the plan, which writes none of what is read here (see the header's stream order)
+  if (pg.page_tokens != 0) pdl_wait();
   // 1. the request's length, parents and the gates (one round trip)
   if (tid < D) {
     s_par[tid] = parents[(int64_t)b * D + tid];
