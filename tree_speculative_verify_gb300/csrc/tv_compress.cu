@@ -368,8 +368,9 @@ __global__ void __cluster_dims__(kC128Ranks, 1, 1) __launch_bounds__(kThreads)
   for (int i = threadIdx.x; i < d; i += blockDim.x) sm.gate128[i] = g[i];
   const int n = Lb / 128;
   int parity = 0;
-  for (int j = blockIdx.y; j < n; j += gridDim.y, parity ^= 1) {
-    if (!page_writable(pg, b, (int64_t)j * 128, status)) continue;   // uniform over the cluster
+  for (int j = blockIdx.y; j < n; j += gridDim.y) {
+    // (uniform over the cluster; a skipped entry leaves the receive buffers' turn as it is)
+    if (!page_writable(pg, b, (int64_t)j * 128, status)) continue;
     if (threadIdx.x < kC128Tokens) {
       const int64_t row =
           layer_row(pg, b, (int64_t)j * 128 + kC128Tokens * rank + threadIdx.x, raw_cap, 1, status);
@@ -381,6 +382,7 @@ __global__ void __cluster_dims__(kC128Ranks, 1, 1) __launch_bounds__(kThreads)
     cp_async_commit();
     const int64_t out = layer_row(pg, b, j, cap_m, 128, status) * d;
     entry128<T>(d, sm.gate128, CK + out, CV + out, parity, sm, [] {});
+    parity ^= 1;
   }
 }
 
