@@ -309,7 +309,8 @@ int tv_accept_walk(const tv_shape* shape, const int32_t* parents, const int32_t*
  *   parents [B][D] in (stage_chain == 1 only, else nullable)
  * Device errors: TV_ERR_CAPACITY (L+n > raw_cap or an entry beyond cap_m; request untouched),
  * TV_ERR_ARG (accept_len outside 1..D, a path id outside 0..D-1 or, with pages, no page for a
- * committed position; request untouched).
+ * committed position; request untouched).  An empty slot of a page pool is left alone without an
+ * error.
  */
 int tv_refresh_commit(const tv_shape* shape, const int32_t* parents, const int32_t* accept_len,
                       const int32_t* path, const void* treeK, const void* treeV, const void* scrK4,
@@ -383,6 +384,11 @@ int tv_token_logprobs(const tv_shape* shape, int32_t vocab, int64_t ld, int32_t 
  * like the others and can be captured; all three leave everything as it was when there are not
  * enough free pages (TV_ERR_CAPACITY).  Pages are taken in the order of the requests and positions
  * that need them, the lowest-numbered free page first, so results do not depend on timing.
+ * An empty slot -- L[b] = 0 and no page for its first position (page_table[b][0] = -1), as
+ * tv_pages_fork leaves a released one -- takes no part in a round: no call stages, selects or commits
+ * anything for it (committed_pos -1) or records an error, as long as its parents are a tree; its other
+ * outputs are unspecified.  It stays empty while tv_pages_reserve is given need[b] <= 0 for it; with
+ * need[b] > 0 the round starts a request on an empty prefix.
  * workspace: device buffer of ws_bytes >= tv_pages_workspace_size(shape), 256-byte aligned; calls
  * that overlap on the GPU need one each.
  */

@@ -581,3 +581,76 @@ def test_scratch_pad_right_behind_a_pages_call_sees_its_results(call):
                         + [st.rawK[table[live]], st.c4K[table[live]]])
         for a, b in zip(*runs):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("kernel,stage,sparse", [
+    (_lib.TV_ATTN_AUTO, 0, False), (_lib.TV_ATTN_AUTO, 1, False), (_lib.TV_ATTN_SIMT, 0, False),
+    (_lib.TV_ATTN_AUTO, 0, True), (_lib.TV_ATTN_SIMT, 1, True)])
+def test_released_slots_stay_empty(kernel, stage, sparse):
+    # rounds, called and replayed, pass over slots without a need: no page, no length, no error, and
+    # the others' rounds are those of a batch in which nothing was released
+    wl = workloads.long_context(B=4, L=(9000, 12000), n_sel=512) if sparse else \
+        workloads.serving(B=5, L=(500, 1400))
+    P, n_pool = (2048, 32) if sparse else (512, 24)
+    shape, st = engine.alloc_pool(wl, P, n_pool, kernel, stage_chain=stage)
+    rb = engine.alloc_round(wl, shape)
+    engine.prefill(shape, st, rb)
+    fshape, full = engine.clone_pool(shape, st)
+    frb = engine.alloc_round(wl, fshape)
+    gone, live = [1, 3], [b for b in range(wl.B) if b not in (1, 3)]
+    source = torch.arange(wl.B, dtype=torch.int32, device="cuda")
+    source[gone] = -1
+    engine.fork(shape, st, rb, source)
+    rb.need[gone] = 0
+    free = n_pool - len({p for b in live for p in st.page_table[b].tolist() if p >= 0})
+    assert int((st.page_refs == 0).sum()) == free
+    graph = None
+    for k in range(4):
+        if k < 2:
+            engine.verify_round(shape, st, rb, select=sparse)
+        else:
+            graph = graph or engine.RoundGraph(shape, st, rb, select=sparse)
+            graph.replay()
+        engine.verify_round(fshape, full, frb, select=sparse)
+        torch.cuda.synchronize()
+        assert int(rb.status.item()) == int(frb.status.item()) == 0
+        assert st.L[gone].tolist() == [0, 0]
+        assert bool((st.page_table[gone] == -1).all()) and bool((rb.committed[gone] == -1).all())
+        held = st.page_table[st.page_table >= 0].long()
+        assert torch.equal(torch.bincount(held, minlength=n_pool).int(), st.page_refs)
+        for name in ("O", "lse", "accept_len", "path", "bonus", "committed"):
+            assert torch.equal(getattr(rb, name)[live], getattr(frb, name)[live]), name
+        assert torch.equal(st.L[live], full.L[live])
+    engine.draft_decode(shape, st, rb)
+    torch.cuda.synchronize()
+    assert int(rb.status.item()) == 0 and st.L[gone].tolist() == [0, 0]
+    if not sparse:
+        rb.need[1] = wl.D          # a request starts on the slot
+        engine.verify_round(shape, st, rb)
+        torch.cuda.synchronize()
+        assert int(rb.status.item()) == 0
+        assert st.L[gone].tolist() == [int(rb.accept_len[1]), 0] and int(st.page_table[1, 0]) >= 0
+
+
+def test_missing_page_of_a_live_request_is_still_an_error():
+    wl = workloads.serving(B=2, L=(512, 512))
+    shape, st = engine.alloc_pool(wl, 512, 4)
+    rb = engine.alloc_round(wl, shape)
+    engine.prefill(shape, st, rb)
+    rb.need.zero_()
+    L = st.L.clone()
+    engine.verify_round(shape, st, rb)
+    torch.cuda.synchronize()
+    assert int(rb.status.item()) == _lib_code("TV_ERR_ARG")
+    assert torch.equal(st.L, L) and bool((rb.committed == -1).all())
+    # nor is a slot empty whose first page is there, or whose table holds another number
+    for first in (2, 77):
+        rb.status.zero_()
+        st.L.zero_()
+        st.page_table.fill_(-1)
+        st.page_table[:, 0] = torch.tensor([first, first + 1], dtype=torch.int32)
+        engine.verify_round(shape, st, rb)
+        torch.cuda.synchronize()
+        want = 0 if first == 2 else _lib_code("TV_ERR_ARG")
+        assert int(rb.status.item()) == want
+        assert (st.L.tolist() == [0, 0]) == (first == 77)

@@ -107,7 +107,7 @@ __device__ __forceinline__ EntryRef resolve_entry(const AttnParams<T>& p, const 
     if (p.n_sel > 0) {
       j = p.sel[(int64_t)b * p.n_sel + e];
       if (j < 0 || j >= lay.L / 4) {
-        record_error(p.status, TV_ERR_SELECTION);
+        if (!empty_slot(p.pg, b, lay.L)) record_error(p.status, TV_ERR_SELECTION);
         return r;
       }
     }

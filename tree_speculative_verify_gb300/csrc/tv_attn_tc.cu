@@ -211,7 +211,7 @@ __global__ void order_kernel(Params p, int32_t* order) {
 // Selected C4 entries ("sparse" prefix attention): copies entry sel[b][i] of request b's K and V
 // into row i of a dense per-request buffer, so the attention kernel reads the selection as
 // contiguous tiles.  One warp per selected entry; an index outside 0 .. L/4 - 1 (or past the C4
-// capacity) records TV_ERR_SELECTION and leaves a zero row.
+// capacity) leaves a zero row and, but for an empty slot's, records TV_ERR_SELECTION.
 __global__ void gather_sel_kernel(Paging pg, int B, int n_sel, int64_t c4_cap,
                                   const int32_t* __restrict__ L,
                                   const int32_t* __restrict__ sel, const uint4* __restrict__ c4K,
@@ -224,7 +224,7 @@ __global__ void gather_sel_kernel(Paging pg, int B, int n_sel, int64_t c4_cap,
   const int j = sel[w];
   const int Lb = L[b];
   const bool ok = Lb >= 0 && j >= 0 && j < Lb / 4 && j < c4_cap;
-  if (!ok && lane == 0) record_error(status, TV_ERR_SELECTION);
+  if (!ok && lane == 0 && !empty_slot(pg, b, Lb)) record_error(status, TV_ERR_SELECTION);
   constexpr int kRowU4 = 512 * 2 / 16;   // 64 x 16 B per bf16 row of 512
   const int64_t src = ok ? layer_row(pg, b, j, c4_cap, 4, status) * kRowU4 : 0;
   const int64_t dst = w * kRowU4;

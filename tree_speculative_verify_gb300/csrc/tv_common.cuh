@@ -125,6 +125,12 @@ inline Paging paging_of(const tv_shape* s) {
   return p;
 }
 
+// Whether slot b of a page pool is empty: no committed token and no page for the first one, as
+// tv_pages_fork leaves a released slot.  A round passes over it.
+__device__ __forceinline__ bool empty_slot(const Paging& pg, int b, int L) {
+  return pg.page_tokens != 0 && L == 0 && pg.table[(int64_t)b * pg.max_pages] == -1;
+}
+
 // Row of row `idx` of request b in a layer with `cap` rows per request.  A page id outside the
 // pool records TV_ERR_ARG and addresses page 0 (so no access leaves the pool).  With pages, an
 // index past the request's capacity (the padding rows of a partial tile, never used unmasked) is

@@ -536,6 +536,7 @@ __global__ void __cluster_dims__(kC128Ranks, 1, 1) __launch_bounds__(kThreads)
   // 2. the tree and the closers
   tree_structure(D, s_par, s_first, s_dep, s_cached, &s_ok);
   const bool ok = s_ok && Lb >= 0 && Lb <= raw_cap;
+  const bool staging = stage && !empty_slot(pg, b, Lb);
   if (tid < 32) {
     const int n4 = (ok && has4) ? closing_nodes(D, Lb, s_dep, 4, s_list4) : 0;
     const int n128 = (ok && has128) ? closing_nodes(D, Lb, s_dep, 128, s_list128) : 0;
@@ -585,7 +586,7 @@ __global__ void __cluster_dims__(kC128Ranks, 1, 1) __launch_bounds__(kThreads)
   for (int v = rank; v < D; v += kC128Ranks) {
     const int pos = Lb + s_dep[v];
     const int64_t out = ((int64_t)b * D + v) * d;
-    if (ok && stage && s_cached[v] && pos < raw_cap && page_writable(pg, b, pos, status)) {
+    if (ok && staging && s_cached[v] && pos < raw_cap && page_writable(pg, b, pos, status)) {
       const int64_t dst = layer_row(pg, b, pos, raw_cap, 1, status) * d;
       for (int i = tid; i < d; i += blockDim.x) {
         rawK[dst + i] = treeK[out + i];
@@ -620,7 +621,7 @@ __global__ void __cluster_dims__(kC128Ranks, 1, 1) __launch_bounds__(kThreads)
     const int64_t entry = (pos + 1) / 4 - 1;
     T* sK = nullptr;
     T* sV = nullptr;
-    if (stage && s_cached[v] && entry < c4_cap &&   // C4 refreshes promptly
+    if (staging && s_cached[v] && entry < c4_cap &&   // C4 refreshes promptly
         page_writable(pg, b, pos, status)) {
       const int64_t dst = layer_row(pg, b, entry, c4_cap, 4, status) * d;
       sK = c4K + dst;
@@ -690,7 +691,8 @@ __global__ void refresh_kernel(Paging pg, int D, int d, int es, int comp_mask, i
   if (tid == 0) {
     const int Lb = s_L, n = s_n;
     int ok = 1, code = 0;
-    if (n < 1 || n > D || Lb < 0) { ok = 0; code = TV_ERR_ARG; }
+    if (empty_slot(pg, b, Lb)) ok = 0;   // nothing to commit to: no error
+    else if (n < 1 || n > D || Lb < 0) { ok = 0; code = TV_ERR_ARG; }
     for (int i = 0; ok && i < n; ++i)
       if (s_path[i] < 0 || s_path[i] >= D) { ok = 0; code = TV_ERR_ARG; }
     if (ok) {
@@ -704,7 +706,7 @@ __global__ void refresh_kernel(Paging pg, int D, int d, int es, int comp_mask, i
         code = TV_ERR_ARG;
       }
     }
-    if (!ok) record_error(status, code);
+    if (code != 0) record_error(status, code);
     // with staging, the accepted nodes on the cached chain (the root, its lowest-numbered child,
     // ...) already sit in their final raw rows and C4 entries: the accepted path follows that
     // chain up to the first node where it leaves it

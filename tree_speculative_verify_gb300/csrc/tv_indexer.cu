@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(kScoreThreads, 4)
 // grid (8, B), clusters of 8 along x; launched as a programmatic dependent of score_kernel.
 // score_ws: [B][c4_cap] fp32 scores.
 __global__ void __cluster_dims__(kTopkRanks, 1, 1) __launch_bounds__(kTopkThreads)
-    select_kernel(int64_t c4_cap, int n_sel, const int32_t* __restrict__ L,
+    select_kernel(Paging pg, int64_t c4_cap, int n_sel, const int32_t* __restrict__ L,
                   const float* __restrict__ score_ws, int32_t* __restrict__ sel,
                   int32_t* status) {
   namespace cg = cooperative_groups;
@@ -155,7 +155,8 @@ __global__ void __cluster_dims__(kTopkRanks, 1, 1) __launch_bounds__(kTopkThread
   int32_t* out = sel + (int64_t)b * n_sel;
   if (n4l < n_sel || n4l > c4_cap) {   // uniform over the cluster
     if (rank == 0) {
-      if (tid == 0) record_error(status, n4l > c4_cap ? TV_ERR_CAPACITY : TV_ERR_SELECTION);
+      if (tid == 0 && !empty_slot(pg, b, Lb))
+        record_error(status, n4l > c4_cap ? TV_ERR_CAPACITY : TV_ERR_SELECTION);
       for (int i = tid; i < n_sel; i += blockDim.x) out[i] = -1;
     }
     return;
@@ -330,7 +331,7 @@ int tv_launch_indexer(const tv_shape* s, int d_idx, const void* q_idx, const voi
   const int64_t staged = per <= tv::kStageKeys ? per : 0;
   const size_t smem = (size_t)((staged + 3) / 4 * 4) * sizeof(uint32_t);
   tv::launch_pdl(tv::select_kernel, dim3(tv::kTopkRanks, s->B), dim3(tv::kTopkThreads), smem,
-                 stream, (int64_t)s->c4_cap, (int)s->n_sel, L, (const float*)score_ws, sel,
-                 status);
+                 stream, tv::paging_of(s), (int64_t)s->c4_cap, (int)s->n_sel, L,
+                 (const float*)score_ws, sel, status);
   return tv_check_launch("tv_indexer_topk");
 }

@@ -87,7 +87,8 @@ class RoundBuffers:
     workspace: torch.Tensor
     q_idx: torch.Tensor = None    # [B][64] bf16 indexer queries (sparse C4 path only)
     idx_ws: torch.Tensor = None   # indexer score workspace
-    need: torch.Tensor = None     # [B] int32 positions to reserve per round (managed pools only)
+    need: torch.Tensor = None     # [B] int32 positions to reserve per round, 0 for empty slots
+                                  # (managed pools only)
     logits: torch.Tensor = None   # [B][D][vocab] the model's logits (scored rounds, alloc_scores)
     logits_lse: torch.Tensor = None     # [B][D] fp32
     entropy: torch.Tensor = None        # [B][D] fp32, nats
@@ -294,14 +295,17 @@ def score(shape, rb, inv_temperature=1.0, stream=None):
 
 
 def reserve(shape, st, rb, need=None, stream=None):
-    """Pages for the next ``need`` positions of every request (default: the round's D)."""
+    """Pages for the next ``need`` positions of every request (default: ``rb.need``, the round's D
+    until the caller fills in less: the depth of a request's tree plus 1 is enough, and 0 keeps an
+    empty slot empty)."""
     _lib.tv_pages_reserve(shape, rb.need if need is None else need, st.L, st.page_refs, st.page_ws,
                           rb.status, stream)
 
 
 def fork(shape, st, rb, source, keep=None, stream=None):
     """Releases, truncates and branches the slots of a managed pool: ``source[b]`` is b (stays), -1
-    (released) or the slot that b becomes a copy of; ``keep`` truncates (see tv_pages_fork)."""
+    (released) or the slot that b becomes a copy of; ``keep`` truncates (see tv_pages_fork).  Rounds
+    pass over a released slot once ``rb.need[b]`` is 0; else the next one starts a request on it."""
     _lib.tv_pages_fork(shape, source, keep, st.L, st.page_refs, st.rawK, st.rawV, st.c4K, st.c4V,
                        st.c128K, st.c128V, st.k_idx, st.page_ws, rb.status, stream)
 
