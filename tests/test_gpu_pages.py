@@ -654,3 +654,25 @@ def test_missing_page_of_a_live_request_is_still_an_error():
         want = 0 if first == 2 else _lib_code("TV_ERR_ARG")
         assert int(rb.status.item()) == want
         assert (st.L.tolist() == [0, 0]) == (first == 77)
+
+
+@pytest.mark.parametrize("stage", [0, 1])
+def test_capturing_a_round_takes_no_pages(stage):
+    # neither with pages to spare nor without, when the capture's own round cannot have its pages
+    wl = workloads.serving(B=3, L=(512, 512))
+    for n_pool in (3, 12):
+        shape, st = engine.alloc_pool(wl, 512, n_pool, stage_chain=stage)
+        rb = engine.alloc_round(wl, shape)
+        engine.prefill(shape, st, rb)
+        torch.cuda.synchronize()
+        state = [st.L, st.page_table, st.page_refs, rb.status, st.rawK[:3], st.c4V[:3], st.c128K[:3]]
+        before = [t.clone() for t in state]
+        shorter = st.L - 10
+        graph = engine.RoundGraph(shape, st, rb, prologue=lambda: st.L.copy_(shorter))
+        for a, b in zip(state, before):
+            assert torch.equal(a, b)
+        graph.replay()               # at the prologue's lengths every position has its page
+        torch.cuda.synchronize()
+        assert int(rb.status.item()) == 0
+        assert torch.equal(st.L, shorter + rb.accept_len)
+        assert st.page_table[:, 1:].max() == -1 and int(st.page_refs.sum()) == 3

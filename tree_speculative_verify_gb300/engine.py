@@ -355,7 +355,8 @@ class RoundGraph:
     replays the verification step as a CUDA graph sized for the tree configuration; here the five
     calls (and an optional ``prologue`` of stream work, e.g. refilling inputs) are captured once
     and ``replay()`` relaunches them with a single graph launch.  Construction runs one round
-    without its commit (outputs and scratch pad are overwritten, the persistent state is not).
+    without its commit (outputs and scratch pad are overwritten, the persistent state is not; the
+    pages that this round takes from a managed pool, and what it reports about them, are taken back).
     The buffers in ``st`` / ``rb`` must stay allocated and at the same addresses; their contents
     may change between replays.
     """
@@ -364,7 +365,11 @@ class RoundGraph:
                  scored=False):
         # one eager round first, without the commit (the persistent state is left as it was):
         # the library's once-per-device set-up happens outside the capture
+        kept = [st.page_table, st.page_refs, rb.status] if st.page_refs is not None else []
+        before = [t.clone() for t in kept]
         verify_round(shape, st, rb, scale, None, False, select, scored)
+        for t, was in zip(kept, before):
+            t.copy_(was)
         torch.cuda.synchronize()
         self.graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(self.graph):
