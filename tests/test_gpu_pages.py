@@ -676,3 +676,42 @@ def test_capturing_a_round_takes_no_pages(stage):
         assert int(rb.status.item()) == 0
         assert torch.equal(st.L, shorter + rb.accept_len)
         assert st.page_table[:, 1:].max() == -1 and int(st.page_refs.sum()) == 3
+
+
+def test_calls_from_two_host_threads():
+    # pools of different sizes, both planned by one CTA with more shared memory than a kernel gets
+    # unasked: neither thread's launches fail for the other's
+    import threading
+    P, errors, pools = 512, [], []
+    for k, n_pool in enumerate((8192, 6300)):
+        L = [700] * 8
+        pools.append(Pool([[n_pool - 1 - 2 * b, n_pool - 2 - 2 * b, -1] for b in range(8)], L, n_pool, P, seed=k))
+    need = torch.full((8,), 8, dtype=torch.int32, device="cuda")
+    stay = torch.arange(8, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+
+    def work(s):
+        try:
+            stream = torch.cuda.Stream()
+            for _ in range(2000):
+                _lib.tv_pages_fork(s.shape, stay, None, s.L, s.refs, *s.layers(), None, s.ws, s.status, stream)
+                _lib.tv_pages_reserve(s.shape, need, s.L, s.refs, s.ws, s.status, stream)
+                _lib.tv_pages_compact(s.shape, s.L, s.refs, *s.layers(), s.remap, s.n_live, s.ws, s.status,
+                                      stream)
+            stream.synchronize()
+        except Exception as e:   # reported by the test's own thread
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(s,)) for s in pools]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    torch.cuda.synchronize()
+    for s in pools:
+        pages.fork(s.o, P, list(range(8)))
+        pages.reserve(s.o, P, [8] * 8)
+        code, remap, n = pages.compact(s.o, P)
+        s.check([])
+        assert s.n_live.tolist() == [n]

@@ -225,9 +225,7 @@ __device__ __forceinline__ bool list_free_pages(const PlanArgs& a, int rank, con
 
 // ---- fork: release, truncate, share ------------------------------------------------------------
 // Shared memory of a single CTA: counts and free list of the pages, four numbers per request.
-static size_t fork_smem(const tv_shape* s) {
-  return ((size_t)2 * s->n_pool_pages + (size_t)4 * s->B) * 4;
-}
+static size_t fork_smem(int n_pool, int B) { return ((size_t)2 * n_pool + (size_t)4 * B) * 4; }
 
 template <int kRanks>
 __global__ void __launch_bounds__(kPlanThreads)
@@ -370,9 +368,7 @@ __global__ void __launch_bounds__(kPlanThreads)
 }
 
 // ---- reserve: the pages of the next tokens -------------------------------------------------------
-static size_t reserve_smem(const tv_shape* s) {
-  return ((size_t)2 * s->n_pool_pages + (size_t)2 * s->B) * 4;
-}
+static size_t reserve_smem(int n_pool, int B) { return ((size_t)2 * n_pool + (size_t)2 * B) * 4; }
 
 // A round needs a page or two per request, which its thread looks at; a prompt's pages are looked at
 // by the thread's warp.
@@ -472,7 +468,7 @@ __global__ void __launch_bounds__(kPlanThreads)
 }
 
 // ---- compaction ----------------------------------------------------------------------------------
-static size_t compact_smem(const tv_shape* s) { return (size_t)5 * s->n_pool_pages * 4; }
+static size_t compact_smem(int n_pool, int) { return (size_t)5 * n_pool * 4; }
 
 template <int kRanks>
 __global__ void __launch_bounds__(kPlanThreads)
@@ -697,8 +693,10 @@ static int launch_copy(const char* fn, const tv_shape* s, const PlanArgs& p, voi
 // reserve 64 slots, 400 pages: 3.0 and 4.4; 1024 slots, 8192 pages: 3.9 and 4.5.
 template <typename... KArgs, typename... Args>
 static int launch_plan(const char* fn, const tv_shape* s, int64_t steps, void (*one)(KArgs...),
-                       void (*cluster)(KArgs...), size_t smem, cudaStream_t stream, Args... args) {
+                       void (*cluster)(KArgs...), size_t (*smem_of)(int, int), cudaStream_t stream,
+                       Args... args) {
   const bool single = s->n_pool_pages <= kOnePages && steps <= kOneSteps;
+  const size_t smem = smem_of(s->n_pool_pages, s->B);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(single ? 1 : kPlanRanks);
   cfg.blockDim = dim3(kPlanThreads);
@@ -713,8 +711,10 @@ static int launch_plan(const char* fn, const tv_shape* s, int64_t steps, void (*
   cfg.attrs = attr;
   cfg.numAttrs = single ? 1 : 2;
   cudaError_t e = cudaSuccess;
-  if (single && smem > 48 * 1024)
-    e = cudaFuncSetAttribute(one, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (single && smem > 48 * 1024)   // always the most that any call takes (a request has a step or
+                                    // more): another host thread may be launching the same kernel
+    e = cudaFuncSetAttribute(one, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)smem_of(kOnePages, kOneSteps));
   if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, single ? one : cluster, KArgs(args)...);
   return e == cudaSuccess ? tv_check_launch(fn) : launch_error(fn, e);
 }
@@ -729,7 +729,7 @@ int tv_launch_fork(const tv_shape* s, const int32_t* source, const int32_t* keep
   const char* fn = "tv_pages_fork";
   const tv::PlanArgs a = tv::plan_args(s, L, refs, workspace, status);
   if (int rc = tv::launch_plan(fn, s, (int64_t)s->B * s->max_pages, tv::fork_plan_kernel<1>,
-                               tv::fork_plan_kernel<tv::kPlanRanks>, tv::fork_smem(s), stream, a, L, source, keep))
+                               tv::fork_plan_kernel<tv::kPlanRanks>, tv::fork_smem, stream, a, L, source, keep))
     return rc;
   return tv::launch_copy(fn, s, a, pools, keys, d_idx, source, stream);
 }
@@ -738,7 +738,7 @@ int tv_launch_reserve(const tv_shape* s, const int32_t* need, const int32_t* L, 
                       void* workspace, int32_t* status, cudaStream_t stream) {
   const tv::PlanArgs a = tv::plan_args(s, L, refs, workspace, status);
   return tv::launch_plan("tv_pages_reserve", s, s->B, tv::reserve_kernel<1>,
-                         tv::reserve_kernel<tv::kPlanRanks>, tv::reserve_smem(s), stream, a, need);
+                         tv::reserve_kernel<tv::kPlanRanks>, tv::reserve_smem, stream, a, need);
 }
 
 int tv_launch_compact(const tv_shape* s, const int32_t* L, int32_t* refs, void* const pools[6],
@@ -747,7 +747,7 @@ int tv_launch_compact(const tv_shape* s, const int32_t* L, int32_t* refs, void* 
   const char* fn = "tv_pages_compact";
   const tv::PlanArgs a = tv::plan_args(s, L, refs, workspace, status);
   if (int rc = tv::launch_plan(fn, s, (int64_t)s->B * s->max_pages, tv::compact_plan_kernel<1>,
-                               tv::compact_plan_kernel<tv::kPlanRanks>, tv::compact_smem(s), stream,
+                               tv::compact_plan_kernel<tv::kPlanRanks>, tv::compact_smem, stream,
                                a, remap, n_live))
     return rc;
   return tv::launch_copy(fn, s, a, pools, nullptr, 0, nullptr, stream);
