@@ -425,3 +425,30 @@ def test_acceptance_walk_takes_the_targets_of_the_call_in_front(B):
             assert rb.path[b, :n].tolist() == list(path)[:n]
             lengths.add(n)
     assert len(lengths) > 1
+
+
+@pytest.mark.parametrize("dtype,T,rows,V,ranks,columns", [
+    (F32, 256, 104, 140003, 1, 1), (BF, 256, 104, 140003, 1, 1), (F32, 128, 600, 70003, 1, 1),
+    (BF, 128, 600, 70003, 1, 1), (F32, 64, 1300, 8191, 1, 8), (BF, 64, 1300, 16384, 1, 8),
+    (F32, 256, 1, 2200000, 16, 1), (BF, 256, 2, 2300000, 16, 1)])
+def test_more_large_logits_in_few_threads_than_the_list_holds(dtype, T, rows, V, ranks, columns):
+    # all large logits of a CTA's share (T threads, `ranks` CTAs per row) in the vectors of fewer threads
+    # than there are alternatives, and more of them than the 512 candidates: the bound stays at the
+    # others' value, the list overflows twice, and every alternative takes a scan of its own
+    kvec = 8 if dtype == BF else 4
+    n_vec = -(-V // kvec)
+    per = -(-n_vec // ranks)
+    i = torch.arange(V, device="cuda") // kvec
+    col = (i % per) % T < columns
+    assert int(col[: min(V, (per - T) * kvec)].sum()) > 512
+    x = torch.full((rows, 1, V), -3.0, dtype=dtype, device="cuda")
+    vals = torch.linspace(1.0, 200.0, int(col.sum()), device="cuda")
+    order = torch.randperm(len(vals), generator=torch.Generator().manual_seed(2)).cuda()
+    x[0, 0, col] = vals[order].to(dtype)
+    x[-1, 0, col] = vals.to(dtype)
+    tokens = np.full((rows, 1), 20, dtype=np.int32)
+    pick = sorted({0, rows - 1})
+    for K in (32, 2):
+        got, status = _run(x, tokens, None, 1.0, K)
+        assert status == 0
+        _check(x[pick], {k: v[pick] for k, v in got.items()}, tokens[pick], None, 1.0, K)

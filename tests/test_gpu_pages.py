@@ -715,3 +715,54 @@ def test_calls_from_two_host_threads():
         code, remap, n = pages.compact(s.o, P)
         s.check([])
         assert s.n_live.tolist() == [n]
+
+
+@pytest.mark.parametrize("d,dtype,comp,P", [(72, "f32", (4, 128), 1536), (512, "bf16", (4,), 512),
+                                            (24, "f32", (128,), 512), (8, "bf16", (128,), 1024)])
+@pytest.mark.parametrize("n_pool", [60, 8300])
+def test_compact_of_other_pools(d, dtype, comp, P, n_pool):
+    # fp32 rows, one compressor, both plan variants
+    if n_pool > 1000:
+        d = 8
+    rng = np.random.default_rng(d + P)
+    L = [int(x) for x in rng.integers(0, 4 * P + 1, size=12)]
+    table = _random_table(rng, 12, 5, n_pool, L, P)
+    for g in range(min(L[3], L[2]) // P):
+        table[3][g] = table[2][g]
+    extra = [p for p in (n_pool - 1, n_pool - 4, 7)]
+    s = Pool(table, L, n_pool, P, d, dtype, comp, extra=extra)
+    assert s.compact() == 0
+    s.check([])
+    assert s.compact() == 0
+    s.check([])
+
+
+def test_draft_steps_on_a_managed_pool():
+    # the draft side's call reserves its own pages, commits nothing, and computes what it does on a
+    # contiguous cache
+    base = workloads.draft_beam(B=4, steps=3, L=(1500, 2600))
+    for step in (1, 2, 3):
+        wl = workloads.draft_level(base, step)
+        wl.L[0] = 1536                    # its next position lies on a page that is not there yet
+        shape, st = engine.alloc_pool(wl, 512, 40)
+        rb = engine.alloc_round(wl, shape)
+        engine.prefill(shape, st, rb)
+        torch.cuda.synchronize()
+        L, mapped = st.L.clone(), st.page_table.clone()
+        engine.draft_decode(shape, st, rb)
+        cshape = engine.shape_for(wl)
+        cshape.raw_cap, cshape.c4_cap, cshape.c128_cap = shape.raw_cap, shape.c4_cap, shape.c128_cap
+        view = st.page_table.long().clamp(min=0)
+        logical = lambda t: t[view].reshape(wl.B, -1, wl.d).contiguous()
+        cst = engine.DeviceState(*(logical(getattr(st, k)) for m in MS for k in MS[m]), L=L.clone())
+        crb = engine.alloc_round(wl, cshape)
+        engine.draft_decode(cshape, cst, crb)
+        torch.cuda.synchronize()
+        assert int(rb.status.item()) == int(crb.status.item()) == 0
+        for name in ("O", "lse", "scrK4", "scrV128"):
+            assert torch.equal(getattr(rb, name), getattr(crb, name)), name
+        assert torch.equal(st.L, L)
+        new = (mapped == -1) & (st.page_table >= 0)
+        assert int(new[0].sum()) == 1 and torch.equal(st.page_table[~new], mapped[~new])
+        held = st.page_table[st.page_table >= 0].long()
+        assert torch.equal(torch.bincount(held, minlength=40).int(), st.page_refs)
