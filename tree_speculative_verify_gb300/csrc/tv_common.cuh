@@ -132,22 +132,30 @@ __device__ __forceinline__ bool empty_slot(const Paging& pg, int b, int L) {
 }
 
 // Row of row `idx` of request b in a layer with `cap` rows per request.  A page id outside the
-// pool records TV_ERR_ARG and addresses page 0 (so no access leaves the pool).  With pages, an
-// index past the request's capacity (the padding rows of a partial tile, never used unmasked) is
-// clamped to its last row, so the page-table read stays inside the request's row of the table.
-__device__ __forceinline__ int64_t layer_row(const Paging& pg, int b, int64_t idx, int64_t cap,
-                                             int tokens_per_row, int32_t* status) {
+// pool records TV_ERR_ARG and gives ~row on page 0 (negative), which a call that writes leaves out.
+// With pages, an index past the request's capacity (the padding rows of a partial tile, never used
+// unmasked) is clamped to its last row, so the page-table read stays inside the request's row of the
+// table.
+__device__ __forceinline__ int64_t mapped_row(const Paging& pg, int b, int64_t idx, int64_t cap,
+                                              int tokens_per_row, int32_t* status) {
   if (pg.page_tokens == 0)
     return (int64_t)b * cap + (tv_in_range(idx, 0, cap, status, 5) ? idx : 0);
   if (idx >= cap) idx = cap - 1;
   if (idx < 0) idx = 0;
   const int64_t rpp = pg.page_tokens / tokens_per_row;
-  int32_t page = pg.table[(int64_t)b * pg.max_pages + idx / rpp];
+  const int32_t page = pg.table[(int64_t)b * pg.max_pages + idx / rpp];
   if (page < 0 || page >= pg.n_pool_pages) {
     record_error(status, TV_ERR_ARG);
-    page = 0;
+    return ~(idx % rpp);
   }
   return (int64_t)page * rpp + idx % rpp;
+}
+
+// The same for reads: a page id outside the pool addresses page 0, so no access leaves the pool.
+__device__ __forceinline__ int64_t layer_row(const Paging& pg, int b, int64_t idx, int64_t cap,
+                                             int tokens_per_row, int32_t* status) {
+  const int64_t row = mapped_row(pg, b, idx, cap, tokens_per_row, status);
+  return row < 0 ? ~row : row;
 }
 
 }  // namespace tv

@@ -298,21 +298,6 @@ __device__ void entry128(int d, const float* gate, T* outK, T* outV, int parity,
   __syncthreads();   // the rows may be refetched for the next entry
 }
 
-// Whether the page of position `pos` of request b can be written: true without pages.  A page id
-// outside the pool (an unmapped page, say) records TV_ERR_ARG; the caller skips its writes, which
-// layer_row would send to page 0.
-__device__ __forceinline__ bool page_writable(const Paging& pg, int b, int64_t pos,
-                                              int32_t* status) {
-  if (pg.page_tokens == 0) return true;
-  const int64_t g = pos / pg.page_tokens;
-  if (g < pg.max_pages) {
-    const int32_t page = pg.table[(int64_t)b * pg.max_pages + g];
-    if (page >= 0 && page < pg.n_pool_pages) return true;
-  }
-  record_error(status, TV_ERR_ARG);
-  return false;
-}
-
 // ---- prefill: every complete block of the committed prefix ---------------------------------
 // C4: grid.x entry index (strided), grid.y request.
 template <typename T>
@@ -333,13 +318,16 @@ __global__ void __launch_bounds__(kThreads) prefill4_kernel(
   for (int i = threadIdx.x; i < d; i += blockDim.x) sm.gate4[i] = g[i];
   const int n = Lb / 4;
   for (int j = blockIdx.x; j < n; j += gridDim.x) {
-    if (!page_writable(pg, b, (int64_t)j * 4, status)) continue;   // uniform over the CTA
     if (threadIdx.x < 4) {
-      const int64_t row = layer_row(pg, b, (int64_t)j * 4 + threadIdx.x, raw_cap, 1, status);
-      rowK[threadIdx.x] = rawK + row * d;
-      rowV[threadIdx.x] = rawV + row * d;
+      const int64_t row = mapped_row(pg, b, (int64_t)j * 4 + threadIdx.x, raw_cap, 1, status);
+      rowK[threadIdx.x] = row < 0 ? nullptr : rawK + row * d;
+      rowV[threadIdx.x] = row < 0 ? nullptr : rawV + row * d;
     }
     __syncthreads();
+    if (rowK[0] == nullptr) {   // no page: nothing to write (uniform over the CTA)
+      __syncthreads();
+      continue;
+    }
     fetch_rows<T>(sm.rows4, rowK, rowV, 4, nullptr, d);
     cp_async_commit();
     const int64_t out = layer_row(pg, b, j, cap4, 4, status) * d;
@@ -369,15 +357,17 @@ __global__ void __cluster_dims__(kC128Ranks, 1, 1) __launch_bounds__(kThreads)
   const int n = Lb / 128;
   int parity = 0;
   for (int j = blockIdx.y; j < n; j += gridDim.y) {
-    // (uniform over the cluster; a skipped entry leaves the receive buffers' turn as it is)
-    if (!page_writable(pg, b, (int64_t)j * 128, status)) continue;
     if (threadIdx.x < kC128Tokens) {
       const int64_t row =
-          layer_row(pg, b, (int64_t)j * 128 + kC128Tokens * rank + threadIdx.x, raw_cap, 1, status);
-      rowK[threadIdx.x] = rawK + row * d;
-      rowV[threadIdx.x] = rawV + row * d;
+          mapped_row(pg, b, (int64_t)j * 128 + kC128Tokens * rank + threadIdx.x, raw_cap, 1, status);
+      rowK[threadIdx.x] = row < 0 ? nullptr : rawK + row * d;
+      rowV[threadIdx.x] = row < 0 ? nullptr : rawV + row * d;
     }
     __syncthreads();
+    if (rowK[0] == nullptr) {   // no page: nothing to write (uniform over the cluster, whose rows lie
+      __syncthreads();          // on one page); the receive buffers' turn stays as it is
+      continue;
+    }
     fetch_rows<T>(sm.rows, rowK, rowV, kC128Tokens, nullptr, d);
     cp_async_commit();
     const int64_t out = layer_row(pg, b, j, cap_m, 128, status) * d;
@@ -586,11 +576,11 @@ __global__ void __cluster_dims__(kC128Ranks, 1, 1) __launch_bounds__(kThreads)
   for (int v = rank; v < D; v += kC128Ranks) {
     const int pos = Lb + s_dep[v];
     const int64_t out = ((int64_t)b * D + v) * d;
-    if (ok && staging && s_cached[v] && pos < raw_cap && page_writable(pg, b, pos, status)) {
-      const int64_t dst = layer_row(pg, b, pos, raw_cap, 1, status) * d;
-      for (int i = tid; i < d; i += blockDim.x) {
-        rawK[dst + i] = treeK[out + i];
-        rawV[dst + i] = treeV[out + i];
+    if (ok && staging && s_cached[v] && pos < raw_cap) {
+      const int64_t row = mapped_row(pg, b, pos, raw_cap, 1, status);
+      for (int i = row < 0 ? d : tid; i < d; i += blockDim.x) {   // (no page: not staged)
+        rawK[row * d + i] = treeK[out + i];
+        rawV[row * d + i] = treeV[out + i];
       }
     }
     const bool closes4 = ok && ((pos + 1) & 3) == 0;
@@ -621,11 +611,12 @@ __global__ void __cluster_dims__(kC128Ranks, 1, 1) __launch_bounds__(kThreads)
     const int64_t entry = (pos + 1) / 4 - 1;
     T* sK = nullptr;
     T* sV = nullptr;
-    if (staging && s_cached[v] && entry < c4_cap &&   // C4 refreshes promptly
-        page_writable(pg, b, pos, status)) {
-      const int64_t dst = layer_row(pg, b, entry, c4_cap, 4, status) * d;
-      sK = c4K + dst;
-      sV = c4V + dst;
+    if (staging && s_cached[v] && entry < c4_cap) {   // C4 refreshes promptly
+      const int64_t row = mapped_row(pg, b, entry, c4_cap, 4, status);
+      if (row >= 0) {
+        sK = c4K + row * d;
+        sV = c4V + row * d;
+      }
     }
     entry4<T>(d, sm.c4.gate4, scrK4 + out, scrV4 + out, sK, sV, j == rank && n128 > 0 ? 1 : 0,
               sm.c4);
@@ -700,11 +691,6 @@ __global__ void refresh_kernel(Paging pg, int D, int d, int es, int comp_mask, i
       if (Lnew > raw_cap) { ok = 0; code = TV_ERR_CAPACITY; }
       if ((comp_mask & TV_COMP_C4) && Lnew / 4 > c4_cap) { ok = 0; code = TV_ERR_CAPACITY; }
       if ((comp_mask & TV_COMP_C128) && Lnew / 128 > c128_cap) { ok = 0; code = TV_ERR_CAPACITY; }
-      // every page the commit writes is there (n <= 64 positions lie in at most two pages)
-      if (ok && !(page_writable(pg, b, Lb, status) && page_writable(pg, b, Lnew - 1, status))) {
-        ok = 0;
-        code = TV_ERR_ARG;
-      }
     }
     if (code != 0) record_error(status, code);
     // with staging, the accepted nodes on the cached chain (the root, its lowest-numbered child,
@@ -735,8 +721,11 @@ __global__ void refresh_kernel(Paging pg, int D, int d, int es, int comp_mask, i
     return;
   }
   const int Lb = s_L, n = s_n;
+  bool mapped = true;   // the position's page is there
   if (tid < n) {
     const int i = tid;
+    const int64_t row = mapped_row(pg, b, Lb + i, raw_cap, 1, status);
+    mapped = row >= 0;
     const int64_t src = ((int64_t)b * D + s_path[i]) * row_bytes;
     const bool on_chain = i < s_staged;
     const int e = Lb + i;
@@ -744,7 +733,7 @@ __global__ void refresh_kernel(Paging pg, int D, int d, int es, int comp_mask, i
     const bool e4 = (comp_mask & TV_COMP_C4) && ((e + 1) & 3) == 0 && !on_chain;
     const bool e128 = (comp_mask & TV_COMP_C128) && ((e + 1) & 127) == 0;
     if (raw) {
-      const int64_t dst = layer_row(pg, b, e, raw_cap, 1, status) * row_bytes;
+      const int64_t dst = row * row_bytes;
       s_srcK[3 * i] = treeK + src;
       s_srcV[3 * i] = treeV + src;
       s_dstK[3 * i] = rawK + dst;
@@ -771,7 +760,10 @@ __global__ void refresh_kernel(Paging pg, int D, int d, int es, int comp_mask, i
       s_srcK[3 * i + 2] = nullptr;
     }
   }
-  __syncthreads();
+  if (!__syncthreads_and(mapped)) {   // a page is missing: nothing is committed
+    for (int i = tid; i < D; i += blockDim.x) cpos[i] = -1;
+    return;
+  }
   // the copies, kCopyUnroll chunks per thread with all their loads in flight before the stores
   constexpr int kCopyUnroll = 4;
   const int chunks = (int)(row_bytes / 16);
