@@ -80,19 +80,21 @@ __device__ __forceinline__ float max_nan(float a, float b) {   // NaN if either 
 }
 __device__ __forceinline__ bool is_far(float m, float c) { return !(fabsf(m * c) < kFar); }
 
-// m c - b of a maximum whose sums are relative to 2^b, 0 of a far one
+// m c - fl(m c)
 __device__ __forceinline__ float residual_of(float m, float c) {
-  return is_far(m, c) ? 0.f : fmaf(m, c, -__fmul_rn(m, c));
+  return fmaf(m, c, -__fmul_rn(m, c));
 }
 
 // p relative to a maximum m >= p.m
 __device__ __forceinline__ void rebase(Partial& p, float m, float c) {
   if (m > p.m) {
     // the sums are relative to the rounded products (not contracted) or, far, to m c itself; where
-    // one of the two is far, the difference of m c and p.m c goes over to the other's base
-    const float d = is_far(m, c) || is_far(p.m, c)
-                        ? (p.m - m) * c + (residual_of(m, c) - residual_of(p.m, c))
-                        : __fmul_rn(p.m, c) - __fmul_rn(m, c);
+    // one of the two is far, the difference of p.m c and m c also takes the other's residual
+    // (selected, not branched to: the masked batch of 120 rows 10.05 us, 10.26 us with branches)
+    const bool far = is_far(m, c), was_far = is_far(p.m, c);
+    const float r = residual_of(far ? p.m : m, c), mixed = far == was_far ? 0.f : far ? -r : r;
+    const float d = far || was_far ? (p.m - m) * c + mixed
+                                   : __fmul_rn(p.m, c) - __fmul_rn(m, c);
     const float e = fmaxf(d, kMinExp), f = exp2_approx(e);
     p.t = (p.t + e * p.s) * f;
     p.s *= f;
@@ -661,7 +663,8 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const T* logits,
   const bool none = !bad && p.m == -INFINITY;
   const float nan = __int_as_float(0x7fffffff);
   // ln S relative to m: the rounding of m c taken out (-inf for an empty row)
-  const float ln_s = logf(p.s), log_s = ln_s - residual_of(p.m, c) * kLn2;
+  const float residual = is_far(p.m, c) ? 0.f : residual_of(p.m, c);
+  const float ln_s = logf(p.s), log_s = ln_s - residual * kLn2;
   auto log_prob = [&](float x) {
     return bad ? nan : x == -INFINITY ? x : (x - p.m) * a.scale - log_s;
   };
