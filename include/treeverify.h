@@ -358,7 +358,8 @@ int tv_indexer_topk(const tv_shape* shape, int d_idx, const void* q_idx, const v
  *            parents (n_tok = D) scores every draft token under its parent, the root as 0.
  * Sums are kept in fp32 relative to the largest logit.  A logit of -inf is a masked token
  * (probability 0, ln p = -inf).  A row of -inf only has lse = -inf, entropy 0, target -1, no
- * alternatives and ln p = -inf.  The type's lowest finite value is an ordinary logit.
+ * alternatives and ln p = -inf.  The type's lowest finite value is an ordinary logit.  Results beyond
+ * fp32's range (that value at scale > 1, say) are -inf or +inf.
  *   Uses shape->B and D (rows = B * D).  vocab 1..2^30; logits [B][D] rows of vocab elements, ld
  *   >= vocab elements apart, of type logits_dtype (TV_F32 | TV_BF16), aligned to that type only.
  *   n_tok 0..1024, tokens and nodes [B][n_tok] int32 in (nullable when n_tok == 0; nodes null:

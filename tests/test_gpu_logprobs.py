@@ -452,3 +452,26 @@ def test_more_large_logits_in_few_threads_than_the_list_holds(dtype, T, rows, V,
         got, status = _run(x, tokens, None, 1.0, K)
         assert status == 0
         _check(x[pick], {k: v[pick] for k, v in got.items()}, tokens[pick], None, 1.0, K)
+
+
+def test_scored_rounds_at_a_temperature():
+    wl = workloads.small()
+    shape = engine.shape_for(wl)
+    outs = []
+    for graphed in (False, True):
+        st, rb = engine.alloc_state(wl), engine.alloc_round(wl, shape)
+        engine.prefill(shape, st, rb)
+        engine.alloc_scores(rb, shape, workloads.VOCAB, n_top=2)
+        rb.logits.normal_(generator=torch.Generator(device="cuda").manual_seed(4))
+        if graphed:
+            engine.RoundGraph(shape, st, rb, scored=True, inv_temperature=2.5).replay()
+        else:
+            engine.verify_round(shape, st, rb, scored=True, inv_temperature=2.5)
+        torch.cuda.synchronize()
+        assert int(rb.status.item()) == 0
+        outs.append([t.cpu().numpy() for t in (rb.logits_lse, rb.entropy, rb.draft_logprobs, rb.top_logprobs)])
+    for a, b in zip(*outs):
+        assert np.array_equal(a, b)
+    got = dict(zip(("lse", "entropy", "logprobs", "top_logprobs"), outs[0]), target=rb.target.cpu().numpy(),
+               top_ids=rb.top_ids.cpu().numpy())
+    _check(rb.logits, got, wl.draft, wl.parents, 2.5, 2)

@@ -316,11 +316,13 @@ def compact(shape, st, rb, remap, n_live, stream=None):
                           st.c128V, remap, n_live, st.page_ws, rb.status, stream)
 
 
-def verify_round(shape, st, rb, scale=None, stream=None, commit=True, select=False, scored=False):
+def verify_round(shape, st, rb, scale=None, stream=None, commit=True, select=False, scored=False,
+                 inv_temperature=1.0):
     """One target-verify round: plan, scratch pad, attention, acceptance, refresh; with
     ``select`` the indexer first picks the sparse path's C4 entries on the device, with ``scored``
-    the target tokens come from ``rb.logits`` (else the caller has filled ``rb.target``).  On a
-    managed pool the round's pages are reserved first."""
+    the target tokens come from ``rb.logits`` (else the caller has filled ``rb.target``), the log
+    probabilities and entropies at ``inv_temperature``.  On a managed pool the round's pages are
+    reserved first (``rb.need``)."""
     if st.page_refs is not None:
         reserve(shape, st, rb, None, stream)
     if select:
@@ -329,7 +331,7 @@ def verify_round(shape, st, rb, scale=None, stream=None, commit=True, select=Fal
     branch_compress(shape, st, rb, stream)
     attention(shape, st, rb, scale, stream)
     if scored:
-        score(shape, rb, 1.0, stream)
+        score(shape, rb, inv_temperature, stream)
     accept(shape, st, rb, stream)
     if commit:
         refresh(shape, st, rb, stream)
@@ -362,12 +364,12 @@ class RoundGraph:
     """
 
     def __init__(self, shape, st, rb, scale=None, commit=True, prologue=None, select=False,
-                 scored=False):
+                 scored=False, inv_temperature=1.0):
         # one eager round first, without the commit (the persistent state is left as it was):
         # the library's once-per-device set-up happens outside the capture
         kept = [st.page_table, st.page_refs, rb.status] if st.page_refs is not None else []
         before = [t.clone() for t in kept]
-        verify_round(shape, st, rb, scale, None, False, select, scored)
+        verify_round(shape, st, rb, scale, None, False, select, scored, inv_temperature)
         for t, was in zip(kept, before):
             t.copy_(was)
         torch.cuda.synchronize()
@@ -376,7 +378,7 @@ class RoundGraph:
             stream = torch.cuda.current_stream()
             if prologue is not None:
                 prologue()
-            verify_round(shape, st, rb, scale, stream, commit, select, scored)
+            verify_round(shape, st, rb, scale, stream, commit, select, scored, inv_temperature)
 
     def replay(self):
         self.graph.replay()
