@@ -387,9 +387,10 @@ int tv_token_logprobs(const tv_shape* shape, int32_t vocab, int64_t ld, int32_t 
  * that need them, the lowest-numbered free page first, so results do not depend on timing.
  * An empty slot -- L[b] = 0 and no page for its first position (page_table[b][0] = -1), as
  * tv_pages_fork leaves a released one -- takes no part in a round: no call stages, selects or commits
- * anything for it (committed_pos -1) or records an error, as long as its parents are a tree; its other
- * outputs are unspecified.  It stays empty while tv_pages_reserve is given need[b] <= 0 for it; with
- * need[b] > 0 the round starts a request on an empty prefix.
+ * anything for it (committed_pos -1) or records an error, as long as its parents are a tree and what
+ * tv_token_logprobs is given for it is valid; its other outputs are unspecified.  It stays empty while
+ * tv_pages_reserve is given need[b] <= 0 for it; with need[b] > 0 the round starts a request on an
+ * empty prefix.
  * workspace: device buffer of ws_bytes >= tv_pages_workspace_size(shape), 256-byte aligned; calls
  * that overlap on the GPU need one each.
  */
