@@ -103,6 +103,9 @@ typedef struct CUstream_st* tv_stream_t; /* the same handle type as cudaStream_t
 #define TV_ATTN_AUTO 0    /* tensor-core kernel where supported, else the SIMT kernel */
 #define TV_ATTN_SIMT 1    /* CUDA-core fp32 kernel: any supported shape, fp32 or bf16 */
 #define TV_ATTN_TCGEN05 2 /* tcgen05 tensor-core kernel: bf16, d == 512 */
+/* rope_pairs of tv_chunk_append */
+#define TV_ROPE_HALVES 0
+#define TV_ROPE_PAIRS 1
 
 typedef struct tv_shape {
   int32_t B;           /* requests (>= 0; B == 0 turns every call into a no-op) */
@@ -449,6 +452,97 @@ int tv_pages_compact(const tv_shape* shape, const int32_t* L, int32_t* page_refs
                      void* rawV, void* c4K, void* c4V, void* c128K, void* c128V, int32_t* remap,
                      int32_t* n_live, void* workspace, size_t ws_bytes, int32_t* status,
                      tv_stream_t stream);
+
+/*
+ * New tokens into the cache: a prompt, a part of one, or one token per request, in one ragged batch.
+ * The report's rounds extend the cache by accepted tree tokens only ([TSD-V4] §4.2) and leave
+ * prompts to the serving engine; the rules here are those of tv_prefill_compress and
+ * tv_refresh_commit.  Request b's new tokens are rows starts[b] .. starts[b+1] - 1 of the batch's
+ * n_new rows, in order; token i of it goes to position p = L[b] + i:
+ *   rawK row p <- K row with its last rope_dim elements rotated by the position: with r = rope_dim
+ *   and f = inv_freq, pair i (x, y) becomes (x cos a - y sin a, x sin a + y cos a), a = p * f[i]
+ *   radians, i < r/2; the pair is elements (i, i + r/2) of the r (TV_ROPE_HALVES) or (2i, 2i + 1)
+ *   (TV_ROPE_PAIRS); rotated in fp32, the angle reduced in fp64, stored in the cache dtype
+ *   rawV row p <- V row;  Qr row <- Q row, every head rotated the same way
+ *   every block that the new tokens complete gets its C4 / C128 entry, from the rows as they are
+ *   stored: bit for bit what tv_prefill_compress writes for the same rows, however the tokens were
+ *   split into calls
+ *   L[b] <- L[b] + starts[b+1] - starts[b]
+ * Uses shape->B, H, d, dtype, comp_mask, the capacities and the paging.
+ *   n_new 0..2^30, n_new * H < 2^31; starts [B+1] int32 in, 0 <= starts[0], ascending, starts[B] <=
+ *   n_new (rows of no request are left alone); K, V n_new rows of d elements in, ld_kv >= d elements
+ *   apart; Q [n_new][H][d] in (nullable, with Qr), Qr [n_new][H][d] out, may be Q: then only the
+ *   rotated elements are written; rope_dim even, 0..d (0: no rotation, inv_freq nullable); inv_freq
+ *   [rope_dim / 2] fp32 in; g4, g128 [d] fp32 in and c4K .. c128V out (nullable when the compressor
+ *   is inactive).  K, V, Q, Qr, the caches and ld_kv's bytes 16-byte aligned.
+ * Device errors, each leaving that request as it was (its Qr rows are unspecified): TV_ERR_ARG
+ * (starts that descend or leave 0 .. n_new, L < 0, no page for a new position), TV_ERR_CAPACITY
+ * (L + n > raw_cap or an entry beyond cap_m).
+ */
+int tv_chunk_append(const tv_shape* shape, int32_t n_new, const int32_t* starts, const void* K,
+                    const void* V, int64_t ld_kv, const void* Q, int32_t rope_dim,
+                    int32_t rope_pairs, const float* inv_freq, const float* g4, const float* g128,
+                    void* Qr, void* rawK, void* rawV, void* c4K, void* c4V, void* c128K,
+                    void* c128V, int32_t* L, int32_t* status, tv_stream_t stream);
+
+/*
+ * Attention of a chunk of new tokens over the cache that holds them ([TSD-V4] §2.2: compressed
+ * attention of ordinary causal decoding; §3.1's visibility for a chain).  Request b's queries are
+ * rows starts[b] .. starts[b+1] - 1; they belong to the last n = starts[b+1] - starts[b] positions
+ * of its cache, p = L[b] - n + i (call it after tv_chunk_append, which advances L).  Every head of
+ * the token at position p attends, with logit scale `scale`, to the C4 entries 0 .. p/4 - 1, the
+ * C128 entries 0 .. p/128 - 1 and the raw rows raw_lo(p) .. p: one decode step for n = 1, the same
+ * numbers as decoding token by token for any n.
+ * Uses shape->B, H, d, W, tail_mode, comp_mask, dtype, attn_kernel, the capacities and the paging;
+ * n_sel must be 0 (selection lists belong to rounds).
+ *   n_new, starts as in tv_chunk_append; Q [n_new][H][d] in; O [n_new][H][d] out (dtype); lse
+ *   [n_new][H] fp32 out: natural-log sum of exp(logits); rows of no request are left alone
+ *   Q, O and the caches 16-byte aligned; workspace: device buffer of ws_bytes >=
+ *   tv_chunk_workspace_size(shape, n_new), 256-byte aligned; calls that overlap on the GPU need one
+ *   each.
+ * Host errors: TV_ERR_ARG, TV_ERR_SHAPE, TV_ERR_WORKSPACE, TV_ERR_DTYPE (TV_ATTN_TCGEN05 asked for
+ * an unsupported shape).
+ * Device errors, that request's rows left alone: TV_ERR_ARG (starts that descend or leave 0 ..
+ * n_new, L < n), TV_ERR_CAPACITY (L > raw_cap or more entries than cap_m); TV_ERR_ARG for a page
+ * that is missing (page 0 is read instead); TV_ERR_TIMEOUT.
+ */
+size_t tv_chunk_workspace_size(const tv_shape* shape, int32_t n_new);
+int tv_chunk_attn(const tv_shape* shape, int32_t n_new, const int32_t* starts, const void* Q,
+                  const void* c4K, const void* c4V, const void* c128K, const void* c128V,
+                  const void* rawK, const void* rawV, const int32_t* L, float scale, void* O,
+                  float* lse, void* workspace, size_t ws_bytes, int32_t* status,
+                  tv_stream_t stream);
+
+/*
+ * Beam search's selection over beams and vocabulary, in the slots that tv_pages_fork reorders the
+ * cache by (the report keeps one sequence per request; a draft tree's levels are grown the same
+ * way).  The B slots are B / width groups of `width` neighbours, each slot a beam.  With x the logits
+ * of slot b and ln p as in tv_token_logprobs, slot b's candidates are its tokens t with x[t] > -inf
+ * and score scores[b] + ln p(t); a beam that has ended (done[b] != 0) has one, itself: token eos at
+ * score scores[b].  A score of -inf: an empty slot, no candidates.  The `width` best candidates of
+ * the group go on (equal scores: the lower slot first, then the lower id; scores are compared in
+ * fp64): a beam with candidates among them keeps its best in its own slot, the others fill the
+ * group's free slots in ascending order, best first.  Per slot:
+ *   source [B] int32: the slot it continues (0 .. B-1), -1 if candidates ran out: what tv_pages_fork
+ *          takes, which copies and releases the pages; token [B] int32 (-1 without a source);
+ *          new_scores [B] fp32 (-inf without a source); new_done [B] int32: 1 if the source had
+ *          ended or the token is eos, else 0; rank [B] int32: its place in the group, 0 the best
+ *          (-1 without a source)
+ *   Uses shape->B and comp_mask..dtype only for validation.  width 1..32 dividing B; vocab, ld,
+ *   logits_dtype, logits (one row per slot) and scale as in tv_token_logprobs; scores [B] fp32 in;
+ *   done [B] int32 in (nullable: none has ended; eos is then only compared with); new_scores may be
+ *   scores and new_done may be done; new_done and rank are nullable.
+ *   workspace: device buffer of ws_bytes >= tv_beam_workspace_size(shape, width), 256-byte aligned;
+ *   calls that overlap on the GPU need one each.
+ * Device errors: TV_ERR_VALUE (a NaN or +inf among the logits of a slot with a score, or such a
+ * score: that slot has no candidates).
+ */
+size_t tv_beam_workspace_size(const tv_shape* shape, int32_t width);
+int tv_beam_select(const tv_shape* shape, int32_t width, int32_t vocab, int64_t ld,
+                   int32_t logits_dtype, const void* logits, const float* scores,
+                   const int32_t* done, int32_t eos, float scale, int32_t* source, int32_t* token,
+                   float* new_scores, int32_t* new_done, int32_t* rank, void* workspace,
+                   size_t ws_bytes, int32_t* status, tv_stream_t stream);
 
 /*
  * Testing aid for the failure path of the tensor-core attention (the report has no counterpart).

@@ -27,6 +27,8 @@ round     one full verify round: the five steps above in order
 indexer   top-k selection of persistent C4 entries by an fp32 indexer score (sparse C4 path)
 logprobs  from logits to target tokens, alternatives, log probabilities and entropy
 pages     branching, reserving and compacting the pages of the pools
+chunk     new tokens behind a prefix: rotated rows, entries, attention
+beam      selection over beams and vocabulary, slot by slot
 
 Parity status: every function here is pinned by the ``-m "not gpu"`` tests
 (``tests/test_oracle_*.py``) against brute force, closed forms, special cases or library
@@ -49,7 +51,7 @@ from .refresh import refresh_commit_request
 from .round import verify_round
 from .indexer import index_scores, topk_ascending, indexer_select
 from .logprobs import row_logprobs, row_order, token_logprobs
-from . import pages
+from . import beam, chunk, pages
 
 __all__ = [
     "round_to_storage",
@@ -75,4 +77,6 @@ __all__ = [
     "row_order",
     "token_logprobs",
     "pages",
+    "chunk",
+    "beam",
 ]

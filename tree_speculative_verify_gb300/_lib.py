@@ -27,6 +27,7 @@ TV_TAIL_WINDOW, TV_TAIL_REMAINDER = 0, 1
 TV_COMP_C4, TV_COMP_C128 = 1, 2
 TV_F32, TV_BF16 = 0, 1
 TV_ATTN_AUTO, TV_ATTN_SIMT, TV_ATTN_TCGEN05 = 0, 1, 2
+TV_ROPE_HALVES, TV_ROPE_PAIRS = 0, 1
 _LOGIT_TYPES = {torch.float32: TV_F32, torch.bfloat16: TV_BF16}
 
 EXPORTS = (
@@ -36,7 +37,8 @@ EXPORTS = (
     "tv_tree_verify_attn", "tv_accept_walk", "tv_refresh_commit", "tv_tree_verify_attn_noalloc",
     "tv_indexer_workspace_size", "tv_indexer_topk", "tv_debug_attn_timeout", "tv_noalloc_prepare",
     "tv_token_logprobs", "tv_pages_workspace_size", "tv_pages_fork", "tv_pages_reserve",
-    "tv_pages_compact",
+    "tv_pages_compact", "tv_chunk_append", "tv_chunk_workspace_size", "tv_chunk_attn",
+    "tv_beam_workspace_size", "tv_beam_select",
 )
 
 
@@ -91,6 +93,16 @@ _SIGS = {
                       ctypes.c_int),
     "tv_pages_reserve": ([_SHAPE] + [_P] * 4 + [ctypes.c_size_t, _P, _P], ctypes.c_int),
     "tv_pages_compact": ([_SHAPE] + [_P] * 11 + [ctypes.c_size_t, _P, _P], ctypes.c_int),
+    "tv_chunk_append": ([_SHAPE, ctypes.c_int32] + [_P] * 3 + [ctypes.c_int64, _P, ctypes.c_int32,
+                                                               ctypes.c_int32] + [_P] * 13,
+                        ctypes.c_int),
+    "tv_chunk_workspace_size": ([_SHAPE, ctypes.c_int32], ctypes.c_size_t),
+    "tv_chunk_attn": ([_SHAPE, ctypes.c_int32] + [_P] * 9 + [ctypes.c_float, _P, _P, _P,
+                                                             ctypes.c_size_t, _P, _P], ctypes.c_int),
+    "tv_beam_workspace_size": ([_SHAPE, ctypes.c_int32], ctypes.c_size_t),
+    "tv_beam_select": ([_SHAPE, ctypes.c_int32, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32]
+                       + [_P] * 3 + [ctypes.c_int32, ctypes.c_float] + [_P] * 6
+                       + [ctypes.c_size_t, _P, _P], ctypes.c_int),
 }
 
 
@@ -380,6 +392,110 @@ def tv_pages_compact(shape, L, page_refs, rawK, rawV, c4K, c4V, c128K, c128V, re
         ws_bytes, _a(status, i32, 1, "status", dev), _s(stream, dev))
     if rc:
         _check("tv_pages_compact", rc)
+
+
+def _layers(shape, rawK, rawV, c4K, c4V, c128K, c128V, dev):
+    """Addresses of the cache's layers, contiguous [B][cap][d] or pools."""
+    if shape.page_tokens:
+        return _pools(shape, rawK, rawV, c4K, c4V, c128K, c128V, dev)
+    dt = torch.bfloat16 if shape.dtype == TV_BF16 else torch.float32
+    mask, row = shape.comp_mask, shape.B * shape.d
+    n = shape.raw_cap * row
+    n4 = shape.c4_cap * row if mask & TV_COMP_C4 else 0
+    n128 = shape.c128_cap * row if mask & TV_COMP_C128 else 0
+    return (_a(rawK, dt, n, "rawK", dev), _a(rawV, dt, n, "rawV", dev), _a(c4K, dt, n4, "c4K", dev),
+            _a(c4V, dt, n4, "c4V", dev), _a(c128K, dt, n128, "c128K", dev),
+            _a(c128V, dt, n128, "c128V", dev))
+
+
+def tv_chunk_append(shape, starts, K, V, Q, rope_dim, rope_pairs, inv_freq, g4, g128, Qr, rawK, rawV,
+                    c4K, c4V, c128K, c128V, L, status, stream=None):
+    """``K``, ``V``: [n_new][d] with unit last stride, both with the same row stride (slices of a wider
+    projection's output, say); ``Q``, ``Qr``: [n_new][H][d] or None; ``inv_freq``: [rope_dim / 2]
+    fp32 or None."""
+    lib, dev, d = _lib or load(), _here(), shape.d
+    dt = torch.bfloat16 if shape.dtype == TV_BF16 else torch.float32
+    f32, i32 = torch.float32, torch.int32
+    for t, name in ((K, "K"), (V, "V")):
+        if t.get_device() != dev:
+            raise ValueError(f"{name}: the tensor must live on the current CUDA device")
+        if t.dtype != dt:
+            raise TypeError(f"{name}: expected {dt}, got {t.dtype}")
+        if t.dim() != 2 or t.shape[1] != d or t.shape[0] != K.shape[0]:
+            raise ValueError(f"{name}: expected [n_new][{d}], got {tuple(t.shape)}")
+        if t.stride(1) != 1 or (t.shape[0] > 1 and t.stride(0) != K.stride(0)):
+            raise ValueError(f"{name}: rows must be contiguous and as far apart as K's")
+    n = K.shape[0]
+    ld = K.stride(0) if n > 1 else d
+    rc = lib.tv_chunk_append(
+        ctypes.byref(shape), n, _a(starts, i32, shape.B + 1, "starts", dev), K.data_ptr(),
+        V.data_ptr(), ld, _a(Q, dt, n * shape.H * d, "Q", dev), rope_dim, rope_pairs,
+        _a(inv_freq, f32, rope_dim // 2, "inv_freq", dev), _a(g4, f32, d, "g4", dev),
+        _a(g128, f32, d, "g128", dev), _a(Qr, dt, n * shape.H * d, "Qr", dev),
+        *_layers(shape, rawK, rawV, c4K, c4V, c128K, c128V, dev), _a(L, i32, shape.B, "L", dev),
+        _a(status, i32, 1, "status", dev), _s(stream, dev))
+    if rc:
+        _check("tv_chunk_append", rc)
+
+
+def tv_chunk_workspace_size(shape, n_new):
+    return int(load().tv_chunk_workspace_size(ctypes.byref(shape), n_new))
+
+
+def tv_chunk_attn(shape, starts, Q, c4K, c4V, c128K, c128V, rawK, rawV, L, scale, O, lse, workspace,
+                  status, stream=None):
+    """``Q``, ``O``: [n_new][H][d]; ``lse``: [n_new][H]."""
+    lib, dev, i32 = _lib or load(), _here(), torch.int32
+    dt = torch.bfloat16 if shape.dtype == TV_BF16 else torch.float32
+    if Q.dim() != 3 or Q.shape[1] != shape.H or Q.shape[2] != shape.d:
+        raise ValueError(f"Q: expected [n_new][{shape.H}][{shape.d}], got {tuple(Q.shape)}")
+    n = Q.shape[0]
+    ws = None if workspace is None else _a(workspace, workspace.dtype, 0, "workspace", dev)
+    ws_bytes = 0 if ws is None else workspace.numel() * workspace.element_size()
+    rawK, rawV, c4K, c4V, c128K, c128V = _layers(shape, rawK, rawV, c4K, c4V, c128K, c128V, dev)
+    rc = lib.tv_chunk_attn(
+        ctypes.byref(shape), n, _a(starts, i32, shape.B + 1, "starts", dev),
+        _a(Q, dt, n * shape.H * shape.d, "Q", dev), c4K, c4V, c128K, c128V, rawK, rawV,
+        _a(L, i32, shape.B, "L", dev), scale, _a(O, dt, n * shape.H * shape.d, "O", dev),
+        _a(lse, torch.float32, n * shape.H, "lse", dev), ws, ws_bytes,
+        _a(status, i32, 1, "status", dev), _s(stream, dev))
+    if rc:
+        _check("tv_chunk_attn", rc)
+
+
+def tv_beam_workspace_size(shape, width):
+    return int(load().tv_beam_workspace_size(ctypes.byref(shape), width))
+
+
+def tv_beam_select(shape, width, logits, scores, done, eos, scale, source, token, new_scores, new_done,
+                   rank, workspace, status, stream=None):
+    """``logits``: [B][vocab] fp32 or bf16 with unit last stride, the rows at least the vocabulary
+    apart; ``done``, ``new_done`` and ``rank`` may be None."""
+    lib, dev, B, i32, f32 = _lib or load(), _here(), shape.B, torch.int32, torch.float32
+    size = logits.shape
+    if len(size) != 2 or size[0] != B:
+        raise ValueError(f"logits: expected [{B}][vocab], got {tuple(size)}")
+    if logits.get_device() != dev:
+        raise ValueError("logits: the tensor must live on the current CUDA device")
+    dtype = _LOGIT_TYPES.get(logits.dtype)
+    if dtype is None:
+        raise TypeError(f"logits: expected float32 or bfloat16, got {logits.dtype}")
+    vocab, (ld, unit) = size[1], logits.stride()
+    if B <= 1:
+        ld = vocab
+    if (unit != 1 and vocab > 1) or ld < vocab:
+        raise ValueError(f"logits: rows must be contiguous, strides {logits.stride()}")
+    ws = None if workspace is None else _a(workspace, workspace.dtype, 0, "workspace", dev)
+    ws_bytes = 0 if ws is None else workspace.numel() * workspace.element_size()
+    rc = lib.tv_beam_select(
+        ctypes.byref(shape), width, vocab, ld, dtype, logits.data_ptr(),
+        _a(scores, f32, B, "scores", dev), _a(done, i32, B, "done", dev), eos, scale,
+        _a(source, i32, B, "source", dev), _a(token, i32, B, "token", dev),
+        _a(new_scores, f32, B, "new_scores", dev), _a(new_done, i32, B, "new_done", dev),
+        _a(rank, i32, B, "rank", dev), ws, ws_bytes, _a(status, i32, 1, "status", dev),
+        _s(stream, dev))
+    if rc:
+        _check("tv_beam_select", rc)
 
 
 def tv_debug_attn_timeout(timeout_ns, withhold_tile):

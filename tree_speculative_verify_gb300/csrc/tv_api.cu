@@ -146,6 +146,21 @@ int tv_launch_reserve(const tv_shape* s, const int32_t* need, const int32_t* L, 
 int tv_launch_compact(const tv_shape* s, const int32_t* L, int32_t* refs, void* const pools[6],
                       int32_t* remap, int32_t* n_live, void* workspace, int32_t* status,
                       cudaStream_t stream);
+int tv_launch_append(const tv_shape* s, int n_new, const int32_t* starts, const void* K,
+                     const void* V, int64_t ld_kv, const void* Q, int rope_dim, int rope_pairs,
+                     const float* inv_freq, const float* g4, const float* g128, void* Qr,
+                     void* rawK, void* rawV, void* c4K, void* c4V, void* c128K, void* c128V,
+                     int32_t* L, int32_t* status, cudaStream_t stream);
+int tv_launch_chunk_attn(const tv_shape* s, int n_new, const int32_t* starts, const void* Q,
+                         const void* c4K, const void* c4V, const void* c128K, const void* c128V,
+                         const void* rawK, const void* rawV, const int32_t* L, float scale,
+                         void* O, float* lse, int32_t* status, cudaStream_t stream);
+size_t tv_beam_workspace(const tv_shape* s, int width);
+int tv_launch_beam(const tv_shape* s, int width, int vocab, int64_t ld, int logits_dtype,
+                   const void* logits, const float* scores, const int32_t* done, int eos,
+                   float scale, int32_t* source, int32_t* token, float* new_scores,
+                   int32_t* new_done, int32_t* rank, void* workspace, int32_t* status,
+                   cudaStream_t stream);
 
 // ---- split-KV geometry of the SIMT kernel -----------------------------------------------------
 struct SimtPlan {
@@ -662,4 +677,161 @@ extern "C" int tv_pages_compact(const tv_shape* s, const int32_t* L, int32_t* pa
   if (int rc = page_pools(s, fn, rawK, rawV, c4K, c4V, c128K, c128V, pools)) return rc;
   return tv_launch_compact(s, L, page_refs, pools, remap, n_live, workspace, status,
                            (cudaStream_t)stream);
+}
+
+// ---- chunks of new tokens ---------------------------------------------------------------------------
+// Checks shared by the tv_chunk_* calls; starts may only be missing where nothing reads it.
+static int check_chunk(const tv_shape* s, const char* fn, int32_t n_new, const int32_t* starts) {
+  if (n_new < 0 || n_new > (1 << 30) || (int64_t)n_new * s->H >= ((int64_t)1 << 31))
+    return tv_set_error(TV_ERR_SHAPE, "%s: n_new = %d outside 0..2^30 or n_new * H >= 2^31", fn, n_new);
+  if (s->B == 0) return TV_OK;
+  TV_REQUIRE(starts, fn);
+  return TV_OK;
+}
+
+// Null and alignment checks of the cache's layers (rows are moved 16 bytes at a time).
+static int check_layers(const tv_shape* s, const char* fn, const void* rawK, const void* rawV,
+                        const void* c4K, const void* c4V, const void* c128K, const void* c128V) {
+  TV_REQUIRE(rawK, fn);
+  TV_REQUIRE(rawV, fn);
+  uintptr_t bits = (uintptr_t)rawK | (uintptr_t)rawV;
+  if (has_c4(s)) {
+    TV_REQUIRE(c4K, fn);
+    TV_REQUIRE(c4V, fn);
+    bits |= (uintptr_t)c4K | (uintptr_t)c4V;
+  }
+  if (has_c128(s)) {
+    TV_REQUIRE(c128K, fn);
+    TV_REQUIRE(c128V, fn);
+    bits |= (uintptr_t)c128K | (uintptr_t)c128V;
+  }
+  if (bits & 15u) return tv_set_error(TV_ERR_ARG, "%s: the caches must be 16-byte aligned", fn);
+  return TV_OK;
+}
+
+extern "C" int tv_chunk_append(const tv_shape* s, int32_t n_new, const int32_t* starts,
+                               const void* K, const void* V, int64_t ld_kv, const void* Q,
+                               int32_t rope_dim, int32_t rope_pairs, const float* inv_freq,
+                               const float* g4, const float* g128, void* Qr, void* rawK,
+                               void* rawV, void* c4K, void* c4V, void* c128K, void* c128V,
+                               int32_t* L, int32_t* status, tv_stream_t stream) {
+  const char* fn = "tv_chunk_append";
+  if (int rc = check_shape(s, fn)) return rc;
+  if (int rc = check_chunk(s, fn, n_new, starts)) return rc;
+  if (rope_dim < 0 || rope_dim > s->d || rope_dim % 2 != 0)
+    return tv_set_error(TV_ERR_SHAPE, "%s: rope_dim = %d is not even in 0..d", fn, rope_dim);
+  if (rope_pairs != TV_ROPE_HALVES && rope_pairs != TV_ROPE_PAIRS)
+    return tv_set_error(TV_ERR_ARG, "%s: unknown rope_pairs %d", fn, rope_pairs);
+  const int es = s->dtype == TV_BF16 ? 2 : 4;
+  if (ld_kv < s->d || ld_kv > ((int64_t)1 << 40) || (ld_kv * es) % 16 != 0)
+    return tv_set_error(TV_ERR_SHAPE, "%s: ld_kv = %lld < d or not a multiple of 16 bytes", fn,
+                        (long long)ld_kv);
+  if (s->B == 0) return TV_OK;
+  TV_REQUIRE(L, fn);
+  TV_REQUIRE(status, fn);
+  if (int rc = check_layers(s, fn, rawK, rawV, c4K, c4V, c128K, c128V)) return rc;
+  if (has_c4(s)) TV_REQUIRE(g4, fn);
+  if (has_c128(s)) TV_REQUIRE(g128, fn);
+  if (n_new > 0) {
+    TV_REQUIRE(K, fn);
+    TV_REQUIRE(V, fn);
+    if (rope_dim > 0) TV_REQUIRE(inv_freq, fn);
+    if (Q != nullptr) TV_REQUIRE(Qr, fn);
+    if (((uintptr_t)K | (uintptr_t)V | (uintptr_t)Q | (uintptr_t)(Q ? Qr : nullptr)) & 15u)
+      return tv_set_error(TV_ERR_ARG, "%s: K, V, Q and Qr must be 16-byte aligned", fn);
+  }
+  return tv_launch_append(s, n_new, starts, K, V, ld_kv, Q, rope_dim, rope_pairs, inv_freq, g4, g128,
+                          Qr, rawK, rawV, c4K, c4V, c128K, c128V, L, status, (cudaStream_t)stream);
+}
+
+extern "C" size_t tv_chunk_workspace_size(const tv_shape* s, int32_t n_new) {
+  const char* fn = "tv_chunk_workspace_size";
+  if (check_shape(s, fn) != TV_OK || s->B == 0 || n_new <= 0) return 0;
+  if ((int64_t)n_new * s->H >= ((int64_t)1 << 31)) {
+    tv_set_error(TV_ERR_SHAPE, "%s: n_new * H >= 2^31", fn);
+    return 0;
+  }
+  return 256;
+}
+
+extern "C" int tv_chunk_attn(const tv_shape* s, int32_t n_new, const int32_t* starts, const void* Q,
+                             const void* c4K, const void* c4V, const void* c128K,
+                             const void* c128V, const void* rawK, const void* rawV,
+                             const int32_t* L, float scale, void* O, float* lse, void* workspace,
+                             size_t ws_bytes, int32_t* status, tv_stream_t stream) {
+  const char* fn = "tv_chunk_attn";
+  if (int rc = check_shape(s, fn)) return rc;
+  if (int rc = check_chunk(s, fn, n_new, starts)) return rc;
+  if (s->n_sel != 0)
+    return tv_set_error(TV_ERR_ARG, "%s: n_sel = %d, selection lists belong to rounds", fn, s->n_sel);
+  if (!(scale > 0.f) || !(scale < 1e30f))
+    return tv_set_error(TV_ERR_ARG, "%s: scale must be a positive finite number", fn);
+  if (s->B == 0 || n_new == 0) return TV_OK;
+  TV_REQUIRE(Q, fn);
+  TV_REQUIRE(L, fn);
+  TV_REQUIRE(O, fn);
+  TV_REQUIRE(lse, fn);
+  TV_REQUIRE(status, fn);
+  if (int rc = check_layers(s, fn, rawK, rawV, c4K, c4V, c128K, c128V)) return rc;
+  if (((uintptr_t)Q | (uintptr_t)O) & 15u)
+    return tv_set_error(TV_ERR_ARG, "%s: Q and O must be 16-byte aligned", fn);
+  TV_REQUIRE(workspace, fn);
+  if (((uintptr_t)workspace) % 256 != 0)
+    return tv_set_error(TV_ERR_ARG, "%s: workspace must be 256-byte aligned", fn);
+  const size_t need = tv_chunk_workspace_size(s, n_new);
+  if (ws_bytes < need)
+    return tv_set_error(TV_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", fn, ws_bytes,
+                        need);
+  return tv_launch_chunk_attn(s, n_new, starts, Q, c4K, c4V, c128K, c128V, rawK, rawV, L, scale, O,
+                              lse, status, (cudaStream_t)stream);
+}
+
+// ---- beams ------------------------------------------------------------------------------------------
+static int check_width(const tv_shape* s, const char* fn, int32_t width) {
+  if (width < 1 || width > 32 || s->B % width != 0)
+    return tv_set_error(TV_ERR_SHAPE, "%s: width = %d outside 1..32 or no divisor of B = %d", fn,
+                        width, s->B);
+  return TV_OK;
+}
+
+extern "C" size_t tv_beam_workspace_size(const tv_shape* s, int32_t width) {
+  const char* fn = "tv_beam_workspace_size";
+  if (check_shape(s, fn) != TV_OK || check_width(s, fn, width) != TV_OK || s->B == 0) return 0;
+  return tv_beam_workspace(s, width);
+}
+
+extern "C" int tv_beam_select(const tv_shape* s, int32_t width, int32_t vocab, int64_t ld,
+                              int32_t logits_dtype, const void* logits, const float* scores,
+                              const int32_t* done, int32_t eos, float scale, int32_t* source,
+                              int32_t* token, float* new_scores, int32_t* new_done, int32_t* rank,
+                              void* workspace, size_t ws_bytes, int32_t* status,
+                              tv_stream_t stream) {
+  const char* fn = "tv_beam_select";
+  if (int rc = check_shape(s, fn)) return rc;
+  if (int rc = check_width(s, fn, width)) return rc;
+  if (vocab < 1 || vocab > (1 << 30) || ld < vocab || ld > ((int64_t)1 << 40))
+    return tv_set_error(TV_ERR_SHAPE, "%s: vocab = %d outside 1..2^30 or ld = %lld < vocab", fn, vocab,
+                        (long long)ld);
+  if (logits_dtype != TV_F32 && logits_dtype != TV_BF16)
+    return tv_set_error(TV_ERR_ARG, "%s: unknown logits_dtype %d", fn, logits_dtype);
+  if (!(scale > 0.f) || !(scale < 1e30f))
+    return tv_set_error(TV_ERR_ARG, "%s: scale must be a positive finite number", fn);
+  if (s->B == 0) return TV_OK;
+  TV_REQUIRE(logits, fn);
+  TV_REQUIRE(scores, fn);
+  TV_REQUIRE(source, fn);
+  TV_REQUIRE(token, fn);
+  TV_REQUIRE(new_scores, fn);
+  TV_REQUIRE(status, fn);
+  if ((uintptr_t)logits % (logits_dtype == TV_BF16 ? 2 : 4) != 0)
+    return tv_set_error(TV_ERR_ARG, "%s: logits must be aligned to their type", fn);
+  TV_REQUIRE(workspace, fn);
+  if (((uintptr_t)workspace) % 256 != 0)
+    return tv_set_error(TV_ERR_ARG, "%s: workspace must be 256-byte aligned", fn);
+  const size_t need = tv_beam_workspace(s, width);
+  if (ws_bytes < need)
+    return tv_set_error(TV_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", fn, ws_bytes,
+                        need);
+  return tv_launch_beam(s, width, vocab, ld, logits_dtype, logits, scores, done, eos, scale, source,
+                        token, new_scores, new_done, rank, workspace, status, (cudaStream_t)stream);
 }

@@ -1,0 +1,155 @@
+// Beam search's selection over beams and vocabulary.
+//
+// tv_token_logprobs' kernel reads the logits once and leaves every beam's `width` best tokens with
+// their log probabilities in the workspace; no other token of a beam can be among its group's
+// `width` best.  A warp per group then merges the beams' lists, which are sorted: lane w holds the
+// head of beam w's list, and `width` times the best head goes on.
+//
+// A candidate's score is scores[w] + scale (x - m) - ln S, with m the beam's largest logit and ln S
+// the log of its sum relative to m, which is what the log probability of m itself is (up to sign).
+// Both x and m are exact and the sum is taken in fp64, so the only rounding between two beams is that
+// of ln S in fp32 (2^-24 of a number of a few units); within a beam the order is the logits'.
+#include <math.h>
+
+#include "tv_common.cuh"
+
+int tv_launch_logprobs(const tv_shape* s, int vocab, int64_t ld, int logits_dtype,
+                       const void* logits, int n_tok, const int32_t* tokens, const int32_t* nodes,
+                       float scale, int n_top, float* lse, float* entropy, float* logprobs,
+                       int32_t* top_ids, float* top_logprobs, int32_t* target, int32_t* status,
+                       cudaStream_t stream);
+
+namespace tv {
+
+constexpr int kMaxWidth = 32;
+
+struct BeamArgs {
+  int B, width, eos;
+  int64_t ld;
+  float scale;
+  const float* scores;
+  const int32_t* done;
+  const int32_t* ids;      // [B][width] every beam's best tokens, -1: none
+  const float* logprobs;   // [B][width]
+  int32_t* source;
+  int32_t* token;
+  float* new_scores;
+  int32_t* new_done;
+  int32_t* rank;
+  int32_t* status;
+};
+
+template <typename T>
+__global__ void __launch_bounds__(32) beam_kernel(BeamArgs a, const T* logits) {
+  __shared__ double score[kMaxWidth][kMaxWidth];
+  __shared__ int32_t id[kMaxWidth][kMaxWidth];
+  const int lane = threadIdx.x, W = a.width, first = blockIdx.x * W;
+  pdl_wait();
+  // the beams' candidates; what a group reads of scores and done is read before it writes them
+  const bool beam = lane < W;
+  const float mine = beam ? a.scores[first + lane] : -INFINITY;
+  const bool over = beam && a.done != nullptr && a.done[first + lane] != 0;
+  bool bad = beam && (!(mine == mine) || mine == INFINITY);
+  for (int w = 0; w < W; ++w) {
+    const int64_t b = first + w;
+    const float sum = __shfl_sync(0xffffffffu, mine, w);
+    const bool ended = __shfl_sync(0xffffffffu, (int)over, w);
+    const bool counts = sum > -INFINITY && sum < INFINITY;
+    const int top = a.ids[b * W];
+    const float lp = a.logprobs[b * W];
+    if (lane == w && counts && !ended && !(lp == lp)) bad = true;   // (its ids are -1)
+    if (lane < W) {
+      int t = -1;
+      double s = -INFINITY;
+      if (counts && ended && lane == 0) {
+        t = a.eos;
+        s = sum;
+      } else if (counts && !ended && top >= 0) {
+        t = a.ids[b * W + lane];
+        if (t >= 0) {
+          const T* row = logits + b * a.ld;
+          s = (double)sum + ((double)a.scale * ((double)load_f(row + t) - (double)load_f(row + top)) +
+                             (double)lp);
+        }
+      }
+      score[w][lane] = s;
+      id[w][lane] = t;
+    }
+  }
+  if (bad) record_error(a.status, TV_ERR_VALUE);
+  __syncwarp();
+  // the `width` best: lane k keeps the k-th
+  int head = 0, from = -1, tok = -1;
+  double best = -INFINITY;
+  for (int k = 0; k < W; ++k) {
+    double s = beam && head < W ? score[lane][head] : -INFINITY;
+    int w = lane;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const double s2 = __shfl_xor_sync(0xffffffffu, s, o);
+      const int w2 = __shfl_xor_sync(0xffffffffu, w, o);
+      if (s2 > s || (s2 == s && w2 < w)) {
+        s = s2;
+        w = w2;
+      }
+    }
+    if (!(s > -INFINITY)) break;   // candidates have run out
+    const int at = __shfl_sync(0xffffffffu, head, w);
+    if (lane == k) {
+      best = s;
+      from = w;
+      tok = id[w][at];
+    }
+    if (lane == w) ++head;
+  }
+  // slots: a beam's best continuation (the first of it) stays, the others fill the free ones
+  const unsigned lower = (1u << lane) - 1u, all = W == 32 ? ~0u : (1u << W) - 1u;
+  const unsigned same = __match_any_sync(0xffffffffu, from);
+  const bool stays = from >= 0 && (same & lower) == 0;
+  const unsigned taken = __reduce_or_sync(0xffffffffu, stays ? 1u << from : 0u);
+  const unsigned moves = __ballot_sync(0xffffffffu, beam && !stays);
+  int slot = from;
+  if (beam && !stays) slot = (int)__fns(all & ~taken, 0, __popc(moves & lower) + 1);
+  const bool was = __shfl_sync(0xffffffffu, (int)over, from >= 0 ? from : 0);
+  if (!beam) return;
+  const int b = first + slot;
+  a.source[b] = from >= 0 ? first + from : -1;
+  a.token[b] = tok;
+  a.new_scores[b] = (float)best;
+  if (a.new_done) a.new_done[b] = from >= 0 && (was || tok == a.eos) ? 1 : 0;
+  if (a.rank) a.rank[b] = from >= 0 ? lane : -1;
+}
+
+}  // namespace tv
+
+size_t tv_beam_workspace(const tv_shape* s, int width) {
+  return ((size_t)s->B * width * 8 + 255) / 256 * 256;
+}
+
+int tv_launch_beam(const tv_shape* s, int width, int vocab, int64_t ld, int logits_dtype,
+                   const void* logits, const float* scores, const int32_t* done, int eos,
+                   float scale, int32_t* source, int32_t* token, float* new_scores,
+                   int32_t* new_done, int32_t* rank, void* workspace, int32_t* status,
+                   cudaStream_t stream) {
+  tv_shape rows = *s;
+  rows.D = 1;
+  int32_t* ids = (int32_t*)workspace;
+  float* logprobs = (float*)(ids + (size_t)s->B * width);
+  if (int rc = tv_launch_logprobs(&rows, vocab, ld, logits_dtype, logits, 0, nullptr, nullptr, scale,
+                                  width, nullptr, nullptr, nullptr, ids, logprobs, nullptr, nullptr,
+                                  stream))
+    return rc;
+  const tv::BeamArgs a = {s->B, width, eos, ld, scale, scores, done, ids, logprobs, source, token,
+                          new_scores, new_done, rank, status};
+  const dim3 grid(s->B / width);
+  const cudaError_t e =
+      logits_dtype == TV_BF16
+          ? tv::launch_pdl(tv::beam_kernel<__nv_bfloat16>, grid, dim3(32), 0, stream, a,
+                           (const __nv_bfloat16*)logits)
+          : tv::launch_pdl(tv::beam_kernel<float>, grid, dim3(32), 0, stream, a, (const float*)logits);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return tv_set_error(TV_ERR_CUDA, "tv_beam_select: launch failed: %s", cudaGetErrorString(e));
+  }
+  return tv_check_launch("tv_beam_select");
+}

@@ -316,6 +316,66 @@ def compact(shape, st, rb, remap, n_live, stream=None):
                           st.c128V, remap, n_live, st.page_ws, rb.status, stream)
 
 
+def append(shape, st, rb, starts, K, V, Q=None, rope_dim=0, rope_pairs=_lib.TV_ROPE_HALVES,
+           inv_freq=None, Qr=None, stream=None):
+    """New tokens behind the committed ones of every request: rows ``starts[b]`` to ``starts[b + 1]`` of
+    ``K`` and ``V`` [n][d] (see tv_chunk_append).  Their positions need pages on a managed pool
+    (``reserve``).  Rotates the queries ``Q`` [n][H][d] into ``Qr`` (default: in place)."""
+    _lib.tv_chunk_append(shape, starts, K, V, Q, rope_dim, rope_pairs, inv_freq, rb.g4, rb.g128,
+                         Q if Qr is None else Qr, st.rawK, st.rawV, st.c4K, st.c4V, st.c128K,
+                         st.c128V, st.L, rb.status, stream)
+
+
+def alloc_chunk(shape, n_new, device="cuda"):
+    """Workspace of ``chunk_attention`` for up to ``n_new`` new tokens."""
+    return torch.empty(max(_lib.tv_chunk_workspace_size(shape, n_new), 256), dtype=torch.uint8,
+                       device=device)
+
+
+def chunk_attention(shape, st, rb, starts, Q, workspace, O=None, lse=None, scale=None, stream=None):
+    """Attention of the tokens that ``append`` just added, rows as there; returns (O, lse)."""
+    O = torch.empty_like(Q) if O is None else O
+    lse = torch.empty(Q.shape[:2], dtype=torch.float32, device=Q.device) if lse is None else lse
+    _lib.tv_chunk_attn(shape, starts, Q, st.c4K, st.c4V, st.c128K, st.c128V, st.rawK, st.rawV, st.L,
+                       1.0 / math.sqrt(shape.d) if scale is None else scale, O, lse, workspace,
+                       rb.status, stream)
+    return O, lse
+
+
+@dataclass
+class Beams:
+    """Beam search over a managed pool: ``width`` neighbouring slots are one group.  ``scores`` starts
+    as 0 in a group's first slot and -inf in the others (they become copies of it)."""
+    width: int
+    eos: int
+    scores: torch.Tensor      # [B] fp32
+    done: torch.Tensor        # [B] int32
+    source: torch.Tensor      # [B] int32, what tv_pages_fork takes
+    token: torch.Tensor       # [B] int32, the tokens to append next
+    rank: torch.Tensor        # [B] int32
+    workspace: torch.Tensor
+
+
+def alloc_beams(shape, width, eos, device="cuda"):
+    i = lambda: torch.zeros(shape.B, dtype=torch.int32, device=device)
+    scores = torch.full((shape.B,), -math.inf, dtype=torch.float32, device=device)
+    scores[::width] = 0.0
+    ws = torch.empty(max(_lib.tv_beam_workspace_size(shape, width), 256), dtype=torch.uint8,
+                     device=device)
+    return Beams(width=width, eos=eos, scores=scores, done=i(), source=i(), token=i(), rank=i(),
+                 workspace=ws)
+
+
+def beam_step(shape, st, rb, beams, logits, scale=1.0, stream=None):
+    """Selects the groups' best continuations from ``logits`` [B][vocab] (the rows of done and empty
+    slots do not count) and reorders the pool's pages by them: slot b then holds the cache of the
+    beam that ``beams.token[b]`` continues."""
+    _lib.tv_beam_select(shape, beams.width, logits, beams.scores, beams.done, beams.eos, scale,
+                        beams.source, beams.token, beams.scores, beams.done, beams.rank,
+                        beams.workspace, rb.status, stream)
+    fork(shape, st, rb, beams.source, None, stream)
+
+
 def verify_round(shape, st, rb, scale=None, stream=None, commit=True, select=False, scored=False,
                  inv_temperature=1.0):
     """One target-verify round: plan, scratch pad, attention, acceptance, refresh; with
