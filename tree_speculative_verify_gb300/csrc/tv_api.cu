@@ -744,6 +744,12 @@ extern "C" int tv_chunk_append(const tv_shape* s, int32_t n_new, const int32_t* 
                           Qr, rawK, rawV, c4K, c4V, c128K, c128V, L, status, (cudaStream_t)stream);
 }
 
+static bool chunk_tc_supported(const tv_shape* s) { return tv_chunk_tc_ok(s) && tv_tc_available(); }
+static bool chunk_use_tc(const tv_shape* s) {
+  if (s->attn_kernel == TV_ATTN_SIMT) return false;
+  return s->attn_kernel == TV_ATTN_TCGEN05 || chunk_tc_supported(s);
+}
+
 extern "C" size_t tv_chunk_workspace_size(const tv_shape* s, int32_t n_new) {
   const char* fn = "tv_chunk_workspace_size";
   if (check_shape(s, fn) != TV_OK || s->B == 0 || n_new <= 0) return 0;
@@ -751,7 +757,7 @@ extern "C" size_t tv_chunk_workspace_size(const tv_shape* s, int32_t n_new) {
     tv_set_error(TV_ERR_SHAPE, "%s: n_new * H >= 2^31", fn);
     return 0;
   }
-  return 256;
+  return align256(chunk_use_tc(s) ? tv_chunk_tc_workspace(s, n_new) : 0) + 256;
 }
 
 extern "C" int tv_chunk_attn(const tv_shape* s, int32_t n_new, const int32_t* starts, const void* Q,
@@ -782,6 +788,13 @@ extern "C" int tv_chunk_attn(const tv_shape* s, int32_t n_new, const int32_t* st
   if (ws_bytes < need)
     return tv_set_error(TV_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", fn, ws_bytes,
                         need);
+  if (chunk_use_tc(s)) {
+    if (!chunk_tc_supported(s))
+      return tv_set_error(TV_ERR_DTYPE, "%s: the tcgen05 kernel needs bf16, d = 512 and an sm_103 device",
+                          fn);
+    return tv_launch_chunk_tc(s, n_new, starts, Q, c4K, c4V, c128K, c128V, rawK, rawV, L, scale, O,
+                              lse, workspace, status, (cudaStream_t)stream);
+  }
   return tv_launch_chunk_attn(s, n_new, starts, Q, c4K, c4V, c128K, c128V, rawK, rawV, L, scale, O,
                               lse, status, (cudaStream_t)stream);
 }

@@ -93,6 +93,7 @@ constexpr int kPBuf = 33 * 1024;           // a P buffer (1 KB aligned)
 constexpr int kDp = 8;          // rows per section of the extra tile (D <= 8)
 constexpr int kExtraEntries = 32;   // tree | C4 scratch | C128 scratch | zeros
 constexpr int kRankMax = 2048;      // batches up to this size are ranked in the kernel's prologue
+constexpr int kChunkTiles = 2;      // chunks of new tokens: least KV tiles worth a KV chunk of their own
 
 // The wait for the kernel this one depends on, at most once per thread (waited: this thread has
 // waited, or the whole CTA did in the prologue); a repeated griddepcontrol.wait is not free.
@@ -131,6 +132,11 @@ struct Params {
                    // the raw tail are first gathered into the workspace (contiguous per request)
   int tail_rows;   // rows per request of the gathered raw tail (paged pools only)
   int64_t rows_c4, rows_c128, rows_raw;   // row extents of the C4, C128 and raw maps
+  // chunks of new tokens (kChunk): rows of the Q and O maps are all n_new * H rows
+  const int32_t* starts;   // [B+1] request b's tokens are rows starts[b] .. starts[b+1] - 1
+  int n_new;
+  int n_slots;             // slots of 256-row tiles: at least as many as there are tiles
+  int64_t raw_lim, c4_lim, c128_lim;   // capacities (c4_cap and c128_cap are strides in rows)
   uint64_t timeout_ns;   // bound of every wait (kTimeoutNs unless a test shortens it)
   int withhold_tile;     // test aid: the producers never issue this tile's K copies (-1: none)
 };
@@ -320,8 +326,13 @@ struct Header {
   uint32_t tmem;
   int abort;
   int32_t len[kRankMax];       // the requests' lengths L (read once, in the prologue)
-  uint16_t order[kRankMax];    // requests by decreasing tile count (ranked in the prologue)
-  uint16_t tiles[kRankMax];    // tile counts of the requests (clamped to 65535; ranking only)
+  union {
+    struct {
+      uint16_t order[kRankMax];   // requests by decreasing tile count (ranked in the prologue)
+      uint16_t tiles[kRankMax];   // tile counts of the requests (clamped to 65535; ranking only)
+    };
+    int32_t starts[kRankMax];     // chunks of new tokens: the starts (up to kRankMax - 1 requests)
+  };
 };
 // A P buffer holds 128 rows x 128 entries of bf16 P as two 64-entry panels (K-major, 128-byte
 // swizzle), followed by the 128 rows' fp32 rescale factors.
@@ -392,7 +403,7 @@ __device__ __forceinline__ void signal_leader(Smem& sm, uint64_t* bar, uint32_t*
 // caches: b * cap + idx.  Paged pools: C4 rows through the page table (a 64-row box never crosses
 // a C4 page: a page holds a multiple of 128 entries and tiles start at multiples of 128); C128
 // entries and raw positions from the gathered copies in the workspace.
-template <bool kPaged>
+template <bool kPaged, bool kChunk>
 __device__ __forceinline__ int64_t tile_row(const Params& p, int kind, int b, int64_t idx,
                                             int t0) {
   if (kind == kC4) {
@@ -400,6 +411,8 @@ __device__ __forceinline__ int64_t tile_row(const Params& p, int kind, int b, in
     return (int64_t)b * p.c4_cap + idx;
   }
   if (kind == kC128) return (int64_t)b * p.c128_cap + idx;
+  // (a chunk's raw tiles start at multiples of 128 and lie on one page)
+  if (kPaged && kChunk) return layer_row(p.pg, b, idx, p.raw_cap, 1, p.status);
   if (kPaged) return (int64_t)b * p.tail_rows + (idx - t0);
   return (int64_t)b * p.raw_cap + idx;
 }
@@ -434,12 +447,77 @@ __device__ __forceinline__ uint64_t desc_add(uint64_t desc, uint32_t byte_offset
 struct Item {
   int b, rt, chunk, tb, te;
   Layout y;
+  int row0;   // chunks: this CTA's first row in the Q and O maps
+  int rows;   // chunks: its rows (the tile's, at most 128 of them; none or negative: padding)
+  int pos0;   // chunks: position of the request's first new token
+  int nc;     // KV chunks of the item's rows (chunks: at most p.n_chunks, by its tiles)
 };
 
+// Chunks of new tokens.  Request b's n tokens make n * H rows (token-major) and ceil(n * H / 256)
+// pairs of row tiles; their slots start at floor(starts[b] * H / 256) + b, which leaves every
+// request room for its pairs whatever the others have, so that an item is found by a search of the
+// starts, without a list.  Tokens see different entries: the pair's tiles reach to what its last
+// token sees and the softmax masks the rest.  All KV chunks of a slot come n_slots items apart.
+template <bool kPaged>
+__device__ __forceinline__ void chunk_item(const Params& p, const int32_t* starts, const int32_t* len,
+                                           int slot, int chunk, int sub, Item& it) {
+  it.tb = it.te = it.rows = 0;
+  it.y.T = 0;
+  it.chunk = chunk;
+  it.nc = 1;
+  int lo = 0, hi = p.B;   // requests whose slots start at or below this one
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if ((int64_t)starts[mid] * p.H / 256 + mid <= slot)
+      lo = mid + 1;
+    else
+      hi = mid;
+  }
+  const int b = lo - 1;
+  if (b < 0) return;
+  const int s0 = starts[b], n = starts[b + 1] - s0, L = len[b];
+  const int64_t first = ((int64_t)slot - ((int64_t)s0 * p.H / 256 + b)) * 256, rows = (int64_t)n * p.H;
+  if (s0 < 0 || n <= 0 || s0 + (int64_t)n > p.n_new || first >= rows || L < n || L > p.raw_lim ||
+      ((p.comp_mask & TV_COMP_C4) && L / 4 > p.c4_lim) ||
+      ((p.comp_mask & TV_COMP_C128) && L / 128 > p.c128_lim))
+    return;
+  it.b = b;
+  it.rt = (int)(first / 128) + sub;
+  it.row0 = (int)((int64_t)s0 * p.H + first + 128 * sub);
+  it.rows = (int)(rows - first) - 128 * sub;
+  it.pos0 = L - n;
+  const int last = (int)(rows < first + 256 ? rows : first + 256) - 1;
+  const int p_lo = it.pos0 + (int)first / p.H, p_hi = it.pos0 + last / p.H;
+  Layout& y = it.y;
+  y.L = p_hi + 1;
+  y.n4 = (p.comp_mask & TV_COMP_C4) ? p_hi / 4 : 0;
+  y.n128 = (p.comp_mask & TV_COMP_C128) ? p_hi / 128 : 0;
+  y.t0 = raw_lo_of(p_lo, p.tail_mode, p.W, m_min_of(p.comp_mask));
+  if (kPaged) y.t0 &= ~127;   // raw tiles that lie on one page (pages hold a multiple of 512 rows)
+  y.nraw = y.L - y.t0;
+  y.T4 = (y.n4 + 127) / 128;
+  y.T128 = (y.n128 + 127) / 128;
+  y.Traw = (y.nraw + 127) / 128;
+  y.T = y.T4 + y.T128 + y.Traw;
+  it.nc = min(p.n_chunks, (y.T + kChunkTiles - 1) / kChunkTiles);
+  if (chunk >= it.nc) return;
+  it.tb = (int)((int64_t)y.T * chunk / it.nc);
+  it.te = (int)((int64_t)y.T * (chunk + 1) / it.nc);
+}
+
+template <bool kPaged, bool kChunk>
 __device__ __forceinline__ bool item_at(const Params& p, const Smem& sm, int k, uint32_t sub,
                                         Item& it) {
   const int G = (int)(gridDim.x / kClusterCtas), c = (int)(blockIdx.x / kClusterCtas);
   const int pos = (k & 1) ? k * G + (G - 1 - c) : k * G + c;
+  if (kChunk) {
+    if (pos >= p.n_slots * p.n_chunks) return false;
+    const bool cached = p.B < kRankMax;   // (see the kernel's prologue)
+    chunk_item<kPaged>(p, cached ? sm.h.starts : p.starts,
+                       cached ? sm.h.len : p.L, pos % p.n_slots, pos / p.n_slots, (int)sub, it);
+    return true;
+  }
+  it.nc = p.n_chunks;
   if (pos >= p.B * p.n_chunks * p.n_pairs) return false;
   int x = pos;
   const int pair_idx = x % p.n_pairs;
@@ -484,7 +562,7 @@ struct Ring {
 // slices.  Pair O: every entry of each tile for this CTA's 256 value columns, in two slots (one
 // per 256-column group of O) of two 64-column blocks; rows past the tile's entry count rounded up
 // to 64 are not loaded.
-template <bool kPaged, bool kOverlap>
+template <bool kPaged, bool kOverlap, bool kChunk>
 __device__ void producer(const Params& p, Smem& sm, bool role_s, uint32_t sub) {
   const int lane = threadIdx.x & 31;
   const uint32_t leader = cluster_rank() & ~1u;
@@ -516,11 +594,11 @@ __device__ void producer(const Params& p, Smem& sm, bool role_s, uint32_t sub) {
   bool ok = true;
   int q = 0;   // non-empty items so far
   Item it;
-  for (int k = 0; ok && item_at(p, sm, k, sub, it); ++k) {
+  for (int k = 0; ok && item_at<kPaged, kChunk>(p, sm, k, sub, it); ++k) {
     if (it.tb >= it.te) continue;
     const int b = it.b;
     const Layout& y = it.y;
-    const int tree_row = tv_in_range(b * p.D, 0, p.tree_rows, p.status, 2) ? b * p.D : 0;
+    const int tree_row = !kChunk && tv_in_range(b * p.D, 0, p.tree_rows, p.status, 2) ? b * p.D : 0;
     // pair O: the previous item's epilogue stages O in the V ring; its slots are free again
     // once the role warps report v_free
     if (!role_s && q > 0 && !mbar_wait(&sm.h.v_free, (q - 1) & 1, &sm.h.abort, p.timeout_ns)) {
@@ -538,7 +616,7 @@ __device__ void producer(const Params& p, Smem& sm, bool role_s, uint32_t sub) {
           if (j == 0) mbar_arrive_expect_tx(&sm.h.q_tma, 8 * 16384);
           for (int s = 2 * j; s < 2 * j + 2; ++s)
             tma_load_3d(r.base + r.slot * kSlotBytes + (s & 1) * 16384, &p.mQ, 64 * s,
-                        128 * it.rt, b, &sm.h.q_tma);
+                        kChunk ? it.row0 : 128 * it.rt, kChunk ? 0 : b, &sm.h.q_tma);
           if (sub == 0) mbar_arrive(&sm.h.full[r.slot]);
         }
         finish(false);
@@ -550,12 +628,12 @@ __device__ void producer(const Params& p, Smem& sm, bool role_s, uint32_t sub) {
       int2 rw = make_int2(0, 0);
       if (t < it.tb || t >= it.te) return rw;
       const Tile x = tile_of(y, t);
-      if (x.kind == kExtra) return rw;
+      if (!kChunk && x.kind == kExtra) return rw;
       if (role_s) {
-        rw.x = (int)tile_row<kPaged>(p, x.kind, b, x.row0 + (int)sub * (x.nqk / 2), y.t0);
+        rw.x = (int)tile_row<kPaged, kChunk>(p, x.kind, b, x.row0 + (int)sub * (x.nqk / 2), y.t0);
       } else {
-        rw.x = (int)tile_row<kPaged>(p, x.kind, b, x.row0, y.t0);
-        rw.y = kPaged ? (int)tile_row<kPaged>(p, x.kind, b, x.row0 + 64, y.t0) : rw.x + 64;
+        rw.x = (int)tile_row<kPaged, kChunk>(p, x.kind, b, x.row0, y.t0);
+        rw.y = kPaged ? (int)tile_row<kPaged, kChunk>(p, x.kind, b, x.row0 + 64, y.t0) : rw.x + 64;
       }
       return rw;
     };
@@ -575,7 +653,7 @@ __device__ void producer(const Params& p, Smem& sm, bool role_s, uint32_t sub) {
         if (role_s) {
           loads = t != p.withhold_tile;   // test aid: the MMA issuer's wait for it runs out
           if (lane == 0 && loads) {
-            if (x.kind == kExtra) {
+            if (!kChunk && x.kind == kExtra) {
               // leader: tree rows | C4 scratch rows; follower: C128 scratch rows | zero rows
               expect(kKSlices * 2 * kDp * 128);
               for (int ks = 0; ks < kKSlices; ++ks) {
@@ -603,7 +681,7 @@ __device__ void producer(const Params& p, Smem& sm, bool role_s, uint32_t sub) {
           }
         } else if (lane == 0) {
           const int col0 = 256 * g + 128 * (int)sub;
-          if (x.kind == kExtra) {
+          if (!kChunk && x.kind == kExtra) {
             expect(2 * 4 * kDp * 128);
             for (int cb = 0; cb < 2; ++cb) {
               uint8_t* d = dst + cb * kVBlock;
@@ -657,6 +735,7 @@ __device__ __forceinline__ bool wait_ring(const Params& p, Smem& sm, const Ring&
 
 // Pair S: S_t = Q K_t^T into S buffer t & 1 (M = 256, N = the tile's entries, K = 512: A = Q from
 // TMEM columns [256, 512), B = K from the ring).
+template <bool kPaged, bool kChunk>
 __device__ void mma_s(const Params& p, Smem& sm) {
   const uint32_t tmem = sm.h.tmem;
   const uint16_t pair = 0x3;
@@ -665,7 +744,7 @@ __device__ void mma_s(const Params& p, Smem& sm) {
   int g = 0, q = 0;   // tiles and non-empty items so far
   bool ok = true;
   Item it;
-  for (int k = 0; ok && item_at(p, sm, k, 0, it); ++k) {
+  for (int k = 0; ok && item_at<kPaged, kChunk>(p, sm, k, 0, it); ++k) {
     const int n = it.te - it.tb;
     if (n <= 0) continue;
     if (!mbar_wait(&sm.h.q_full, q & 1, &sm.h.abort, p.timeout_ns)) {
@@ -717,6 +796,7 @@ __device__ void mma_s(const Params& p, Smem& sm) {
 // Pair O: O[:, 256j .. 256j+255] += P_t V_t[:, 256j .. 256j+255] for j = 0, 1 (M = 256, N = 256,
 // K = the tile's entries: A = P from the P buffer of parity t, B = V from the ring).  An item's
 // first PV waits until the previous item's O has left TMEM.
+template <bool kPaged, bool kChunk>
 __device__ void mma_o(const Params& p, Smem& sm) {
   const uint32_t tmem = sm.h.tmem;
   const uint16_t pair = 0xC, pair_s = 0x3;
@@ -727,7 +807,7 @@ __device__ void mma_o(const Params& p, Smem& sm) {
   int g = 0, q = 0;
   bool ok = true;
   Item it;
-  for (int k = 0; ok && item_at(p, sm, k, 0, it); ++k) {
+  for (int k = 0; ok && item_at<kPaged, kChunk>(p, sm, k, 0, it); ++k) {
     const int n = it.te - it.tb;
     if (n <= 0) continue;
     if (q > 0 && !mbar_wait(&sm.h.o_free, (q - 1) & 1, &sm.h.abort, p.timeout_ns)) {
@@ -789,6 +869,7 @@ __device__ void mma_o(const Params& p, Smem& sm) {
 // Pair O: tile t's rescale applied and P_t landed in this CTA -> p_full.
 // A follower cannot signal tile t + 2 before the leader's barrier of tile t completed (the
 // pipelines make the later signal depend on the earlier one), so two parities suffice.
+template <bool kPaged, bool kChunk>
 __device__ void signal_s(const Params& p, Smem& sm, uint32_t rank) {
   const uint32_t leader = rank & ~1u;
   const bool is_leader = (rank & 1u) == 0;
@@ -798,7 +879,7 @@ __device__ void signal_s(const Params& p, Smem& sm, uint32_t rank) {
   const uint32_t src0 = smem_u32(sm.buf + kSSlots * kSlotBytes);
   int g = 0, q = 0;
   Item it;
-  for (int k = 0; item_at(p, sm, k, rank & 1u, it); ++k) {
+  for (int k = 0; item_at<kPaged, kChunk>(p, sm, k, rank & 1u, it); ++k) {
     const int n = it.te - it.tb;
     if (n <= 0) continue;
     if (!mbar_wait(&sm.h.q_local, q & 1, &sm.h.abort, p.timeout_ns)) {
@@ -841,12 +922,13 @@ __device__ void signal_s(const Params& p, Smem& sm, uint32_t rank) {
   asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 
+template <bool kPaged, bool kChunk>
 __device__ void signal_o(const Params& p, Smem& sm, uint32_t rank) {
   const uint32_t leader = rank & ~1u;
   const bool is_leader = (rank & 1u) == 0;
   int g = 0;
   Item it;
-  for (int k = 0; item_at(p, sm, k, rank & 1u, it); ++k) {
+  for (int k = 0; item_at<kPaged, kChunk>(p, sm, k, rank & 1u, it); ++k) {
     const int n = it.te - it.tb;
     bool ok = true;
     for (int i = 0; i < n; ++i, ++g) {
@@ -897,7 +979,7 @@ __device__ __noinline__ uint64_t row_masks(const Params& p, int b, int grow, int
   return ((uint64_t)(uint32_t)raw_lo << 32) | extra_mask;
 }
 
-template <bool kOverlap>
+template <bool kPaged, bool kOverlap, bool kChunk>
 __device__ void softmax_s(const Params& p, Smem& sm, uint32_t rank) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quad = warp & 3;
@@ -916,13 +998,14 @@ __device__ void softmax_s(const Params& p, Smem& sm, uint32_t rank) {
   bool ok = true;
   bool waited = !kOverlap;   // this thread has waited for the kernel it depends on
   Item it;
-  for (int k = 0; ok && item_at(p, sm, k, rank & 1u, it); ++k) {
+  for (int k = 0; ok && item_at<kPaged, kChunk>(p, sm, k, rank & 1u, it); ++k) {
     const int n = it.te - it.tb;
     if (n <= 0) continue;
     const int b = it.b;
     const int grow = 128 * it.rt + row;
-    const bool row_ok = grow < p.DH;
+    const bool row_ok = kChunk ? row < it.rows : grow < p.DH;
     const Layout& y = it.y;
+    const int pos = kChunk ? it.pos0 + grow / p.H : 0;   // the row's token (padding: past the chunk)
     // Q: the producer's TMA put this item's Q rows in the ring as eight slices of 128 rows x 64
     // dims (128-byte swizzle), slices 2j and 2j+1 in the j-th slot after the ring position the
     // item started at (2 slots per earlier tile, 4 per earlier item); this thread moves dims
@@ -968,7 +1051,8 @@ __device__ void softmax_s(const Params& p, Smem& sm, uint32_t rank) {
       raw_lo = (int)(rm >> 32);
       extra_mask = (uint32_t)rm;
     };
-    if (waited) load_masks();
+    if (!kChunk && waited) load_masks();
+    if (kChunk) raw_lo = raw_lo_of(pos, p.tail_mode, p.W, m_min_of(p.comp_mask));
 
     float m_ref = -INFINITY, l_run = 0.f;
     // The two warps of a row (column halves) meet at one named barrier per tile.  A warp whose
@@ -1005,12 +1089,19 @@ __device__ void softmax_s(const Params& p, Smem& sm, uint32_t rank) {
         // extra tile's per-node bits.  One code path for every tile kind.
         if (kOverlap && x.kind >= kRaw && !masks) load_masks();
         uint64_t vmask;
-        if (x.kind == kExtra) {
+        if (!kChunk && x.kind == kExtra) {
           vmask = c0 == 0 ? (uint64_t)extra_mask : 0ull;
         } else {
-          const int hi = min(64, max(0, x.valid - c0));
+          // (chunks: only as far as this row's token sees)
+          const int end = !kChunk          ? x.valid
+                          : x.kind == kC4  ? min(x.valid, pos / 4 - x.row0)
+                          : x.kind == kRaw ? min(x.valid, pos + 1 - x.row0)
+                                           : min(x.valid, pos / 128 - x.row0);
+          const int hi = min(64, max(0, end - c0));
           const int lo = x.kind == kRaw ? min(hi, max(0, raw_lo - x.row0 - c0)) : 0;
-          vmask = (hi == 64 ? ~0ull : ((1ull << hi) - 1ull)) & ~((1ull << lo) - 1ull);
+          // (a chunk's raw tiles start below what its rows see: lo may be 64; a tree's lo is below D)
+          const uint64_t below = kChunk && lo == 64 ? ~0ull : (1ull << lo) - 1ull;
+          vmask = (hi == 64 ? ~0ull : ((1ull << hi) - 1ull)) & ~below;
         }
         const uint32_t vlo = (uint32_t)vmask, vhi = (uint32_t)(vmask >> 32);
         // row maximum of the visible raw logits (scale > 0, so the scaled maximum follows); the
@@ -1108,8 +1199,8 @@ __device__ void softmax_s(const Params& p, Smem& sm, uint32_t rank) {
       st_async_v2(mapa_cluster(smem_u32(&sm.h.ml[mb][row][0]), partner), __float_as_uint(m_ref),
                   __float_as_uint(l_tot), mapa_cluster(smem_u32(&sm.h.ml_full[mb]), partner));
       if (kOverlap) pdl_wait_once(waited);   // no write before the kernel depended on completed
-      if (row_ok && p.n_chunks == 1)
-        p.lse[(int64_t)b * p.DH + grow] =
+      if (row_ok && it.nc == 1)
+        p.lse[kChunk ? (int64_t)it.row0 + row : (int64_t)b * p.DH + grow] =
             l_tot > 0.f ? (m_ref + log2f(l_tot)) * 0.6931471805599453f : -INFINITY;
     }
   }
@@ -1117,7 +1208,7 @@ __device__ void softmax_s(const Params& p, Smem& sm, uint32_t rank) {
 
 // ---- pair O role warps: per-tile rescale, then each item's epilogue ------------------------------
 // Warp w (2..9) serves lane quadrant w % 4 and O columns 256ch .. 256ch+255, ch = (w-2)/4.
-template <bool kOverlap>
+template <bool kPaged, bool kOverlap, bool kChunk>
 __device__ void rescale_epilogue_o(const Params& p, Smem& sm, uint32_t rank) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quad = warp & 3;
@@ -1129,14 +1220,15 @@ __device__ void rescale_epilogue_o(const Params& p, Smem& sm, uint32_t rank) {
   const int d = 512;
   int g = 0, q = 0;
   bool waited = !kOverlap;   // (without the overlap the prologue waited)
+  int staged = 0;            // items stored from the V ring so far
   Item it;
-  for (int k = 0; item_at(p, sm, k, rank & 1u, it); ++k) {
+  for (int k = 0; item_at<kPaged, kChunk>(p, sm, k, rank & 1u, it); ++k) {
     const int n = it.te - it.tb;
     const int b = it.b;
     const int grow = 128 * it.rt + row;
-    const bool row_ok = grow < p.DH;
+    const bool row_ok = kChunk ? row < it.rows : grow < p.DH;
     if (n <= 0) {
-      if (it.y.T > 0 && p.n_chunks > 1 && row_ok) {   // an empty KV chunk: l = 0
+      if (!kChunk && it.y.T > 0 && p.n_chunks > 1 && row_ok) {   // an empty KV chunk: l = 0
         if (kOverlap) pdl_wait_once(waited);   // no write before the kernel depended on completed
         float* prow = p.part + part_row(p, b, grow, it.chunk) * (d + 4);
         for (int c = 0; c < 256; c += 4)
@@ -1196,7 +1288,30 @@ __device__ void rescale_epilogue_o(const Params& p, Smem& sm, uint32_t rank) {
     // extra tile was loaded after that wait)
     if (kOverlap) pdl_wait_once(waited);
     const float m = sm.h.ml[mb][row][0], l = sm.h.ml[mb][row][1];
-    if (p.n_chunks == 1) {
+    if (it.nc == 1 && kChunk && it.rows < 128) {
+      // a chunk's partial row tile: the rows behind it are another request's, so each thread stores
+      // its own row's columns
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      __nv_bfloat16* orow = p.O + ((int64_t)it.row0 + row) * 512 + 256 * ch;
+      for (int c = 0; c < 256 / 32; ++c) {
+        uint32_t r[32];
+        tmem_ld32(tmem + lane_base + 256 * ch + 32 * c, r);
+        tmem_wait_ld();
+        if (row_ok) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(r[8 * j + 2 * i]) * inv,
+                                                             __uint_as_float(r[8 * j + 2 * i + 1]) * inv);
+              w[i] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+            *reinterpret_cast<uint4*>(orow + 32 * c + 8 * j) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+    } else if (it.nc == 1) {
       // O leaves through shared memory and TMA stores: the V ring (idle from o_full until this
       // CTA's producer sees o_free) takes this CTA's 128 rows x 512 columns as eight 64-column
       // boxes with the 128-byte swizzle (16-byte chunk c of a row at c ^ (row & 7)); rows past
@@ -1233,24 +1348,27 @@ __device__ void rescale_epilogue_o(const Params& p, Smem& sm, uint32_t rank) {
       // one thread stores the boxes once every warp has staged its rows (a bounded wait, not a
       // CTA barrier: a warp that gave up never arrives), then frees the V ring
       if (warp == 2 && lane == 0) {
-        if (!mbar_wait(&sm.h.stage_full, (q - 1) & 1, &sm.h.abort, p.timeout_ns)) {
+        if (!mbar_wait(&sm.h.stage_full, staged & 1, &sm.h.abort, p.timeout_ns)) {
           fail(sm, p.status);
           return;
         }
-        if (tv_in_range(b, 0, p.B, p.status, 3) && tv_in_range(128 * it.rt, 0, p.DH, p.status, 3))
+        const int y0 = kChunk ? it.row0 : 128 * it.rt, z0 = kChunk ? 0 : b;
+        if (tv_in_range(b, 0, p.B, p.status, 3) && tv_in_range(y0, 0, p.DH, p.status, 3))
           for (int j = 0; j < 8; ++j)
             asm volatile(
                 "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::
                     "l"(reinterpret_cast<uint64_t>(&p.mO)),
-                "r"(64 * j), "r"(128 * it.rt), "r"(b), "r"(smem_u32(stage + j * 16384))
+                "r"(64 * j), "r"(y0), "r"(z0), "r"(smem_u32(stage + j * 16384))
                 : "memory");
         asm volatile("cp.async.bulk.commit_group;" ::: "memory");
         asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
         mbar_arrive(&sm.h.v_free);
       }
+      ++staged;
       continue;
     } else {
-      float* prow = p.part + part_row(p, b, grow, it.chunk) * (d + 4);
+      float* prow = p.part + (kChunk ? part_row(p, 0, it.row0 + row, it.chunk)
+                                     : part_row(p, b, grow, it.chunk)) * (d + 4);
       for (int c = 0; c < 256 / 32; ++c) {
         uint32_t r[32];
         tmem_ld32(tmem + lane_base + 256 * ch + 32 * c, r);
@@ -1281,7 +1399,8 @@ __device__ void rescale_epilogue_o(const Params& p, Smem& sm, uint32_t rank) {
 // producer free of the page-table work.  kOverlap: the launch chain's overlap with the kernel
 // before this one (the kernel ranks the requests itself and waits late); without it, the
 // instantiation waits in its prologue and keeps the late-wait checks out of its tile loops.
-template <bool kPaged, bool kOverlap>
+// kChunk: chunks of new tokens (tv_chunk_attn), whose items come from the starts.
+template <bool kPaged, bool kOverlap, bool kChunk>
 __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant__ Params p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
@@ -1291,7 +1410,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     if (threadIdx.x == 0) record_error(p.status, TV_ERR_CUDA);
     return;
   }
-  pdl_launch_dependents();   // the acceptance walk reads nothing this kernel writes
+  if (!kChunk) pdl_launch_dependents();   // the acceptance walk reads nothing this kernel writes
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (kOverlap && warp >= 2) {
     // the requests' lengths and tile counts for the ranking below, read through L2 (there is no
@@ -1345,6 +1464,28 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     tmem_alloc2(&sm.h.tmem, 512);
     tmem_relinquish2();
   }
+  if (kChunk) {
+    // the starts and lengths, which the kernel before this one may have written; the grid's first
+    // CTA reports what makes a request invalid
+    pdl_wait();
+    pdl_launch_dependents();   // (the merge reads them ahead of its wait)
+    for (int b = threadIdx.x; b < p.B && (p.B < kRankMax || blockIdx.x == 0); b += blockDim.x) {
+      const int s0 = p.starts[b], s1 = p.starts[b + 1], L = p.L[b];
+      if (p.B < kRankMax) {
+        sm.h.starts[b] = s0;
+        sm.h.len[b] = L;
+        if (b == p.B - 1) sm.h.starts[p.B] = s1;
+      }
+      if (blockIdx.x == 0) {
+        if (s0 < 0 || s1 < s0 || s1 > p.n_new || (s1 > s0 && L < s1 - s0))
+          record_error(p.status, TV_ERR_ARG);
+        else if (s1 > s0 && (L > p.raw_lim || ((p.comp_mask & TV_COMP_C4) && L / 4 > p.c4_lim) ||
+                             ((p.comp_mask & TV_COMP_C128) && L / 128 > p.c128_lim)))
+          record_error(p.status, TV_ERR_CAPACITY);
+      }
+    }
+    __syncthreads();
+  }
   tc_fence_before();
   cluster_sync();   // every CTA's barriers exist before any remote arrive, store or pair MMA
   tc_fence_after();
@@ -1361,34 +1502,34 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
       sm.h.order[r] = (uint16_t)b;
     }
     __syncthreads();
-  } else {
+  } else if (!kChunk) {
     // a programmatic dependent of the ranking kernel: the set-up above overlaps it; every read
     // of the round's inputs comes after it has completed
     pdl_wait();
   }
 
   if (warp == 0) {
-    producer<kPaged, kOverlap>(p, sm, role_s, sub);
+    producer<kPaged, kOverlap, kChunk>(p, sm, role_s, sub);
   } else if (warp == 1) {
     if (lane == 0 && sub == 0) {
       if (role_s)
-        mma_s(p, sm);
+        mma_s<kPaged, kChunk>(p, sm);
       else
-        mma_o(p, sm);
+        mma_o<kPaged, kChunk>(p, sm);
     }
     __syncwarp();
   } else if (warp == kSigWarp) {
     if (lane == 0) {
       if (role_s)
-        signal_s(p, sm, rank);
+        signal_s<kPaged, kChunk>(p, sm, rank);
       else
-        signal_o(p, sm, rank);
+        signal_o<kPaged, kChunk>(p, sm, rank);
     }
     __syncwarp();
   } else if (role_s) {
-    softmax_s<kOverlap>(p, sm, rank);
+    softmax_s<kPaged, kOverlap, kChunk>(p, sm, rank);
   } else {
-    rescale_epilogue_o<kOverlap>(p, sm, rank);
+    rescale_epilogue_o<kPaged, kOverlap, kChunk>(p, sm, rank);
   }
 
   if (kOverlap) pdl_wait();   // this kernel completes only after the one it depends on
@@ -1406,6 +1547,81 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
   }
   tc_fence_after();
   if (warp == 1) tmem_dealloc2(sm.h.tmem, 512);
+}
+
+// ---- chunks of new tokens: what goes around the attention ------------------------------------------
+// Paged pools: copies each request's C128 entries into contiguous rows of the workspace, `stride` (a
+// multiple of 16) per request.  A page holds 4 entries per 512 tokens, too few for the attention's
+// 64-row boxes.  Rows up to the next multiple of 16 are zeros: the values of masked columns are
+// multiplied by zero probabilities.  A warp per row.
+__global__ void gather_c128_kernel(Paging pg, int64_t c128_cap, int64_t stride, int64_t raw_cap,
+                                   const int32_t* L, const uint4* __restrict__ K,
+                                   const uint4* __restrict__ V, uint4* gK, uint4* gV,
+                                   int32_t* status) {
+  constexpr int kRowU4 = 512 * 2 / 16;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int b = blockIdx.y, lane = threadIdx.x & 31, Lb = L[b];
+  if (Lb <= 0 || Lb > raw_cap) return;
+  const int n = (Lb - 1) / 128;   // the last token sees no more
+  for (int64_t w = (int64_t)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32; w < ((n + 15) & ~15);
+       w += (int64_t)gridDim.x * (blockDim.x / 32)) {
+    const bool some = w < n;
+    const int64_t src = some ? layer_row(pg, b, w, c128_cap, 128, status) * kRowU4 : 0;
+    const int64_t dst = ((int64_t)b * stride + w) * kRowU4;
+#pragma unroll
+    for (int i = 0; i < kRowU4; i += 32) {
+      const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+      gK[dst + i + lane] = some ? K[src + i + lane] : z;
+      gV[dst + i + lane] = some ? V[src + i + lane] : z;
+    }
+  }
+}
+
+// Joins the KV chunks of one slot's rows: grid (slots, 8), a warp per row, 4 rows per warp.
+template <bool kPaged>
+__global__ void __launch_bounds__(256) chunk_merge_kernel(const __grid_constant__ Params p) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  Item it;
+  chunk_item<kPaged>(p, p.starts, p.L, blockIdx.x, 0, 0, it);   // (the attention has waited for these)
+  const int nc = it.nc, rows = min(it.rows, 256);
+  pdl_wait();
+  if (nc == 1) return;
+  constexpr int64_t kRow = 512 + 4;
+  for (int r = 32 * blockIdx.y + warp; r < min(rows, 32 * (int)blockIdx.y + 32); r += 8) {
+    const int64_t row = (int64_t)it.row0 + r;
+    const float* pr = p.part + row * p.n_chunks * kRow;
+    float m = -INFINITY, l = 0.f;   // lane c: chunk c (and c + 32)
+    for (int c = lane; c < nc; c += 32) {
+      const float mc = pr[c * kRow + 512], lc = pr[c * kRow + 513];
+      if (lc > 0.f) {
+        const float top = fmaxf(m, mc);
+        l = l * exp2f(m - top) + lc * exp2f(mc - top);
+        m = top;
+      }
+    }
+    const float M = warp_max(m);
+    const float sum = warp_sum(l > 0.f ? l * exp2f(m - M) : 0.f), inv = 1.f / sum;
+    float4 acc[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+    for (int c = 0; c < nc; ++c) {
+      const float* pc = pr + c * kRow;
+      const float w = pc[513] > 0.f ? exp2f(pc[512] - M) * inv : 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float4 v = *reinterpret_cast<const float4*>(pc + 128 * k + 4 * lane);
+        acc[k].x = fmaf(w, v.x, acc[k].x);
+        acc[k].y = fmaf(w, v.y, acc[k].y);
+        acc[k].z = fmaf(w, v.z, acc[k].z);
+        acc[k].w = fmaf(w, v.w, acc[k].w);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) store_f4(p.O + row * 512 + 128 * k + 4 * lane, acc[k]);
+    if (lane == 0) p.lse[row] = (M + log2f(sum)) * 0.6931471805599453f;
+  }
 }
 
 }  // namespace tc
@@ -1459,11 +1675,15 @@ int cluster_slots() {
   if (slots[dev] == 0) {
     using namespace tv::tc;
     const int smem = (int)sizeof(Smem);
-    if (cudaFuncSetAttribute(attn_kernel<false, false>,
+    if (cudaFuncSetAttribute(attn_kernel<false, false, false>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
-        cudaFuncSetAttribute(attn_kernel<false, true>,
+        cudaFuncSetAttribute(attn_kernel<false, true, false>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
-        cudaFuncSetAttribute(attn_kernel<true, false>,
+        cudaFuncSetAttribute(attn_kernel<true, false, false>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+        cudaFuncSetAttribute(attn_kernel<false, false, true>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+        cudaFuncSetAttribute(attn_kernel<true, false, true>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
       cudaGetLastError();
       return 0;
@@ -1480,7 +1700,7 @@ int cluster_slots() {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, attn_kernel<false, false>, &cfg) != cudaSuccess ||
+    if (cudaOccupancyMaxActiveClusters(&n, attn_kernel<false, false, false>, &cfg) != cudaSuccess ||
         n <= 0) {
       cudaGetLastError();
       int sms = 0;
@@ -1732,15 +1952,162 @@ int tv_launch_attn_tc(const tv_shape* s, const tv::AttnParams<__nv_bfloat16>& a,
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  const cudaError_t le = paged                ? cudaLaunchKernelEx(&cfg, attn_kernel<true, false>, p)
-                         : p.order == nullptr ? cudaLaunchKernelEx(&cfg, attn_kernel<false, true>, p)
-                                              : cudaLaunchKernelEx(&cfg, attn_kernel<false, false>, p);
+  const cudaError_t le = paged                ? cudaLaunchKernelEx(&cfg, attn_kernel<true, false, false>, p)
+                         : p.order == nullptr ? cudaLaunchKernelEx(&cfg, attn_kernel<false, true, false>, p)
+                                              : cudaLaunchKernelEx(&cfg, attn_kernel<false, false, false>, p);
   if (le != cudaSuccess)
     return tv_check_launch("tv_tree_verify_attn (tcgen05 cluster launch)");
   if (int rc = tv_check_launch("tv_tree_verify_attn (tcgen05)")) return rc;
   if (p.n_chunks > 1)
     return tv_launch_merge<__nv_bfloat16>(s->B, DH, 512, p.n_chunks, p.part, a.O, a.lse, stream);
   return TV_OK;
+}
+
+// ---- chunks of new tokens --------------------------------------------------------------------------
+bool tv_chunk_tc_ok(const tv_shape* s) {
+  const int64_t lim = (int64_t)1 << 31;
+  return s->dtype == TV_BF16 && s->d == 512 && (int64_t)s->B * (s->c128_cap + 16) < lim &&
+         (s->page_tokens > 0 ||
+          ((int64_t)s->B * s->raw_cap < lim && (int64_t)s->B * s->c4_cap < lim));
+}
+
+static int64_t chunk_slots(const tv_shape* s, int n_new) {
+  return (int64_t)n_new * s->H / 256 + s->B;
+}
+
+// KV chunks that an item may be split into, from the same model as tc_chunks: items (at most the
+// slots, as the host does not know the requests' sizes) over the resident clusters, with the tiles of
+// a full cache; the kernel splits an item with fewer tiles into fewer.
+static int chunk_kv_chunks(const tv_shape* s, int n_new) {
+  int slots = cluster_slots();
+  if (slots <= 0) slots = 36;
+  const int64_t items = chunk_slots(s, n_new);
+  if (items >= 4 * slots) return 1;
+  int64_t tiles = 2 + (s->tail_mode == TV_TAIL_WINDOW ? (s->W + 127) / 128 : 1);
+  if (s->comp_mask & TV_COMP_C4) tiles += (s->c4_cap + 127) / 128;
+  if (s->comp_mask & TV_COMP_C128) tiles += (s->c128_cap + 127) / 128;
+  constexpr int64_t kItemTiles = 4;
+  const int n_max = (int)(tiles < 64 ? tiles : 64);
+  int64_t best_cost = -1, cost[65];
+  for (int n = 1; n <= n_max; ++n) {
+    cost[n] = (items * n + slots - 1) / slots * ((tiles + n - 1) / n + kItemTiles);
+    if (best_cost < 0 || cost[n] < best_cost) best_cost = cost[n];
+  }
+  for (int n = 1; n <= n_max; ++n)
+    if (10 * cost[n] <= 11 * best_cost) return n;
+  return 1;
+}
+
+static int64_t chunk_c128_stride(const tv_shape* s) { return (s->c128_cap + 15) / 16 * 16; }
+static size_t chunk_gather_bytes(const tv_shape* s) {   // one of K / V (multiple of 1 KB)
+  return s->page_tokens > 0 && (s->comp_mask & TV_COMP_C128)
+             ? (size_t)s->B * chunk_c128_stride(s) * 1024
+             : 0;
+}
+
+size_t tv_chunk_tc_workspace(const tv_shape* s, int n_new) {
+  const int n = chunk_kv_chunks(s, n_new);
+  return 2 * chunk_gather_bytes(s) +
+         (n > 1 ? (size_t)n_new * s->H * n * (512 + 4) * sizeof(float) : 0);
+}
+
+int tv_launch_chunk_tc(const tv_shape* s, int n_new, const int32_t* starts, const void* Q,
+                       const void* c4K, const void* c4V, const void* c128K, const void* c128V,
+                       const void* rawK, const void* rawV, const int32_t* L, float scale, void* O,
+                       float* lse, void* workspace, int32_t* status, cudaStream_t stream) {
+  using namespace tv::tc;
+  const char* fn = "tv_chunk_attn";
+  Params p;
+  const bool c4 = s->comp_mask & TV_COMP_C4, c128 = s->comp_mask & TV_COMP_C128;
+  const bool paged = s->page_tokens > 0;
+  char* ws = reinterpret_cast<char*>(workspace);
+  const size_t gather = chunk_gather_bytes(s);
+  const uint64_t pool = (uint64_t)s->n_pool_pages * (paged ? s->page_tokens : 0);
+  auto rows_or_one = [](uint64_t r) { return r > 0 ? r : (uint64_t)1; };
+  const uint64_t B = (uint64_t)s->B, rows = (uint64_t)n_new * s->H;
+  const uint64_t rawrows = rows_or_one(paged ? pool : B * (uint64_t)s->raw_cap);
+  // an inactive compressor's maps are pointed at the raw rows (never read: it has no tiles)
+  const uint64_t c4rows = !c4 ? rawrows : rows_or_one(paged ? pool / 4 : B * (uint64_t)s->c4_cap);
+  const int64_t stride = paged ? chunk_c128_stride(s) : s->c128_cap;
+  const uint64_t c128rows = !c128 ? rawrows : rows_or_one(B * (uint64_t)stride);
+  const void* k4 = c4 ? c4K : rawK;
+  const void* v4 = c4 ? c4V : rawV;
+  const void* k128 = !c128 ? rawK : paged ? ws : c128K;
+  const void* v128 = !c128 ? rawV : paged ? ws + gather : c128V;
+  if (!(make_map(&p.mQ, Q, 3, rows, 1, 128) && make_map(&p.mO, O, 3, rows, 1, 128) &&
+        make_map(&p.mC4K, k4, 2, c4rows, 1, 64) && make_map(&p.mC4V, v4, 2, c4rows, 1, 64) &&
+        make_map(&p.mC128K, k128, 2, c128rows, 1, 64) &&
+        make_map(&p.mC128V, v128, 2, c128rows, 1, 64) &&
+        make_map(&p.mRawK, rawK, 2, rawrows, 1, 64) && make_map(&p.mRawV, rawV, 2, rawrows, 1, 64)))
+    return tv_set_error(TV_ERR_CUDA, "%s: tensor-map encoding failed", fn);
+  p.rows_c4 = (int64_t)c4rows;
+  p.rows_c128 = (int64_t)c128rows;
+  p.rows_raw = (int64_t)rawrows;
+  p.B = s->B;
+  p.D = 1;
+  p.H = s->H;
+  p.DH = (int)rows;
+  p.W = s->W;
+  p.tail_mode = s->tail_mode;
+  p.comp_mask = s->comp_mask;
+  p.n_pairs = 0;
+  p.n_chunks = chunk_kv_chunks(s, n_new);
+  p.n_sel = 0;
+  p.tree_rows = 0;
+  p.raw_cap = p.raw_lim = s->raw_cap;
+  p.c4_cap = p.c4_lim = s->c4_cap;
+  p.c128_cap = stride;
+  p.c128_lim = s->c128_cap;
+  p.L = L;
+  p.raw_lo = nullptr;
+  p.anc = p.vis4 = p.vis128 = nullptr;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.O = reinterpret_cast<__nv_bfloat16*>(O);
+  p.lse = lse;
+  p.part = reinterpret_cast<float*>(ws + 2 * gather);
+  p.order = nullptr;
+  p.status = status;
+  p.pg = tv::paging_of(s);
+  p.tail_rows = 0;
+  p.starts = starts;
+  p.n_new = n_new;
+  p.n_slots = (int)chunk_slots(s, n_new);
+  p.timeout_ns = (uint64_t)g_timeout_ns.load();
+  p.withhold_tile = g_withhold_tile.load();
+  if (cluster_slots() <= 0) return tv_check_launch(fn);
+  if (gather > 0) {
+    const int64_t n = (s->c128_cap + 7) / 8;
+    if (tv::launch_pdl(gather_c128_kernel, dim3((unsigned)(n < 64 ? n : 64), s->B), dim3(256), 0,
+                       stream, p.pg, s->c128_cap, stride, s->raw_cap, L, (const uint4*)c128K,
+                       (const uint4*)c128V, (uint4*)ws, (uint4*)(ws + gather), status) != cudaSuccess)
+      return tv_check_launch(fn);
+  }
+  const int64_t items = (int64_t)p.n_slots * p.n_chunks;
+  const int64_t clusters = items < cluster_slots() ? items : cluster_slots();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(clusters * kClusterCtas));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = sizeof(Smem);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kClusterCtas;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  if ((paged ? cudaLaunchKernelEx(&cfg, attn_kernel<true, false, true>, p)
+             : cudaLaunchKernelEx(&cfg, attn_kernel<false, false, true>, p)) != cudaSuccess)
+    return tv_check_launch(fn);
+  if (p.n_chunks > 1) {
+    const dim3 grid((unsigned)p.n_slots, 8);
+    if ((paged ? tv::launch_pdl(chunk_merge_kernel<true>, grid, dim3(256), 0, stream, p)
+               : tv::launch_pdl(chunk_merge_kernel<false>, grid, dim3(256), 0, stream, p)) != cudaSuccess)
+      return tv_check_launch(fn);
+  }
+  return tv_check_launch(fn);
 }
 
 extern "C" int tv_debug_attn_timeout(int64_t timeout_ns, int32_t withhold_tile) {
