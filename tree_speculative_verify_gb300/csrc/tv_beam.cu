@@ -2,8 +2,8 @@
 //
 // tv_token_logprobs' kernel reads the logits once and leaves every beam's `width` best tokens with
 // their log probabilities in the workspace; no other token of a beam can be among its group's
-// `width` best.  A warp per group then merges the beams' lists, which are sorted: lane w holds the
-// head of beam w's list, and `width` times the best head goes on.
+// `width` best.  A CTA per group then scores the beams' lists, which are sorted, and a warp merges
+// them: lane w holds the head of beam w's list, and `width` times the best head goes on.
 //
 // A candidate's score is scores[w] + scale (x - m) - ln S, with m the beam's largest logit and ln S
 // the log of its sum relative to m, which is what the log probability of m itself is (up to sign).
@@ -39,68 +39,75 @@ struct BeamArgs {
   int32_t* status;
 };
 
+// Doubles as integers in the same order (-0 as 0).
+__device__ __forceinline__ uint64_t key_of(double x) {
+  const int64_t bits = __double_as_longlong(x + 0.0);
+  return (uint64_t)bits ^ (bits < 0 ? ~0ull : 1ull << 63);
+}
+__device__ __forceinline__ double of_key(uint64_t key) {
+  return __longlong_as_double((int64_t)(key ^ (key >> 63 ? 1ull << 63 : ~0ull)));
+}
+constexpr uint64_t kNoCandidate = ~0xfff0000000000000ull;   // of -inf
+
 template <typename T>
-__global__ void __launch_bounds__(32) beam_kernel(BeamArgs a, const T* logits) {
-  __shared__ double score[kMaxWidth][kMaxWidth];
+__global__ void __launch_bounds__(256) beam_kernel(BeamArgs a, const T* logits) {
+  __shared__ uint64_t key[kMaxWidth][kMaxWidth];   // [place in the list][beam]
   __shared__ int32_t id[kMaxWidth][kMaxWidth];
-  const int lane = threadIdx.x, W = a.width, first = blockIdx.x * W;
+  const int W = a.width, first = blockIdx.x * W;
   pdl_wait();
-  // the beams' candidates; what a group reads of scores and done is read before it writes them
-  const bool beam = lane < W;
-  const float mine = beam ? a.scores[first + lane] : -INFINITY;
-  const bool over = beam && a.done != nullptr && a.done[first + lane] != 0;
-  bool bad = beam && (!(mine == mine) || mine == INFINITY);
-  for (int w = 0; w < W; ++w) {
+  pdl_launch_dependents();
+  // the beams' candidates, all at once (what a group reads of scores and done is read before it
+  // writes them)
+  for (int i = threadIdx.x; i < W * W; i += blockDim.x) {
+    const int w = i / W, h = i - w * W;
     const int64_t b = first + w;
-    const float sum = __shfl_sync(0xffffffffu, mine, w);
-    const bool ended = __shfl_sync(0xffffffffu, (int)over, w);
-    const bool counts = sum > -INFINITY && sum < INFINITY;
+    const float sum = a.scores[b], lp = a.logprobs[b * W];
+    const bool ended = a.done != nullptr && a.done[b] != 0;
     const int top = a.ids[b * W];
-    const float lp = a.logprobs[b * W];
-    if (lane == w && counts && !ended && !(lp == lp)) bad = true;   // (its ids are -1)
-    if (lane < W) {
-      int t = -1;
-      double s = -INFINITY;
-      if (counts && ended && lane == 0) {
-        t = a.eos;
-        s = sum;
-      } else if (counts && !ended && top >= 0) {
-        t = a.ids[b * W + lane];
-        if (t >= 0) {
-          const T* row = logits + b * a.ld;
-          s = (double)sum + ((double)a.scale * ((double)load_f(row + t) - (double)load_f(row + top)) +
-                             (double)lp);
-        }
-      }
-      score[w][lane] = s;
-      id[w][lane] = t;
+    int t = a.ids[b * W + h];
+    double s = -INFINITY;
+    if (!(sum < INFINITY)) {   // NaN, +inf
+      if (h == 0) record_error(a.status, TV_ERR_VALUE);
+    } else if (sum > -INFINITY && ended) {
+      t = a.eos;
+      if (h == 0) s = sum;
+    } else if (sum > -INFINITY && t >= 0) {
+      const T* row = logits + b * a.ld;
+      s = (double)sum + ((double)a.scale * ((double)load_f(row + t) - (double)load_f(row + top)) +
+                         (double)lp);
+    } else if (sum > -INFINITY && h == 0 && !(lp == lp)) {   // (its ids are -1)
+      record_error(a.status, TV_ERR_VALUE);
     }
+    key[h][w] = key_of(s);
+    id[h][w] = t;
   }
-  if (bad) record_error(a.status, TV_ERR_VALUE);
+  __syncthreads();
+  if (threadIdx.x >= 32) return;
+  const int lane = threadIdx.x;
+  const bool beam = lane < W;
+  const bool over = beam && a.done != nullptr && a.done[first + lane] != 0;
   __syncwarp();
-  // the `width` best: lane k keeps the k-th
+  // the `width` best: lane k keeps the k-th, lane w holds the head of list w
   int head = 0, from = -1, tok = -1;
   double best = -INFINITY;
+  uint64_t mine = beam ? key[0][lane] : 0;
   for (int k = 0; k < W; ++k) {
-    double s = beam && head < W ? score[lane][head] : -INFINITY;
-    int w = lane;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const double s2 = __shfl_xor_sync(0xffffffffu, s, o);
-      const int w2 = __shfl_xor_sync(0xffffffffu, w, o);
-      if (s2 > s || (s2 == s && w2 < w)) {
-        s = s2;
-        w = w2;
-      }
-    }
-    if (!(s > -INFINITY)) break;   // candidates have run out
+    const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(mine >> 32));
+    const uint32_t low = (uint32_t)(mine >> 32) == hi ? (uint32_t)mine : 0u;
+    const uint32_t lo = __reduce_max_sync(0xffffffffu, low);
+    const uint64_t top = (uint64_t)hi << 32 | lo;
+    if (top <= kNoCandidate) break;   // candidates have run out
+    const int w = __ffs(__ballot_sync(0xffffffffu, mine == top)) - 1;   // equal: the lower beam
     const int at = __shfl_sync(0xffffffffu, head, w);
     if (lane == k) {
-      best = s;
+      best = of_key(top);
       from = w;
-      tok = id[w][at];
+      tok = id[at][w];
     }
-    if (lane == w) ++head;
+    if (lane == w) {
+      ++head;
+      mine = head < W ? key[head][lane] : 0;
+    }
   }
   // slots: a beam's best continuation (the first of it) stays, the others fill the free ones
   const unsigned lower = (1u << lane) - 1u, all = W == 32 ? ~0u : (1u << W) - 1u;
@@ -141,12 +148,12 @@ int tv_launch_beam(const tv_shape* s, int width, int vocab, int64_t ld, int logi
     return rc;
   const tv::BeamArgs a = {s->B, width, eos, ld, scale, scores, done, ids, logprobs, source, token,
                           new_scores, new_done, rank, status};
-  const dim3 grid(s->B / width);
+  const dim3 grid(s->B / width), block(width * width >= 256 ? 256 : (width * width + 31) / 32 * 32);
   const cudaError_t e =
       logits_dtype == TV_BF16
-          ? tv::launch_pdl(tv::beam_kernel<__nv_bfloat16>, grid, dim3(32), 0, stream, a,
+          ? tv::launch_pdl(tv::beam_kernel<__nv_bfloat16>, grid, block, 0, stream, a,
                            (const __nv_bfloat16*)logits)
-          : tv::launch_pdl(tv::beam_kernel<float>, grid, dim3(32), 0, stream, a, (const float*)logits);
+          : tv::launch_pdl(tv::beam_kernel<float>, grid, block, 0, stream, a, (const float*)logits);
   if (e != cudaSuccess) {
     cudaGetLastError();
     return tv_set_error(TV_ERR_CUDA, "tv_beam_select: launch failed: %s", cudaGetErrorString(e));
