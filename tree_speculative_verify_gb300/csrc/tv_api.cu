@@ -154,7 +154,9 @@ int tv_launch_append(const tv_shape* s, int n_new, const int32_t* starts, const 
 int tv_launch_chunk_attn(const tv_shape* s, int n_new, const int32_t* starts, const void* Q,
                          const void* c4K, const void* c4V, const void* c128K, const void* c128V,
                          const void* rawK, const void* rawV, const int32_t* L, float scale,
-                         void* O, float* lse, int32_t* status, cudaStream_t stream);
+                         void* O, float* lse, void* workspace, int32_t* status,
+                         cudaStream_t stream);
+size_t tv_chunk_simt_workspace(const tv_shape* s, int n_new);
 size_t tv_beam_workspace(const tv_shape* s, int width);
 int tv_launch_beam(const tv_shape* s, int width, int vocab, int64_t ld, int logits_dtype,
                    const void* logits, const float* scores, const int32_t* done, int eos,
@@ -757,7 +759,8 @@ extern "C" size_t tv_chunk_workspace_size(const tv_shape* s, int32_t n_new) {
     tv_set_error(TV_ERR_SHAPE, "%s: n_new * H >= 2^31", fn);
     return 0;
   }
-  return align256(chunk_use_tc(s) ? tv_chunk_tc_workspace(s, n_new) : 0) + 256;
+  return align256(chunk_use_tc(s) ? tv_chunk_tc_workspace(s, n_new)
+                                  : tv_chunk_simt_workspace(s, n_new)) + 256;
 }
 
 extern "C" int tv_chunk_attn(const tv_shape* s, int32_t n_new, const int32_t* starts, const void* Q,
@@ -796,7 +799,7 @@ extern "C" int tv_chunk_attn(const tv_shape* s, int32_t n_new, const int32_t* st
                               lse, workspace, status, (cudaStream_t)stream);
   }
   return tv_launch_chunk_attn(s, n_new, starts, Q, c4K, c4V, c128K, c128V, rawK, rawV, L, scale, O,
-                              lse, status, (cudaStream_t)stream);
+                              lse, workspace, status, (cudaStream_t)stream);
 }
 
 // ---- beams ------------------------------------------------------------------------------------------

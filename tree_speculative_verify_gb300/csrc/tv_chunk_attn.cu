@@ -4,18 +4,28 @@
 //
 // Per row (token at position p, head): s_j = scale q.k_j over the visible entries -- C4 j < p/4,
 // C128 j < p/128, raw rows raw_lo(p) .. p -- in one pass with the running maximum m and sum l of
-// exp(s - m); O = sum exp(s_j - m) v_j / l, lse = m + ln l.
+// exp(s - m); O = sum exp(s_j - m) v_j / l, lse = m + ln l.  Everything in fp32.
+//
+// A CTA takes R rows of one request (token-major, so R / H neighbouring tokens) and a share of the
+// entries that its last token sees, N at a time: K and V rows in shared memory as fp32, a register
+// tile of R/16 x N/16 logits per thread, the probabilities through shared memory, a register tile of
+// R/16 rows x 1/16 of the columns of O.  Requests of few rows (decoding) take R = 16, and while the
+// CTAs do not fill the SMs the entries are split over several, whose partial sums a second kernel
+// joins.
 #include <math.h>
 
 #include "tv_chunk.cuh"
+#include "tv_entry.cuh"
 
 namespace tv {
 
 struct ChunkAttnArgs {
   Chunk c;
   int H, d, W, tail_mode;
+  int n_chunks;       // most shares of an item's entries
   float scale_log2;
   float* lse;
+  float* part;        // [n_new * H][n_chunks][d + 4]: O, m (base 2), l
   int32_t* status;
 };
 
@@ -29,92 +39,368 @@ __device__ __forceinline__ int attn_state(const Chunk& c, int b) {
   return chunk_fits(c, L) ? TV_OK : TV_ERR_CAPACITY;
 }
 
-__global__ void chunk_errors_kernel(Chunk c, int32_t* status) {
-  const int b = blockIdx.x * blockDim.x + threadIdx.x;
-  if (b >= c.B) return;
-  const int state = attn_state(c, b);
-  if (state != TV_OK) record_error(status, state);
+constexpr int kShare = 128;   // least entries of a share
+
+// R rows of one request and what they see.  Slots as in the tensor-core kernel: request b's tiles of R
+// rows start at slot floor(starts[b] * H / R) + b.
+struct RowTile {
+  int b, row0, rows;   // first row of all n_new * H, rows (0: nothing to do)
+  int first, pos0;     // first row within the request, position of the request's first new token
+  int n4, n128, t0, entries, shares;
+};
+
+__device__ __forceinline__ RowTile row_tile(const ChunkAttnArgs& a, int R, int slot) {
+  RowTile t;
+  t.rows = 0;
+  t.shares = 1;
+  int lo = 0, hi = a.c.B;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if ((int64_t)a.c.starts[mid] * a.H / R + mid <= slot)
+      lo = mid + 1;
+    else
+      hi = mid;
+  }
+  const int b = lo - 1;
+  if (b < 0 || attn_state(a.c, b) != TV_OK) return t;
+  const int s0 = a.c.starts[b], n = a.c.starts[b + 1] - s0;
+  const int64_t first = ((int64_t)slot - ((int64_t)s0 * a.H / R + b)) * R, rows = (int64_t)n * a.H;
+  if (first >= rows) return t;
+  t.b = b;
+  t.first = (int)first;
+  t.row0 = (int)((int64_t)s0 * a.H + first);
+  t.rows = (int)(rows - first < R ? rows - first : R);
+  t.pos0 = a.c.L[b] - n;
+  const int p_lo = t.pos0 + t.first / a.H, p_hi = t.pos0 + (t.first + t.rows - 1) / a.H;
+  t.n4 = a.c.comp_mask & TV_COMP_C4 ? p_hi / 4 : 0;
+  t.n128 = a.c.comp_mask & TV_COMP_C128 ? p_hi / 128 : 0;
+  t.t0 = raw_lo_of(p_lo, a.tail_mode, a.W, m_min_of(a.c.comp_mask));
+  t.entries = t.n4 + t.n128 + p_hi + 1 - t.t0;
+  t.shares = min(a.n_chunks, (t.entries + kShare - 1) / kShare);
+  return t;
 }
 
-// A warp per row.
-template <typename T>
-__global__ void chunk_rows_kernel(ChunkAttnArgs a, const T* Q, const T* c4K, const T* c4V,
-                                  const T* c128K, const T* c128V, const T* rawK, const T* rawV,
-                                  T* O) {
-  const int lane = threadIdx.x & 31, d = a.d;
-  const int64_t row = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  if (row >= (int64_t)a.c.n_new * a.H) return;
-  const int t = (int)(row / a.H), b = request_of(a.c.starts, a.c.B, t);
-  if (b < 0 || attn_state(a.c, b) != TV_OK) return;
-  const int p = a.c.L[b] - (a.c.starts[b + 1] - t);
-  const int n4 = a.c.comp_mask & TV_COMP_C4 ? p / 4 : 0;
-  const int n128 = a.c.comp_mask & TV_COMP_C128 ? p / 128 : 0;
-  const int lo = raw_lo_of(p, a.tail_mode, a.W, m_min_of(a.c.comp_mask));
-  float q[kMaxHeadDim / 32], o[kMaxHeadDim / 32];
-#pragma unroll
-  for (int k = 0; k < kMaxHeadDim / 32; ++k) {
-    const int e = lane + 32 * k;
-    q[k] = e < d ? load_f(Q + row * d + e) * a.scale_log2 : 0.f;
-    o[k] = 0.f;
-  }
-  float m = -INFINITY, l = 0.f;
-  for (int j = 0; j < n4 + n128 + p + 1 - lo; ++j) {
-    const T *k, *v;
-    if (j < n4) {
-      const int64_t r = layer_row(a.c.pg, b, j, a.c.c4_cap, 4, a.status) * d;
-      k = c4K + r;
-      v = c4V + r;
-    } else if (j < n4 + n128) {
-      const int64_t r = layer_row(a.c.pg, b, j - n4, a.c.c128_cap, 128, a.status) * d;
-      k = c128K + r;
-      v = c128V + r;
-    } else {
-      const int64_t r = layer_row(a.c.pg, b, lo + j - n4 - n128, a.c.raw_cap, 1, a.status) * d;
-      k = rawK + r;
-      v = rawV + r;
+template <typename T, int R, int N, int DM>
+struct SimtTile {
+  static constexpr int kPitch = DM + 4;   // (rows 4 banks apart)
+  float q[R][kPitch];
+  float k[N][kPitch];
+  float v[N][kPitch];
+  float p[R][N + 4];
+  int64_t at[2][N];   // rows of this tile's and the next one's entries, -1: none
+};
+
+template <typename T, int R, int N, int DM>
+__global__ void __launch_bounds__(256)
+    chunk_simt_kernel(ChunkAttnArgs a, const T* Q, const T* c4K, const T* c4V, const T* c128K,
+                      const T* c128V, const T* rawK, const T* rawV, T* O) {
+  using Tile = SimtTile<T, R, N, DM>;
+  constexpr int RI = R / 16, EI = N / 16, CI = DM / 64, VW = VecWidth<T>::n;
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  Tile& sm = *reinterpret_cast<Tile*>(smem_raw);
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, d = a.d;
+  if (blockIdx.x == 0 && blockIdx.y == 0)
+    for (int b = tid; b < a.c.B; b += 256) {
+      const int state = attn_state(a.c, b);
+      if (state != TV_OK) record_error(a.status, state);
     }
-    float s = 0.f;
+  const RowTile t = row_tile(a, R, blockIdx.x);
+  if (t.rows == 0 || (int)blockIdx.y >= t.shares) return;
+  const int e_lo = (int)((int64_t)t.entries * blockIdx.y / t.shares);
+  const int e_hi = (int)((int64_t)t.entries * (blockIdx.y + 1) / t.shares);
+
+  // Where entry e lives: its row, and which layer by e itself.
+  auto locate = [&](int e) -> int64_t {
+    if (e >= e_hi) return -1;
+    if (e < t.n4) return layer_row(a.c.pg, t.b, e, a.c.c4_cap, 4, a.status);
+    if (e < t.n4 + t.n128) return layer_row(a.c.pg, t.b, e - t.n4, a.c.c128_cap, 128, a.status);
+    return layer_row(a.c.pg, t.b, t.t0 + e - t.n4 - t.n128, a.c.raw_cap, 1, a.status);
+  };
+  if (tid < N) sm.at[0][tid] = locate(e_lo + tid);
+  // queries, scaled; columns past d are zeros (as those of K and V are)
+  constexpr int kVecs = DM / VW;
+  for (int i = tid; i < R * kVecs; i += 256) {
+    const int r = i / kVecs, c = (i % kVecs) * VW;
+    float f[VW];
+    uint4 x = make_uint4(0u, 0u, 0u, 0u);
+    if (r < t.rows && c < d) x = ld16(Q + (int64_t)(t.row0 + r) * d + c);
+    cvt16(x, (T*)nullptr, f);
 #pragma unroll
-    for (int i = 0; i < kMaxHeadDim / 32; ++i)
-      if (lane + 32 * i < d) s = fmaf(q[i], load_f(k + lane + 32 * i), s);
-    s = warp_sum(s);
-    const float top = fmaxf(m, s), alpha = exp2f(m - top), e = exp2f(s - top);
-    l = l * alpha + e;
+    for (int k = 0; k < VW; k += 4)
+      *reinterpret_cast<float4*>(&sm.q[r][c + k]) =
+          make_float4(f[k] * a.scale_log2, f[k + 1] * a.scale_log2, f[k + 2] * a.scale_log2,
+                      f[k + 3] * a.scale_log2);
+  }
+  // what this thread's rows see
+  int lim4[RI], lim128[RI], lo[RI], hi[RI];
 #pragma unroll
-    for (int i = 0; i < kMaxHeadDim / 32; ++i)
-      if (lane + 32 * i < d) o[i] = o[i] * alpha + e * load_f(v + lane + 32 * i);
-    m = top;
+  for (int i = 0; i < RI; ++i) {
+    const int r = min(ty + 16 * i, t.rows - 1), p = t.pos0 + (t.first + r) / a.H;
+    lim4[i] = p / 4;
+    lim128[i] = t.n4 + p / 128;
+    const int base = t.n4 + t.n128 - t.t0;
+    lo[i] = base + raw_lo_of(p, a.tail_mode, a.W, m_min_of(a.c.comp_mask));
+    hi[i] = base + p;
+  }
+  float m[RI], l[RI];
+  float4 o[RI][CI];
+#pragma unroll
+  for (int i = 0; i < RI; ++i) {
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+#pragma unroll
+    for (int c = 0; c < CI; ++c) o[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  __syncthreads();
+  int parity = 0;
+  for (int e0 = e_lo; e0 < e_hi; e0 += N, parity ^= 1) {
+    for (int i = tid; i < N * kVecs; i += 256) {
+      const int r = i / kVecs, c = (i % kVecs) * VW, e = e0 + r;
+      const int64_t row = sm.at[parity][r];
+      uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x;
+      if (row >= 0 && c < d) {
+        const T* ks = e < t.n4 ? c4K : e < t.n4 + t.n128 ? c128K : rawK;
+        const T* vs = e < t.n4 ? c4V : e < t.n4 + t.n128 ? c128V : rawV;
+        x = ld16(ks + row * d + c);
+        y = ld16(vs + row * d + c);
+      }
+      float f[VW];
+      cvt16(x, (T*)nullptr, f);
+#pragma unroll
+      for (int k = 0; k < VW; k += 4)
+        *reinterpret_cast<float4*>(&sm.k[r][c + k]) = make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]);
+      cvt16(y, (T*)nullptr, f);
+#pragma unroll
+      for (int k = 0; k < VW; k += 4)
+        *reinterpret_cast<float4*>(&sm.v[r][c + k]) = make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]);
+    }
+    if (tid < N) sm.at[parity ^ 1][tid] = locate(e0 + N + tid);
+    __syncthreads();
+    // logits: rows ty + 16 i, entries tx + 16 j
+    float s[RI][EI];
+#pragma unroll
+    for (int i = 0; i < RI; ++i)
+#pragma unroll
+      for (int j = 0; j < EI; ++j) s[i][j] = 0.f;
+#pragma unroll 4
+    for (int c = 0; c < DM; c += 4) {
+      float4 x[RI], y[EI];
+#pragma unroll
+      for (int i = 0; i < RI; ++i) x[i] = *reinterpret_cast<const float4*>(&sm.q[ty + 16 * i][c]);
+#pragma unroll
+      for (int j = 0; j < EI; ++j) y[j] = *reinterpret_cast<const float4*>(&sm.k[tx + 16 * j][c]);
+#pragma unroll
+      for (int i = 0; i < RI; ++i)
+#pragma unroll
+        for (int j = 0; j < EI; ++j) {
+          s[i][j] = fmaf(x[i].x, y[j].x, s[i][j]);
+          s[i][j] = fmaf(x[i].y, y[j].y, s[i][j]);
+          s[i][j] = fmaf(x[i].z, y[j].z, s[i][j]);
+          s[i][j] = fmaf(x[i].w, y[j].w, s[i][j]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < RI; ++i) {
+      float top = m[i];
+#pragma unroll
+      for (int j = 0; j < EI; ++j) {
+        const int e = e0 + tx + 16 * j;
+        const bool seen = e < e_hi && (e < t.n4              ? e < lim4[i]
+                                       : e < t.n4 + t.n128 ? e < lim128[i]
+                                                             : e >= lo[i] && e <= hi[i]);
+        s[i][j] = seen ? s[i][j] : -INFINITY;
+        top = fmaxf(top, s[i][j]);
+      }
+#pragma unroll
+      for (int w = 8; w > 0; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+      const float base = top == -INFINITY ? 0.f : top;   // (nothing seen yet)
+      const float alpha = exp2f(m[i] - base);
+      m[i] = top;
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < EI; ++j) {
+        const float e = exp2f(s[i][j] - base);
+        sum += e;
+        sm.p[ty + 16 * i][tx + 16 * j] = e;
+      }
+      l[i] = l[i] * alpha + sum;   // (this thread's entries only)
+#pragma unroll
+      for (int c = 0; c < CI; ++c) {
+        o[i][c].x *= alpha;
+        o[i][c].y *= alpha;
+        o[i][c].z *= alpha;
+        o[i][c].w *= alpha;
+      }
+    }
+    __syncwarp();   // a row's probabilities are written and read by the same half-warp
+    // O: columns 4 tx + 64 c
+#pragma unroll 2
+    for (int e = 0; e < N; e += 4) {
+      float4 x[RI];
+#pragma unroll
+      for (int i = 0; i < RI; ++i) x[i] = *reinterpret_cast<const float4*>(&sm.p[ty + 16 * i][e]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int c = 0; c < CI; ++c) {
+          const float4 y = *reinterpret_cast<const float4*>(&sm.v[e + k][4 * tx + 64 * c]);
+#pragma unroll
+          for (int i = 0; i < RI; ++i) {
+            const float w = k == 0 ? x[i].x : k == 1 ? x[i].y : k == 2 ? x[i].z : x[i].w;
+            o[i][c].x = fmaf(w, y.x, o[i][c].x);
+            o[i][c].y = fmaf(w, y.y, o[i][c].y);
+            o[i][c].z = fmaf(w, y.z, o[i][c].z);
+            o[i][c].w = fmaf(w, y.w, o[i][c].w);
+          }
+        }
+    }
+    __syncthreads();
   }
 #pragma unroll
-  for (int i = 0; i < kMaxHeadDim / 32; ++i)
-    if (lane + 32 * i < d) store_f(O + row * d + lane + 32 * i, o[i] / l);
-  if (lane == 0) a.lse[row] = (m + log2f(l)) * 0.6931471805599453f;
+  for (int i = 0; i < RI; ++i) {
+    float sum = l[i];
+#pragma unroll
+    for (int w = 8; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+    const int r = ty + 16 * i;
+    if (r >= t.rows) continue;
+    const int64_t row = t.row0 + r;
+    if (t.shares == 1) {
+      const float inv = 1.f / sum;
+#pragma unroll
+      for (int c = 0; c < CI; ++c)
+        if (4 * tx + 64 * c < d)
+          store_f4(O + row * d + 4 * tx + 64 * c,
+                   make_float4(o[i][c].x * inv, o[i][c].y * inv, o[i][c].z * inv, o[i][c].w * inv));
+      if (tx == 0) a.lse[row] = (m[i] + log2f(sum)) * 0.6931471805599453f;
+    } else {
+      float* part = a.part + (row * a.n_chunks + blockIdx.y) * (d + 4);
+#pragma unroll
+      for (int c = 0; c < CI; ++c)
+        if (4 * tx + 64 * c < d) *reinterpret_cast<float4*>(part + 4 * tx + 64 * c) = o[i][c];
+      if (tx == 0) {
+        part[d] = m[i];
+        part[d + 1] = sum;
+      }
+    }
+  }
 }
 
+// Joins the shares of one slot's rows: a warp per row.
 template <typename T>
-static int launch_chunk_attn(const ChunkAttnArgs& a, const void* Q, const void* c4K,
-                             const void* c4V, const void* c128K, const void* c128V,
-                             const void* rawK, const void* rawV, void* O, cudaStream_t stream) {
-  const char* fn = "tv_chunk_attn";
-  chunk_errors_kernel<<<(a.c.B + 255) / 256, 256, 0, stream>>>(a.c, a.status);
-  if (int rc = tv_check_launch(fn)) return rc;
-  if (a.c.n_new == 0) return TV_OK;
-  const int64_t rows = (int64_t)a.c.n_new * a.H;
-  chunk_rows_kernel<T><<<(unsigned)((rows + 7) / 8), 256, 0, stream>>>(
+__global__ void __launch_bounds__(256) chunk_simt_merge_kernel(ChunkAttnArgs a, int R, T* O) {
+  const int lane = threadIdx.x & 31, d = a.d;
+  const RowTile t = row_tile(a, R, blockIdx.x);
+  if (t.shares == 1) return;
+  for (int r = threadIdx.x >> 5; r < t.rows; r += blockDim.x >> 5) {
+    const int64_t row = t.row0 + r;
+    const float* pr = a.part + row * a.n_chunks * (d + 4);
+    float M = -INFINITY;
+    for (int c = 0; c < t.shares; ++c) M = fmaxf(M, pr[c * (d + 4) + d]);
+    float sum = 0.f;
+    for (int c = 0; c < t.shares; ++c)
+      sum += exp2f(pr[c * (d + 4) + d] - M) * pr[c * (d + 4) + d + 1];
+    const float inv = 1.f / sum;
+    for (int i = 4 * lane; i < d; i += 128) {
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int c = 0; c < t.shares; ++c) {
+        const float w = exp2f(pr[c * (d + 4) + d] - M) * inv;
+        const float4 v = *reinterpret_cast<const float4*>(pr + c * (d + 4) + i);
+        acc.x = fmaf(w, v.x, acc.x);
+        acc.y = fmaf(w, v.y, acc.y);
+        acc.z = fmaf(w, v.z, acc.z);
+        acc.w = fmaf(w, v.w, acc.w);
+      }
+      store_f4(O + row * d + i, acc);
+    }
+    if (lane == 0) a.lse[row] = (M + log2f(sum)) * 0.6931471805599453f;
+  }
+}
+
+// Rows per CTA: 16 for batches whose requests have few rows on average, else as many as O's register
+// tile allows.
+static int simt_rows(const tv_shape* s, int n_new) {
+  if ((int64_t)n_new * s->H <= 24 * (int64_t)s->B) return 16;
+  return s->d > 256 ? 32 : 64;
+}
+static int64_t simt_slots(const tv_shape* s, int n_new) {
+  return (int64_t)n_new * s->H / simt_rows(s, n_new) + s->B;
+}
+// Shares of an item's entries: enough CTAs for two per SM, up to the shares of a full cache.
+static int simt_chunks(const tv_shape* s, int n_new) {
+  const int64_t slots = simt_slots(s, n_new);
+  int64_t entries = (s->tail_mode == TV_TAIL_WINDOW ? s->W : 128) + 64;
+  if (s->comp_mask & TV_COMP_C4) entries += s->c4_cap;
+  if (s->comp_mask & TV_COMP_C128) entries += s->c128_cap;
+  int64_t n = (2 * 152 + slots - 1) / slots;
+  if (n > (entries + kShare - 1) / kShare) n = (entries + kShare - 1) / kShare;
+  return (int)(n < 1 ? 1 : n > 64 ? 64 : n);
+}
+
+template <typename T, int R, int N, int DM>
+static cudaError_t launch_simt(const ChunkAttnArgs& a, int64_t slots, const void* Q,
+                               const void* c4K, const void* c4V, const void* c128K,
+                               const void* c128V, const void* rawK, const void* rawV, void* O,
+                               cudaStream_t stream) {
+  auto kernel = chunk_simt_kernel<T, R, N, DM>;
+  const int smem = (int)sizeof(SimtTile<T, R, N, DM>);
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kernel<<<dim3((unsigned)slots, a.n_chunks), 256, smem, stream>>>(
       a, (const T*)Q, (const T*)c4K, (const T*)c4V, (const T*)c128K, (const T*)c128V,
       (const T*)rawK, (const T*)rawV, (T*)O);
-  return tv_check_launch(fn);
+  return cudaGetLastError();
+}
+
+template <typename T>
+static int launch_chunk_attn(const ChunkAttnArgs& a, int R, int64_t slots, const void* Q,
+                             const void* c4K, const void* c4V, const void* c128K,
+                             const void* c128V, const void* rawK, const void* rawV, void* O,
+                             cudaStream_t stream) {
+#define TV_SIMT(R_, N_, DM_) \
+  launch_simt<T, R_, N_, DM_>(a, slots, Q, c4K, c4V, c128K, c128V, rawK, rawV, O, stream)
+  cudaError_t e;
+  if (R == 16)
+    e = a.d <= 64    ? TV_SIMT(16, 64, 64)
+        : a.d <= 128 ? TV_SIMT(16, 64, 128)
+        : a.d <= 256 ? TV_SIMT(16, 32, 256)
+                     : TV_SIMT(16, 32, 512);
+  else
+    e = a.d <= 64    ? TV_SIMT(64, 64, 64)
+        : a.d <= 128 ? TV_SIMT(64, 64, 128)
+        : a.d <= 256 ? TV_SIMT(64, 32, 256)
+                     : TV_SIMT(32, 32, 512);
+#undef TV_SIMT
+  if (e == cudaSuccess && a.n_chunks > 1) {
+    chunk_simt_merge_kernel<T><<<(unsigned)slots, 256, 0, stream>>>(a, R, (T*)O);
+    e = cudaGetLastError();
+  }
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return tv_set_error(TV_ERR_CUDA, "tv_chunk_attn: launch failed: %s", cudaGetErrorString(e));
+  }
+  return TV_OK;
 }
 
 }  // namespace tv
 
+size_t tv_chunk_simt_workspace(const tv_shape* s, int n_new) {
+  const int n = tv::simt_chunks(s, n_new);
+  return n > 1 ? (size_t)n_new * s->H * n * (s->d + 4) * sizeof(float) : 0;
+}
+
 int tv_launch_chunk_attn(const tv_shape* s, int n_new, const int32_t* starts, const void* Q,
                          const void* c4K, const void* c4V, const void* c128K, const void* c128V,
                          const void* rawK, const void* rawV, const int32_t* L, float scale,
-                         void* O, float* lse, int32_t* status, cudaStream_t stream) {
+                         void* O, float* lse, void* workspace, int32_t* status,
+                         cudaStream_t stream) {
   const tv::ChunkAttnArgs a = {tv::chunk_of(s, n_new, starts, L), s->H, s->d, s->W, s->tail_mode,
-                               scale * 1.4426950408889634f, lse, status};
+                               tv::simt_chunks(s, n_new), scale * 1.4426950408889634f, lse,
+                               (float*)workspace, status};
+  const int R = tv::simt_rows(s, n_new);
+  const int64_t slots = tv::simt_slots(s, n_new);
   return s->dtype == TV_BF16
-             ? tv::launch_chunk_attn<__nv_bfloat16>(a, Q, c4K, c4V, c128K, c128V, rawK, rawV, O, stream)
-             : tv::launch_chunk_attn<float>(a, Q, c4K, c4V, c128K, c128V, rawK, rawV, O, stream);
+             ? tv::launch_chunk_attn<__nv_bfloat16>(a, R, slots, Q, c4K, c4V, c128K, c128V, rawK,
+                                                    rawV, O, stream)
+             : tv::launch_chunk_attn<float>(a, R, slots, Q, c4K, c4V, c128K, c128V, rawK, rawV, O,
+                                            stream);
 }
