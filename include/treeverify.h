@@ -476,7 +476,8 @@ int tv_pages_compact(const tv_shape* shape, const int32_t* L, int32_t* page_refs
  *   [rope_dim / 2] fp32 in; g4, g128 [d] fp32 in and c4K .. c128V out (nullable when the compressor
  *   is inactive).  K, V, Q, Qr, the caches and ld_kv's bytes 16-byte aligned.
  * Device errors, each leaving that request as it was (its Qr rows are unspecified): TV_ERR_ARG
- * (starts that descend or leave 0 .. n_new, L < 0, no page for a new position), TV_ERR_CAPACITY
+ * (starts that leave 0 .. n_new or descend -- the requests behind may then be left out too --, L < 0, no
+ * page for a new position), TV_ERR_CAPACITY
  * (L + n > raw_cap or an entry beyond cap_m).
  */
 int tv_chunk_append(const tv_shape* shape, int32_t n_new, const int32_t* starts, const void* K,
@@ -498,12 +499,12 @@ int tv_chunk_append(const tv_shape* shape, int32_t n_new, const int32_t* starts,
  *   n_new, starts as in tv_chunk_append; Q [n_new][H][d] in; O [n_new][H][d] out (dtype); lse
  *   [n_new][H] fp32 out: natural-log sum of exp(logits); rows of no request are left alone
  *   Q, O and the caches 16-byte aligned; workspace: device buffer of ws_bytes >=
- *   tv_chunk_workspace_size(shape, n_new), 256-byte aligned; calls that overlap on the GPU need one
- *   each.
+ *   tv_chunk_workspace_size(shape, n_new), 256-byte aligned (what is enough for n_new tokens is for
+ *   fewer); calls that overlap on the GPU need one each.
  * Host errors: TV_ERR_ARG, TV_ERR_SHAPE, TV_ERR_WORKSPACE, TV_ERR_DTYPE (TV_ATTN_TCGEN05 asked for
  * an unsupported shape).
- * Device errors, that request's rows left alone: TV_ERR_ARG (starts that descend or leave 0 ..
- * n_new, L < n), TV_ERR_CAPACITY (L > raw_cap or more entries than cap_m); TV_ERR_ARG for a page
+ * Device errors, that request's rows left alone: TV_ERR_ARG (starts that leave 0 .. n_new or, with
+ * all outputs unspecified, descend; L < n), TV_ERR_CAPACITY (L > raw_cap or more entries than cap_m); TV_ERR_ARG for a page
  * that is missing (page 0 is read instead); TV_ERR_TIMEOUT.
  */
 size_t tv_chunk_workspace_size(const tv_shape* shape, int32_t n_new);

@@ -319,6 +319,48 @@ def test_attend_windows_and_compressors(W, tail, ms, d, dtype, H, P):
     s.check_attend()
 
 
+@pytest.mark.parametrize("d,H", [(512, 64), (512, 128), (512, 24), (512, 1), (384, 16), (256, 11), (128, 64),
+                                 (128, 3)])
+@pytest.mark.parametrize("P", [0, 1024])
+@pytest.mark.parametrize("W", [0, 128, 300])
+def test_attend_decoding_batches(d, H, P, W):
+    # requests of no, one and two tokens at lengths around every tile boundary
+    before = [0, 3, 4, 63, 64, 126, 127, 128, 255, 511, 512, 600, 1023, 1024, 1500, 2047, 3000, 5, 900]
+    news = [1, 1, 1, 1, 0, 1, 1, 2, 1, 1, 1, 1, 1, 2, 1, 0, 1, 1, 1]
+    s = Batch(before, news, H=H, d=d, dtype="bf16", P=P, W=W, q_std=2.0, seed=W + H)
+    s.append()
+    s.attend()
+    torch.cuda.synchronize()
+    assert s.status.item() == 0
+    s.check_attend()
+
+
+@pytest.mark.parametrize("d,H,before,n", [(512, 64, 40000, 1), (512, 64, 9000, 2), (512, 16, 20000, 5),
+                                          (128, 8, 5000, 150), (256, 16, 100, 90)])
+def test_attend_long_requests(d, H, before, n):
+    s = Batch([before], [n], H=H, d=d, dtype="bf16", P=2048, q_std=2.0, seed=n)
+    s.append()
+    s.attend()
+    torch.cuda.synchronize()
+    assert s.status.item() == 0
+    s.check_attend()
+
+
+def test_attend_growing_maxima():
+    # logits that grow by hundreds from tile to tile: every tile rescales what is there
+    s = Batch([6000, 6000], [1, 1], H=64, d=512, dtype="bf16", P=512, q_std=0.0, seed=13)
+    s.append()
+    ramp = torch.linspace(0, 1, s.t["c4K"].shape[1], device="cuda")
+    for b in range(2):
+        for g, page in enumerate(s.table[b].tolist()):
+            s.t["c4K"][page] = ((g + ramp) / 12).bfloat16()[:, None] * (1 if b == 0 else -1)
+    s.Q[:] = 1.0
+    s.attend(scale=1.0)
+    torch.cuda.synchronize()
+    assert s.status.item() == 0
+    s.check_attend(scale=1.0)
+
+
 def test_attend_equals_one_token_at_a_time():
     # a chunk sees what its tokens would have seen one by one (up to the order of sums)
     s = Batch([900, 0], [37, 5], H=64, d=512, dtype="bf16", P=512, seed=6)

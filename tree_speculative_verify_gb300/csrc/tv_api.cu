@@ -746,10 +746,13 @@ extern "C" int tv_chunk_append(const tv_shape* s, int32_t n_new, const int32_t* 
                           Qr, rawK, rawV, c4K, c4V, c128K, c128V, L, status, (cudaStream_t)stream);
 }
 
-static bool chunk_tc_supported(const tv_shape* s) { return tv_chunk_tc_ok(s) && tv_tc_available(); }
-static bool chunk_use_tc(const tv_shape* s) {
-  if (s->attn_kernel == TV_ATTN_SIMT) return false;
-  return s->attn_kernel == TV_ATTN_TCGEN05 || chunk_tc_supported(s);
+// The kernel of a chunk.  Tensor cores, bf16: d = 512 with more than two 64-row items per request on
+// average on the tree attention's clusters, which share a tile of keys and values among 256 rows;
+// otherwise, and for d = 128, 256 and 384, 64 rows per CTA.  CUDA cores: everything else.
+enum ChunkKernel { kChunkSimt, kChunkFew, kChunkMany };
+static ChunkKernel chunk_kernel(const tv_shape* s, int32_t n_new) {
+  if (s->attn_kernel == TV_ATTN_SIMT || !tv_few_ok(s) || !tv_tc_available()) return kChunkSimt;
+  return s->d == 512 && (int64_t)n_new * s->H > 128 * (int64_t)s->B ? kChunkMany : kChunkFew;
 }
 
 extern "C" size_t tv_chunk_workspace_size(const tv_shape* s, int32_t n_new) {
@@ -759,8 +762,11 @@ extern "C" size_t tv_chunk_workspace_size(const tv_shape* s, int32_t n_new) {
     tv_set_error(TV_ERR_SHAPE, "%s: n_new * H >= 2^31", fn);
     return 0;
   }
-  return align256(chunk_use_tc(s) ? tv_chunk_tc_workspace(s, n_new)
-                                  : tv_chunk_simt_workspace(s, n_new)) + 256;
+  // enough for any call of fewer tokens too, whichever kernel takes it
+  if (chunk_kernel(s, n_new) == kChunkSimt) return align256(tv_chunk_simt_workspace(s, n_new));
+  const size_t few = tv_few_workspace(s, n_new);
+  const size_t many = s->d == 512 ? tv_chunk_tc_workspace(s, n_new) : 0;
+  return align256(few > many ? few : many);
 }
 
 extern "C" int tv_chunk_attn(const tv_shape* s, int32_t n_new, const int32_t* starts, const void* Q,
@@ -791,13 +797,14 @@ extern "C" int tv_chunk_attn(const tv_shape* s, int32_t n_new, const int32_t* st
   if (ws_bytes < need)
     return tv_set_error(TV_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", fn, ws_bytes,
                         need);
-  if (chunk_use_tc(s)) {
-    if (!chunk_tc_supported(s))
-      return tv_set_error(TV_ERR_DTYPE, "%s: the tcgen05 kernel needs bf16, d = 512 and an sm_103 device",
-                          fn);
-    return tv_launch_chunk_tc(s, n_new, starts, Q, c4K, c4V, c128K, c128V, rawK, rawV, L, scale, O,
-                              lse, workspace, status, (cudaStream_t)stream);
-  }
+  const ChunkKernel k = chunk_kernel(s, n_new);
+  if (k == kChunkSimt && s->attn_kernel == TV_ATTN_TCGEN05)
+    return tv_set_error(TV_ERR_DTYPE, "%s: the tcgen05 kernels need bf16, d a multiple of 128 and an "
+                        "sm_103 device", fn);
+  if (k != kChunkSimt)
+    return (k == kChunkMany ? tv_launch_chunk_tc : tv_launch_few)(
+        s, n_new, starts, Q, c4K, c4V, c128K, c128V, rawK, rawV, L, scale, O, lse, workspace, status,
+        (cudaStream_t)stream);
   return tv_launch_chunk_attn(s, n_new, starts, Q, c4K, c4V, c128K, c128V, rawK, rawV, L, scale, O,
                               lse, workspace, status, (cudaStream_t)stream);
 }

@@ -70,6 +70,7 @@
 #include <mutex>
 
 #include "tv_attn_tc.cuh"
+#include "tv_chunk.cuh"
 #include "tv_sm100.cuh"
 
 namespace tv {
@@ -488,17 +489,17 @@ __device__ __forceinline__ void chunk_item(const Params& p, const int32_t* start
   it.pos0 = L - n;
   const int last = (int)(rows < first + 256 ? rows : first + 256) - 1;
   const int p_lo = it.pos0 + (int)first / p.H, p_hi = it.pos0 + last / p.H;
+  const Span span = span_of(p.comp_mask, p.tail_mode, p.W, p_lo, p_hi, kPaged);
   Layout& y = it.y;
-  y.L = p_hi + 1;
-  y.n4 = (p.comp_mask & TV_COMP_C4) ? p_hi / 4 : 0;
-  y.n128 = (p.comp_mask & TV_COMP_C128) ? p_hi / 128 : 0;
-  y.t0 = raw_lo_of(p_lo, p.tail_mode, p.W, m_min_of(p.comp_mask));
-  if (kPaged) y.t0 &= ~127;   // raw tiles that lie on one page (pages hold a multiple of 512 rows)
-  y.nraw = y.L - y.t0;
-  y.T4 = (y.n4 + 127) / 128;
-  y.T128 = (y.n128 + 127) / 128;
-  y.Traw = (y.nraw + 127) / 128;
-  y.T = y.T4 + y.T128 + y.Traw;
+  y.L = span.end;
+  y.n4 = span.n4;
+  y.n128 = span.n128;
+  y.t0 = span.t0;
+  y.nraw = span.end - span.t0;
+  y.T4 = span.T4;
+  y.T128 = span.T128;
+  y.Traw = span.T - span.T4 - span.T128;
+  y.T = span.T;
   it.nc = min(p.n_chunks, (y.T + kChunkTiles - 1) / kChunkTiles);
   if (chunk >= it.nc) return;
   it.tb = (int)((int64_t)y.T * chunk / it.nc);
@@ -1554,11 +1555,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
 // multiple of 16) per request.  A page holds 4 entries per 512 tokens, too few for the attention's
 // 64-row boxes.  Rows up to the next multiple of 16 are zeros: the values of masked columns are
 // multiplied by zero probabilities.  A warp per row.
-__global__ void gather_c128_kernel(Paging pg, int64_t c128_cap, int64_t stride, int64_t raw_cap,
+__global__ void gather_c128_kernel(Paging pg, int row_u4, int64_t c128_cap, int64_t stride, int64_t raw_cap,
                                    const int32_t* L, const uint4* __restrict__ K,
                                    const uint4* __restrict__ V, uint4* gK, uint4* gV,
                                    int32_t* status) {
-  constexpr int kRowU4 = 512 * 2 / 16;
   pdl_wait();
   pdl_launch_dependents();
   const int b = blockIdx.y, lane = threadIdx.x & 31, Lb = L[b];
@@ -1567,13 +1567,13 @@ __global__ void gather_c128_kernel(Paging pg, int64_t c128_cap, int64_t stride, 
   for (int64_t w = (int64_t)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32; w < ((n + 15) & ~15);
        w += (int64_t)gridDim.x * (blockDim.x / 32)) {
     const bool some = w < n;
-    const int64_t src = some ? layer_row(pg, b, w, c128_cap, 128, status) * kRowU4 : 0;
-    const int64_t dst = ((int64_t)b * stride + w) * kRowU4;
-#pragma unroll
-    for (int i = 0; i < kRowU4; i += 32) {
+    const int64_t src = some ? layer_row(pg, b, w, c128_cap, 128, status) * row_u4 : 0;
+    const int64_t dst = ((int64_t)b * stride + w) * row_u4;
+#pragma unroll 2
+    for (int i = lane; i < row_u4; i += 32) {
       const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-      gK[dst + i + lane] = some ? K[src + i + lane] : z;
-      gV[dst + i + lane] = some ? V[src + i + lane] : z;
+      gK[dst + i] = some ? K[src + i] : z;
+      gV[dst + i] = some ? V[src + i] : z;
     }
   }
 }
@@ -1644,18 +1644,23 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// 2-D (rows x 512) or 3-D (B x rows x 512) bf16 map with the 128-byte swizzle, box 64 x box_rows.
-bool make_map(CUtensorMap* m, const void* base, int rank, uint64_t rows, uint64_t batch,
-              uint32_t box_rows) {
+// 2-D (rows x d) or 3-D (batch x rows x d) bf16 map with the 128-byte swizzle, box 64 x box_rows.
+bool make_map_d(CUtensorMap* m, const void* base, int rank, int d, uint64_t rows, uint64_t batch,
+                uint32_t box_rows) {
   auto fn = encode_fn();
   if (fn == nullptr || base == nullptr) return false;
-  cuuint64_t dims[3] = {512, rows, batch};
-  cuuint64_t strides[2] = {512 * 2, rows * 512 * 2};
+  cuuint64_t dims[3] = {(cuuint64_t)d, rows, batch};
+  cuuint64_t strides[2] = {(cuuint64_t)d * 2, rows * d * 2};
   cuuint32_t box[3] = {64, box_rows, 1};
   cuuint32_t es[3] = {1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides,
             box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool make_map(CUtensorMap* m, const void* base, int rank, uint64_t rows, uint64_t batch,
+              uint32_t box_rows) {
+  return make_map_d(m, base, rank, 512, rows, batch, box_rows);
 }
 
 int n_pairs_of(const tv_shape* s) { return ((s->D * s->H + 127) / 128 + 1) / 2; }
@@ -1964,6 +1969,16 @@ int tv_launch_attn_tc(const tv_shape* s, const tv::AttnParams<__nv_bfloat16>& a,
 }
 
 // ---- chunks of new tokens --------------------------------------------------------------------------
+bool tv_make_map(CUtensorMap* m, const void* base, int rank, int d, uint64_t rows, uint64_t batch,
+                 uint32_t box_rows) {
+  return make_map_d(m, base, rank, d, rows, batch, box_rows);
+}
+
+void tv_attn_test_aid(uint64_t* timeout_ns, int* withhold_tile) {
+  *timeout_ns = (uint64_t)g_timeout_ns.load();
+  *withhold_tile = g_withhold_tile.load();
+}
+
 bool tv_chunk_tc_ok(const tv_shape* s) {
   const int64_t lim = (int64_t)1 << 31;
   return s->dtype == TV_BF16 && s->d == 512 && (int64_t)s->B * (s->c128_cap + 16) < lim &&
@@ -1971,44 +1986,51 @@ bool tv_chunk_tc_ok(const tv_shape* s) {
           ((int64_t)s->B * s->raw_cap < lim && (int64_t)s->B * s->c4_cap < lim));
 }
 
+constexpr int kMostClusters = 64;   // (a device with more clusters splits no further)
+
 static int64_t chunk_slots(const tv_shape* s, int n_new) {
   return (int64_t)n_new * s->H / 256 + s->B;
 }
 
-// KV chunks that an item may be split into, from the same model as tc_chunks: items (at most the
-// slots, as the host does not know the requests' sizes) over the resident clusters, with the tiles of
-// a full cache; the kernel splits an item with fewer tiles into fewer.
+// KV chunks that an item may be split into: while the items (at most the slots, as the host does not
+// know the requests' sizes) do not fill the resident clusters twice, enough for that, up to one per
+// kChunkTiles tiles of a full cache; the kernel splits an item with fewer tiles into fewer.
 static int chunk_kv_chunks(const tv_shape* s, int n_new) {
   int slots = cluster_slots();
   if (slots <= 0) slots = 36;
+  if (slots > kMostClusters) slots = kMostClusters;
   const int64_t items = chunk_slots(s, n_new);
-  if (items >= 4 * slots) return 1;
   int64_t tiles = 2 + (s->tail_mode == TV_TAIL_WINDOW ? (s->W + 127) / 128 : 1);
   if (s->comp_mask & TV_COMP_C4) tiles += (s->c4_cap + 127) / 128;
   if (s->comp_mask & TV_COMP_C128) tiles += (s->c128_cap + 127) / 128;
-  constexpr int64_t kItemTiles = 4;
-  const int n_max = (int)(tiles < 64 ? tiles : 64);
-  int64_t best_cost = -1, cost[65];
-  for (int n = 1; n <= n_max; ++n) {
-    cost[n] = (items * n + slots - 1) / slots * ((tiles + n - 1) / n + kItemTiles);
-    if (best_cost < 0 || cost[n] < best_cost) best_cost = cost[n];
-  }
-  for (int n = 1; n <= n_max; ++n)
-    if (10 * cost[n] <= 11 * best_cost) return n;
-  return 1;
+  const int64_t n = items > 0 ? (2 * slots + items - 1) / items : 1, most = tiles / tv::tc::kChunkTiles;
+  return (int)(n < most ? n : most < 1 ? 1 : most);
 }
 
-static int64_t chunk_c128_stride(const tv_shape* s) { return (s->c128_cap + 15) / 16 * 16; }
-static size_t chunk_gather_bytes(const tv_shape* s) {   // one of K / V (multiple of 1 KB)
+int64_t tv_chunk_c128_stride(const tv_shape* s) { return (s->c128_cap + 15) / 16 * 16; }
+size_t tv_chunk_gather_bytes(const tv_shape* s) {
   return s->page_tokens > 0 && (s->comp_mask & TV_COMP_C128)
-             ? (size_t)s->B * chunk_c128_stride(s) * 1024
+             ? (size_t)s->B * tv_chunk_c128_stride(s) * s->d * 2
              : 0;
 }
 
+int tv_chunk_gather(const tv_shape* s, const int32_t* L, const void* c128K, const void* c128V,
+                    void* rows, int32_t* status, cudaStream_t stream) {
+  const int64_t n = (s->c128_cap + 7) / 8;
+  uint4* to = reinterpret_cast<uint4*>(rows);
+  if (tv::launch_pdl(tv::tc::gather_c128_kernel, dim3((unsigned)(n < 64 ? n : 64), s->B), dim3(256), 0,
+                     stream, tv::paging_of(s), s->d * 2 / 16, s->c128_cap, tv_chunk_c128_stride(s),
+                     s->raw_cap, L, (const uint4*)c128K, (const uint4*)c128V, to,
+                     to + tv_chunk_gather_bytes(s) / 16, status) != cudaSuccess)
+    return tv_check_launch("tv_chunk_attn");
+  return TV_OK;
+}
+
+// Rows times KV chunks never exceed 256 (2 kMostClusters + items), and items are below twice the
+// clusters where there is more than one chunk; no more is asked for more tokens.
 size_t tv_chunk_tc_workspace(const tv_shape* s, int n_new) {
-  const int n = chunk_kv_chunks(s, n_new);
-  return 2 * chunk_gather_bytes(s) +
-         (n > 1 ? (size_t)n_new * s->H * n * (512 + 4) * sizeof(float) : 0);
+  const int64_t rows = (int64_t)n_new * s->H * 64, most = 256 * 4 * kMostClusters;
+  return 2 * tv_chunk_gather_bytes(s) + (size_t)(rows < most ? rows : most) * (512 + 4) * sizeof(float);
 }
 
 int tv_launch_chunk_tc(const tv_shape* s, int n_new, const int32_t* starts, const void* Q,
@@ -2021,14 +2043,14 @@ int tv_launch_chunk_tc(const tv_shape* s, int n_new, const int32_t* starts, cons
   const bool c4 = s->comp_mask & TV_COMP_C4, c128 = s->comp_mask & TV_COMP_C128;
   const bool paged = s->page_tokens > 0;
   char* ws = reinterpret_cast<char*>(workspace);
-  const size_t gather = chunk_gather_bytes(s);
+  const size_t gather = tv_chunk_gather_bytes(s);
   const uint64_t pool = (uint64_t)s->n_pool_pages * (paged ? s->page_tokens : 0);
   auto rows_or_one = [](uint64_t r) { return r > 0 ? r : (uint64_t)1; };
   const uint64_t B = (uint64_t)s->B, rows = (uint64_t)n_new * s->H;
   const uint64_t rawrows = rows_or_one(paged ? pool : B * (uint64_t)s->raw_cap);
   // an inactive compressor's maps are pointed at the raw rows (never read: it has no tiles)
   const uint64_t c4rows = !c4 ? rawrows : rows_or_one(paged ? pool / 4 : B * (uint64_t)s->c4_cap);
-  const int64_t stride = paged ? chunk_c128_stride(s) : s->c128_cap;
+  const int64_t stride = paged ? tv_chunk_c128_stride(s) : s->c128_cap;
   const uint64_t c128rows = !c128 ? rawrows : rows_or_one(B * (uint64_t)stride);
   const void* k4 = c4 ? c4K : rawK;
   const void* v4 = c4 ? c4V : rawV;
@@ -2075,13 +2097,8 @@ int tv_launch_chunk_tc(const tv_shape* s, int n_new, const int32_t* starts, cons
   p.timeout_ns = (uint64_t)g_timeout_ns.load();
   p.withhold_tile = g_withhold_tile.load();
   if (cluster_slots() <= 0) return tv_check_launch(fn);
-  if (gather > 0) {
-    const int64_t n = (s->c128_cap + 7) / 8;
-    if (tv::launch_pdl(gather_c128_kernel, dim3((unsigned)(n < 64 ? n : 64), s->B), dim3(256), 0,
-                       stream, p.pg, s->c128_cap, stride, s->raw_cap, L, (const uint4*)c128K,
-                       (const uint4*)c128V, (uint4*)ws, (uint4*)(ws + gather), status) != cudaSuccess)
-      return tv_check_launch(fn);
-  }
+  if (gather > 0)
+    if (int rc = tv_chunk_gather(s, L, c128K, c128V, ws, status, stream)) return rc;
   const int64_t items = (int64_t)p.n_slots * p.n_chunks;
   const int64_t clusters = items < cluster_slots() ? items : cluster_slots();
   cudaLaunchConfig_t cfg = {};

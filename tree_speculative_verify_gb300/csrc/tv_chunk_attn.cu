@@ -29,16 +29,6 @@ struct ChunkAttnArgs {
   int32_t* status;
 };
 
-// 0, or the error that leaves request b's rows alone.
-__device__ __forceinline__ int attn_state(const Chunk& c, int b) {
-  const int lo = c.starts[b], hi = c.starts[b + 1];
-  if (lo < 0 || hi < lo || hi > c.n_new) return TV_ERR_ARG;
-  if (hi == lo) return TV_OK;
-  const int L = c.L[b];
-  if (L < hi - lo) return TV_ERR_ARG;
-  return chunk_fits(c, L) ? TV_OK : TV_ERR_CAPACITY;
-}
-
 constexpr int kShare = 128;   // least entries of a share
 
 // R rows of one request and what they see.  Slots as in the tensor-core kernel: request b's tiles of R
@@ -383,9 +373,11 @@ static int launch_chunk_attn(const ChunkAttnArgs& a, int R, int64_t slots, const
 
 }  // namespace tv
 
+// Rows times shares never exceed 64 (2 * 152 + slots), and slots are below 2 * 152 where there is more
+// than one share; no more is asked for more tokens.
 size_t tv_chunk_simt_workspace(const tv_shape* s, int n_new) {
-  const int n = tv::simt_chunks(s, n_new);
-  return n > 1 ? (size_t)n_new * s->H * n * (s->d + 4) * sizeof(float) : 0;
+  const int64_t rows = (int64_t)n_new * s->H * 64, most = 64 * 4 * 152;
+  return (size_t)(rows < most ? rows : most) * (s->d + 4) * sizeof(float);
 }
 
 int tv_launch_chunk_attn(const tv_shape* s, int n_new, const int32_t* starts, const void* Q,
