@@ -489,17 +489,17 @@ __device__ __forceinline__ void chunk_item(const Params& p, const int32_t* start
   it.pos0 = L - n;
   const int last = (int)(rows < first + 256 ? rows : first + 256) - 1;
   const int p_lo = it.pos0 + (int)first / p.H, p_hi = it.pos0 + last / p.H;
-  const Span span = span_of(p.comp_mask, p.tail_mode, p.W, p_lo, p_hi, kPaged);
+  const Span span = span_of(p.comp_mask, p.tail_mode, p.W, p_lo, p_hi, kPaged ? 128 : 1);
   Layout& y = it.y;
   y.L = span.end;
   y.n4 = span.n4;
   y.n128 = span.n128;
   y.t0 = span.t0;
   y.nraw = span.end - span.t0;
-  y.T4 = span.T4;
-  y.T128 = span.T128;
-  y.Traw = span.T - span.T4 - span.T128;
-  y.T = span.T;
+  y.T4 = (y.n4 + 127) / 128;
+  y.T128 = (y.n128 + 127) / 128;
+  y.Traw = (y.nraw + 127) / 128;
+  y.T = y.T4 + y.T128 + y.Traw;
   it.nc = min(p.n_chunks, (y.T + kChunkTiles - 1) / kChunkTiles);
   if (chunk >= it.nc) return;
   it.tb = (int)((int64_t)y.T * chunk / it.nc);
@@ -1552,8 +1552,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
 
 // ---- chunks of new tokens: what goes around the attention ------------------------------------------
 // Paged pools: copies each request's C128 entries into contiguous rows of the workspace, `stride` (a
-// multiple of 16) per request.  A page holds 4 entries per 512 tokens, too few for the attention's
-// 64-row boxes.  Rows up to the next multiple of 16 are zeros: the values of masked columns are
+// multiple of 64) per request.  A page holds 4 entries per 512 tokens, too few for the attention's
+// 64-row boxes.  Rows up to the next multiple of 64 are zeros: the values of masked entries are
 // multiplied by zero probabilities.  A warp per row.
 __global__ void gather_c128_kernel(Paging pg, int row_u4, int64_t c128_cap, int64_t stride, int64_t raw_cap,
                                    const int32_t* L, const uint4* __restrict__ K,
@@ -1564,7 +1564,7 @@ __global__ void gather_c128_kernel(Paging pg, int row_u4, int64_t c128_cap, int6
   const int b = blockIdx.y, lane = threadIdx.x & 31, Lb = L[b];
   if (Lb <= 0 || Lb > raw_cap) return;
   const int n = (Lb - 1) / 128;   // the last token sees no more
-  for (int64_t w = (int64_t)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32; w < ((n + 15) & ~15);
+  for (int64_t w = (int64_t)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32; w < ((n + 63) & ~63);
        w += (int64_t)gridDim.x * (blockDim.x / 32)) {
     const bool some = w < n;
     const int64_t src = some ? layer_row(pg, b, w, c128_cap, 128, status) * row_u4 : 0;
@@ -1981,7 +1981,7 @@ void tv_attn_test_aid(uint64_t* timeout_ns, int* withhold_tile) {
 
 bool tv_chunk_tc_ok(const tv_shape* s) {
   const int64_t lim = (int64_t)1 << 31;
-  return s->dtype == TV_BF16 && s->d == 512 && (int64_t)s->B * (s->c128_cap + 16) < lim &&
+  return s->dtype == TV_BF16 && s->d == 512 && (int64_t)s->B * (s->c128_cap + 63) < lim &&
          (s->page_tokens > 0 ||
           ((int64_t)s->B * s->raw_cap < lim && (int64_t)s->B * s->c4_cap < lim));
 }
@@ -2007,7 +2007,7 @@ static int chunk_kv_chunks(const tv_shape* s, int n_new) {
   return (int)(n < most ? n : most < 1 ? 1 : most);
 }
 
-int64_t tv_chunk_c128_stride(const tv_shape* s) { return (s->c128_cap + 15) / 16 * 16; }
+int64_t tv_chunk_c128_stride(const tv_shape* s) { return (s->c128_cap + 63) / 64 * 64; }
 size_t tv_chunk_gather_bytes(const tv_shape* s) {
   return s->page_tokens > 0 && (s->comp_mask & TV_COMP_C128)
              ? (size_t)s->B * tv_chunk_c128_stride(s) * s->d * 2

@@ -40,25 +40,20 @@ __device__ __forceinline__ bool chunk_fits(const Chunk& c, int64_t len) {
          (!(c.comp_mask & TV_COMP_C128) || len / 128 <= c.c128_cap);
 }
 
-// What the tokens at positions p_lo .. p_hi see, as far as the last and from where the first does, in
-// tiles of 128 entries: C4, then C128, then raw rows t0 .. p_hi.  aligned: raw tiles start at multiples
-// of 128, so that each lies on one page.
+// What the tokens at positions p_lo .. p_hi see, as far as the last and from where the first does: C4
+// entries, C128 entries, raw rows t0 .. end - 1.  align: t0 is a multiple of it, so that tiles of as many
+// raw rows lie on one page each.
 struct Span {
   int n4, n128, t0, end;
-  int T4, T128, T;
 };
 
 __device__ __forceinline__ Span span_of(int comp_mask, int tail_mode, int W, int p_lo, int p_hi,
-                                        bool aligned) {
+                                        int align) {
   Span s;
   s.n4 = (comp_mask & TV_COMP_C4) ? p_hi / 4 : 0;
   s.n128 = (comp_mask & TV_COMP_C128) ? p_hi / 128 : 0;
-  s.t0 = raw_lo_of(p_lo, tail_mode, W, m_min_of(comp_mask));
-  if (aligned) s.t0 &= ~127;
+  s.t0 = raw_lo_of(p_lo, tail_mode, W, m_min_of(comp_mask)) & ~(align - 1);
   s.end = p_hi + 1;
-  s.T4 = (s.n4 + 127) / 128;
-  s.T128 = (s.n128 + 127) / 128;
-  s.T = s.T4 + s.T128 + (s.end - s.t0 + 127) / 128;
   return s;
 }
 

@@ -13,10 +13,12 @@
 // O^T of 64 rows and 512 columns takes 256 TMEM columns, two S^T buffers 128: one CTA holds all of it,
 // without a cluster, and every SM streams a share of the batch's tiles.
 //
-// Work: the batch's tiles (128 entries of one item; an item is 64 rows of one request) in one list,
-// request by request; CTA c takes tiles c q .. c q + q - 1, which may end one item, hold whole ones and
-// begin another.  An item that one CTA has whole is written at once; the others leave (O, m, l) per
-// CTA in the workspace -- at most two per CTA -- which a second kernel joins in CTA order.
+// Work is counted in half tiles (64 entries of one item; an item is 64 rows of one request), of which two
+// make a tile: the batch's items stand in one list, request by request, each with kOpen places for opening it
+// and one per half tile, of which CTA c takes q from c q on; they may end one item, hold whole ones and
+// begin another.  An item that one CTA has whole is
+// written at once; the others leave (O, m, l) per CTA in the workspace -- at most two per CTA -- which a
+// second kernel joins in CTA order.
 //
 // Softmax: thread (entry, half of the rows) holds the entry's 32 logits; row maxima are reduced over
 // the lanes by halving exchanges and over the four warps of a half through shared memory; a lane keeps
@@ -43,25 +45,51 @@ constexpr int kThreads = 64 + 32 * kSmxWarps;
 constexpr int kSlotBytes = 16384;
 constexpr int kSlots = 8;          // (V slots are taken in pairs: an even number)
 constexpr int kPBytes = 16384;     // P^T of a tile: 128 entries x 64 rows
-constexpr int kMinTiles = 2;       // least tiles of a CTA while there are CTAs left
+constexpr int kOpen = 3;           // places for opening an item
+constexpr int kMinPlaces = 4;      // least places of a CTA while there are CTAs left
 constexpr float kRescaleThreshold = 8.f;   // log2 units
 
 struct Params {
   CUtensorMap mQ, mC4K, mC4V, mC128K, mC128V, mRawK, mRawV;   // boxes of 64 rows x 64 columns
   Chunk c;
   int H, W, tail_mode;
-  bool paged, gathered;    // gathered: C128 rows in the workspace, c128_stride per request
-  int64_t c128_stride;
+  int64_t c128_stride;     // C128 rows per request
+  bool gathered;           // pools: a page holds too few C128 entries for a box of 64, so the kernel in
+                           // front copies them into the workspace, where the maps point
   float scale_log2;
   __nv_bfloat16* O;
   float* lse;
   float* part;             // [CTA][2][kRows][d + 4]: 0: an item begun before, 1: one that goes on
   int n_slots;
-  int32_t* first_tile;     // [n_slots] of the slots' items (written by CTA 0), then the tiles per CTA
+  int2* pieces;            // [n_slots] of the slots' items: first CTA, CTAs (written by CTA 0)
   int32_t* status;
   uint64_t timeout_ns;
   int withhold_tile;       // test aid: no K copies for this tile of a segment (-1: none)
 };
+
+// An item: rows first .. of request b, its k-th, and the half tiles it takes.
+struct Item {
+  int b, k, row0, rows, pos0, first;
+  Span s;
+  int u4, u128, units;   // C4, C4 and C128, all
+};
+
+__device__ __forceinline__ Item item_of(const Params& p, int b, int k) {
+  Item it;
+  const int s0 = p.c.starts[b], n = p.c.starts[b + 1] - s0;
+  it.b = b;
+  it.k = k;
+  it.first = k * kRows;
+  it.row0 = s0 * p.H + it.first;
+  it.rows = min(kRows, n * p.H - it.first);
+  it.pos0 = p.c.L[b] - n;
+  it.s = span_of(p.c.comp_mask, p.tail_mode, p.W, it.pos0 + it.first / p.H,
+                 it.pos0 + (it.first + it.rows - 1) / p.H, p.c.pg.page_tokens != 0 ? 64 : 1);
+  it.u4 = (it.s.n4 + 63) / 64;
+  it.u128 = it.u4 + (it.s.n128 + 63) / 64;
+  it.units = it.u128 + (it.s.end - it.s.t0 + 63) / 64;
+  return it;
+}
 
 // (the dynamic window of a CTA is 227 KB)
 template <int D>
@@ -78,29 +106,12 @@ struct __align__(1024) Smem {
   uint64_t drain;
   float xmax[2][4][kRows];       // [tile parity][lane quadrant][row]: maxima, at a segment's end sums
   int scan[kThreads / 32 + 1];
-  int range[5];                  // the CTA's first item (request, item of it), its first tile
-                                 // there, tiles per CTA, all tiles
+  int begin, places;             // the CTA's first place in its first item, places in all
+  Item first;                    // its first item
   uint32_t tmem;
   int abort;
 };
 
-// An item: rows first .. of request b.
-struct Item {
-  int row0, rows, pos0, first;
-  Span s;
-};
-
-__device__ __forceinline__ Item item_of(const Params& p, int b, int k) {
-  Item it;
-  const int s0 = p.c.starts[b], n = p.c.starts[b + 1] - s0;
-  it.first = k * kRows;
-  it.row0 = s0 * p.H + it.first;
-  it.rows = min(kRows, n * p.H - it.first);
-  it.pos0 = p.c.L[b] - n;
-  it.s = span_of(p.c.comp_mask, p.tail_mode, p.W, it.pos0 + it.first / p.H,
-                 it.pos0 + (it.first + it.rows - 1) / p.H, p.paged);
-  return it;
-}
 __device__ __forceinline__ int items_of(const Params& p, int b) {
   if (attn_state(p.c, b) != TV_OK) return 0;
   return (int)(((int64_t)(p.c.starts[b + 1] - p.c.starts[b]) * p.H + kRows - 1) / kRows);
@@ -123,60 +134,88 @@ __device__ __forceinline__ int request_at(const Params& p, int slot) {   // -1: 
   return lo - 1;
 }
 
-// One CTA's walk over its tiles, the same in every warp: segments (item, tiles tb .. te - 1).
+// One CTA's walk over its half tiles, the same in every warp: segments (item, half tiles ub .. ue - 1).
 struct Walk {
-  int b, k, n_items, left;   // request, item within it, tiles that remain
-  int skip;                  // tiles of the first item that earlier CTAs have
   Item it;
-  int tb, te;
+  int n_items;   // of the request
+  int left;      // places that remain
+  int ub, ue;
+  bool begun;
+  template <typename S>
+  __device__ Walk(const Params& p, const S& sm) {
+    left = sm.places;
+    if (left <= 0) return;
+    it = sm.first;
+    ub = max(sm.begin - kOpen, 0);
+    left -= max(kOpen - sm.begin, 0);
+    n_items = -1;   // (looked up when the first item is done)
+    begun = false;
+  }
   __device__ bool next(const Params& p) {
     if (left <= 0) return false;
-    while (k >= n_items) {
-      if (++b >= p.c.B) return false;
-      n_items = items_of(p, b);
-      k = 0;
+    if (begun) {
+      int b = it.b, k = it.k + 1;
+      if (n_items < 0) n_items = items_of(p, b);
+      while (k >= n_items) {
+        if (++b >= p.c.B) return false;
+        n_items = items_of(p, b);
+        k = 0;
+      }
+      it = item_of(p, b, k);
+      ub = 0;
+      left -= kOpen;
     }
-    it = item_of(p, b, k);
-    tb = skip;
-    te = min(it.s.T, skip + left);
-    left -= te - tb;
-    skip = 0;
-    ++k;
-    return true;
+    begun = true;
+    ue = min(it.units, ub + left);
+    left -= ue - ub;
+    return ue > ub;   // (the last place may be an item's opening)
   }
-  __device__ bool whole() const { return tb == 0 && te == it.s.T; }
+  __device__ bool whole() const { return ub == 0 && ue == it.units; }
 };
 
-__device__ __forceinline__ Walk walk_from(const Params& p, const int* range) {
-  Walk w;
-  w.left = min(range[3], range[4] - (int)blockIdx.x * range[3]);
-  w.b = range[0];
-  w.k = range[1];
-  w.skip = range[2];
-  w.n_items = w.left > 0 ? items_of(p, w.b) : 0;
-  return w;
+// A tile: two neighbouring half tiles, or a last one.  Entries of a first half that is not full are
+// masked, as are those past the second's, up to a multiple of 16.
+struct Half {
+  int kind, row0, valid;   // 0: C4, 1: C128, 2: raw; first entry, entries
+};
+struct Tile {
+  Half first, second;
+  int units, n16;          // halves; entries that the products take
+};
+__device__ __forceinline__ Half half_at(const Item& it, int u) {
+  Half h;
+  int end;
+  if (u < it.u4) {
+    h.kind = 0;
+    h.row0 = 64 * u;
+    end = it.s.n4;
+  } else if (u < it.u128) {
+    h.kind = 1;
+    h.row0 = 64 * (u - it.u4);
+    end = it.s.n128;
+  } else {
+    h.kind = 2;
+    h.row0 = it.s.t0 + 64 * (u - it.u128);
+    end = it.s.end;
+  }
+  h.valid = min(64, end - h.row0);
+  return h;
+}
+__device__ __forceinline__ Tile tile_at(const Item& it, int u, int ue) {
+  Tile x;
+  x.units = min(2, ue - u);
+  x.first = half_at(it, u);
+  x.second = half_at(it, min(u + 1, ue - 1));   // (one half: the first again)
+  x.n16 = (64 * (x.units - 1) + x.second.valid + 15) & ~15;
+  return x;
 }
 
-struct Tile {
-  int kind, row0, valid, n16;   // 0: C4, 1: C128, 2: raw; entries rounded up to 16
-};
-__device__ __forceinline__ Tile tile_at(const Span& s, int t) {
-  Tile x;
-  if (t < s.T4) {
-    x.kind = 0;
-    x.row0 = 128 * t;
-    x.valid = min(128, s.n4 - x.row0);
-  } else if (t < s.T4 + s.T128) {
-    x.kind = 1;
-    x.row0 = 128 * (t - s.T4);
-    x.valid = min(128, s.n128 - x.row0);
-  } else {
-    x.kind = 2;
-    x.row0 = s.t0 + 128 * (t - s.T4 - s.T128);
-    x.valid = min(128, s.end - x.row0);
-  }
-  x.n16 = (x.valid + 15) & ~15;
-  return x;
+// The row at which a half starts in its layer's map (64 entries from a multiple of 64 on lie on one
+// page).
+__device__ __forceinline__ int row_of(const Params& p, int b, const Half& h) {
+  if (h.kind == 1) return (int)((int64_t)b * p.c128_stride + h.row0);
+  return (int)(h.kind == 0 ? layer_row(p.c.pg, b, h.row0, p.c.c4_cap, 4, p.status)
+                           : layer_row(p.c.pg, b, h.row0, p.c.raw_cap, 1, p.status));
 }
 
 template <typename S>
@@ -184,75 +223,74 @@ __device__ __forceinline__ void fail(S& sm, int32_t* status) {
   if (atomicExch(&sm.abort, 1) == 0) record_error(status, TV_ERR_TIMEOUT);
 }
 
-// ---- copies (warp 0, lane 0) ---------------------------------------------------------------------
+// ---- copies (warp 0) -------------------------------------------------------------------------------
 template <int D>
 __device__ void producer(const Params& p, Smem<D>& sm) {
   constexpr int kSlices = D / 64;
-  Walk w = walk_from(p, sm.range);
+  const int lane = threadIdx.x & 31;
+  Walk w(p, sm);
   int slot = 0, seg = 0;
   uint32_t phase = 0;
-  bool ok = true, waited = !p.gathered;
-  auto acquire = [&] {
-    if (!mbar_wait(&sm.empty[slot], phase ^ 1, &sm.abort, p.timeout_ns)) {
-      fail(sm, p.status);
+  bool ok = true;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (!__all_sync(0xffffffffu, mbar_wait(bar, parity, &sm.abort, p.timeout_ns))) {
+      if (lane == 0) fail(sm, p.status);
       ok = false;
     }
     return ok;
   };
-  auto advance = [&] {
-    if (++slot == kSlots) {
-      slot = 0;
-      phase ^= 1;
-    }
-  };
-  // where a tile's rows start in its map (a tile lies on one page)
-  auto row_of = [&](const Tile& x) -> int {
-    if (x.kind == 0) return (int)layer_row(p.c.pg, w.b, x.row0, p.c.c4_cap, 4, p.status);
-    if (x.kind == 2) return (int)layer_row(p.c.pg, w.b, x.row0, p.c.raw_cap, 1, p.status);
-    return (int)((int64_t)w.b * p.c128_stride + x.row0);
-  };
-  auto load = [&](const Tile& x, int row, const CUtensorMap* m, bool issue) {
-    const int halves = (x.n16 + 63) / 64;
-    for (int s = 0; s < kSlices && ok; ++s) {
-      if (!acquire()) return;
+  // lanes 0 and 1 copy the halves of a slot: `row` is theirs, `map` its half's
+  auto load = [&](const Tile& x, int row, const CUtensorMap* map, bool issue) {
+    for (int s = 0; s < kSlices; ++s) {
+      if (!wait(&sm.empty[slot], phase ^ 1)) return;
       if (issue) {
-        mbar_arrive_expect_tx(&sm.full[slot], halves * 8192);
-        for (int h = 0; h < halves; ++h)
-          tma_load_2d(sm.ring[slot] + h * 8192, m, 64 * s, row + 64 * h, &sm.full[slot]);
+        if (lane == 0) mbar_arrive_expect_tx(&sm.full[slot], x.units * 8192);
+        __syncwarp();
+        if (lane < x.units) tma_load_2d(sm.ring[slot] + lane * 8192, map, 64 * s, row, &sm.full[slot]);
       }
-      advance();
+      if (++slot == kSlots) {
+        slot = 0;
+        phase ^= 1;
+      }
     }
   };
+  auto map_of = [&](const Tile& x, bool v) {
+    const int kind = lane & 1 ? x.second.kind : x.first.kind;
+    return kind == 0 ? (v ? &p.mC4V : &p.mC4K) : kind == 1 ? (v ? &p.mC128V : &p.mC128K)
+                                                           : (v ? &p.mRawV : &p.mRawK);
+  };
+  bool waited = !p.gathered;
   for (; ok && w.next(p); ++seg) {
-    if (seg > 0 && !mbar_wait(&sm.q_free, (seg - 1) & 1, &sm.abort, p.timeout_ns)) {
-      fail(sm, p.status);
-      break;
-    }
-    mbar_arrive_expect_tx(&sm.q_full, kSlices * kRows * 128);
-    for (int s = 0; s < kSlices; ++s)
-      tma_load_2d(sm.q[s], &p.mQ, 64 * s, w.it.row0, &sm.q_full);
-    // K_0, K_1, V_0, K_2, V_1, ..: the order in which the MMAs take them
-    Tile before;
-    int before_row = 0;
-    int row = row_of(tile_at(w.it.s, w.tb));
-    for (int t = w.tb; t <= w.te && ok; ++t) {
-      Tile x;
-      if (t < w.te) {
-        x = tile_at(w.it.s, t);
-        if (x.kind == 1 && !waited) {   // the gathered rows
+    if (seg > 0 && !wait(&sm.q_free, (seg - 1) & 1)) break;
+    if (lane == 0) mbar_arrive_expect_tx(&sm.q_full, kSlices * kRows * 128);
+    __syncwarp();
+    if (lane < kSlices) tma_load_2d(sm.q[lane], &p.mQ, 64 * lane, w.it.row0, &sm.q_full);
+    // K_0, K_1, V_0, K_2, V_1, ..: the order in which the MMAs take them; the next tile's rows are
+    // looked up before this one's copies
+    Tile x = tile_at(w.it, w.ub, w.ue), before = x;
+    int row = row_of(p, w.it.b, lane & 1 ? x.second : x.first), before_row = row;
+    for (int u = w.ub, t = 0; ok; ++t) {
+      const bool more = u < w.ue;
+      Tile after = x;
+      int after_row = row;
+      if (more && u + x.units < w.ue) {
+        after = tile_at(w.it, u + x.units, w.ue);
+        after_row = row_of(p, w.it.b, lane & 1 ? after.second : after.first);
+      }
+      if (more) {
+        if (!waited && (x.first.kind == 1 || x.second.kind == 1)) {
           pdl_wait();
           waited = true;
         }
-        load(x, row, x.kind == 0 ? &p.mC4K : x.kind == 1 ? &p.mC128K : &p.mRawK,
-             t - w.tb != p.withhold_tile);
+        load(x, row, map_of(x, false), t != p.withhold_tile);
       }
-      const int ahead = t + 1 < w.te ? row_of(tile_at(w.it.s, t + 1)) : 0;
-      if (t > w.tb)
-        load(before, before_row, before.kind == 0 ? &p.mC4V : before.kind == 1 ? &p.mC128V : &p.mRawV,
-             true);
+      if (t > 0 && ok) load(before, before_row, map_of(before, true), true);
+      if (!more) break;
+      u += x.units;
       before = x;
       before_row = row;
-      row = ahead;
+      x = after;
+      row = after_row;
     }
   }
   // nothing of this CTA's may be in flight when it exits: after an abort, what was issued is waited for
@@ -273,8 +311,8 @@ __device__ void mma(const Params& p, Smem<D>& sm) {
   const uint64_t ring_mn = smem_desc_sw128(smem_u32(sm.ring[0]), kSlotBytes, 1024);
   const uint64_t q_desc = smem_desc_sw128(smem_u32(sm.q[0]), 16, 1024);
   const uint64_t p_desc = smem_desc_sw128(smem_u32(sm.p[0]), 16, 1024);
-  Walk w = walk_from(p, sm.range);
-  int slot = 0, seg = 0, g = 0;   // g: tiles so far (of earlier segments)
+  Walk w(p, sm);
+  int slot = 0, seg = 0, i = 0;   // i: tiles so far
   uint32_t phase = 0;
   bool ok = true;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -291,8 +329,9 @@ __device__ void mma(const Params& p, Smem<D>& sm) {
     }
   };
   auto add = [](uint64_t desc, uint32_t bytes) { return desc + (uint64_t)(bytes >> 4); };
-  auto product_o = [&](int t, int i) {   // tile t of the segment, i-th of all
-    const int n_k = tile_at(w.it.s, w.tb + t).n16 / 16;
+  // O += V P of the i-th tile of all, the segment's t-th
+  auto product_o = [&](const Tile& x, int t, int i) {
+    const int n_k = x.n16 / 16;
     if (!wait(&sm.p_full[i & 1], (i >> 1) & 1)) return;
     tc_fence_after();
     const uint64_t pd = add(p_desc, (i & 1) * kPBytes);
@@ -311,11 +350,13 @@ __device__ void mma(const Params& p, Smem<D>& sm) {
     mma1_commit(&sm.pv_done[i & 1]);
   };
   for (; ok && w.next(p); ++seg) {
-    const int n = w.te - w.tb;
     if (!wait(&sm.q_full, seg & 1)) break;
     tc_fence_after();
-    for (int t = 0; t < n && ok; ++t) {
-      const int i = g + t;
+    Tile before;
+    int t = 0;
+    for (int u = w.ub; u < w.ue && ok; ++t, ++i) {
+      const Tile x = tile_at(w.it, u, w.ue);
+      u += x.units;
       if (i >= 2 && !wait(&sm.s_free[i & 1], ((i - 2) >> 1) & 1)) break;
       tc_fence_after();
       for (int s = 0; s < kSlices && ok; ++s) {
@@ -330,14 +371,14 @@ __device__ void mma(const Params& p, Smem<D>& sm) {
       }
       if (!ok) break;
       mma1_commit(&sm.s_full[i & 1]);
-      if (t == n - 1) mma1_commit(&sm.q_free);
+      if (u == w.ue) mma1_commit(&sm.q_free);
       if (t == 0 && seg > 0 && !wait(&sm.o_free, (seg - 1) & 1)) break;
-      if (t > 0) product_o(t - 1, i - 1);
+      if (t > 0) product_o(before, t - 1, i - 1);
+      before = x;
     }
-    if (ok) product_o(n - 1, g + n - 1);
+    if (ok) product_o(before, t - 1, i - 1);
     if (!ok) break;
     mma1_commit(&sm.o_full);
-    g += n;
   }
   // every MMA has completed before TMEM is released
   mma1_commit(&sm.drain);
@@ -374,7 +415,7 @@ __device__ void softmax(const Params& p, Smem<D>& sm) {
   const uint32_t tmem = sm.tmem + ((uint32_t)(32 * quad) << 16);
   const float sl2 = p.scale_log2;
   uint8_t* const line = sm.p[0] + (entry >> 3) * 1024 + (entry & 7) * 128;
-  Walk w = walk_from(p, sm.range);
+  Walk w(p, sm);
   int seg = 0, g = 0;
   // A wait that runs out sets the abort flag, after which every wait returns at once: the warps go on
   // through their barriers together and write nothing.
@@ -385,10 +426,20 @@ __device__ void softmax(const Params& p, Smem<D>& sm) {
       ok = false;
     }
   };
-  bool waited = false;
-  for (; w.next(p); ++seg) {
-    const Item& it = w.it;
-    const int n = w.te - w.tb, my_row = 32 * half + lane;
+  // The code is run once for nothing, a tile and an epilogue, while the first copies are on their way (on
+  // whatever TMEM holds, without barriers or results): fetched under load, as the second pass would find
+  // it, a tile takes 7 us instead of 1.
+  bool dry = true;
+  if (w.left <= 0) return;
+  bool waited = !p.gathered;
+  for (;;) {
+    Walk next = w;
+    if (!next.next(p)) break;
+    if (!dry) w = next;
+    const Item it = next.it;
+    const int ub = next.ub, ue = dry ? ub + 1 : next.ue;
+    const bool whole = next.whole();
+    const int my_row = 32 * half + lane;
     // the rows' tokens: row r belongs to position pos0 + (first + r) / H; one token in the common case
     const int p_first = it.pos0 + it.first / p.H;
     const int p_last = it.pos0 + (it.first + it.rows - 1) / p.H;   // (padding rows: anything)
@@ -396,10 +447,10 @@ __device__ void softmax(const Params& p, Smem<D>& sm) {
     float sum[32];
 #pragma unroll
     for (int j = 0; j < 32; ++j) sum[j] = 0.f;
-    for (int t = 0; t < n; ++t, ++g) {
-      const Tile x = tile_at(it.s, w.tb + t);
-      const int buf = g & 1;
-      wait(&sm.s_full[buf], (g >> 1) & 1);
+    for (int u = ub; u < ue;) {
+      const Tile x = tile_at(it, u, ue);
+      const int buf = dry ? 1 : g & 1;
+      if (!dry) wait(&sm.s_full[buf], (g >> 1) & 1);
       tc_fence_after();
       float s[32];
       {
@@ -409,13 +460,14 @@ __device__ void softmax(const Params& p, Smem<D>& sm) {
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.s_free[buf]);
-      // who sees this thread's entry: positions from .. until
-      const int e = x.row0 + entry;
+      if (lane == 0 && !dry) mbar_arrive(&sm.s_free[buf]);
+      // who sees this thread's entry: positions from .. until (the warp's entries are of one half)
+      const Half hf = quad >> 1 ? x.second : x.first;
+      const int in_half = entry & 63, e = hf.row0 + in_half;
       int from, until = 0x7fffffff;
-      if (x.kind == 0) {
+      if (hf.kind == 0) {
         from = 4 * e + 4;
-      } else if (x.kind == 1) {
+      } else if (hf.kind == 1) {
         from = 128 * e + 128;
       } else {
         from = e;
@@ -423,7 +475,7 @@ __device__ void softmax(const Params& p, Smem<D>& sm) {
                                               : e / m_min_of(p.c.comp_mask) * m_min_of(p.c.comp_mask) +
                                                     m_min_of(p.c.comp_mask) - 1;
       }
-      if (entry >= x.valid) from = 0x7fffffff;
+      if (in_half >= hf.valid || (quad >> 1) >= x.units) from = 0x7fffffff;
       if (!(from <= p_first && p_last <= until)) {
         if (p_first == p_last || from > p_last || until < p_first) {
 #pragma unroll
@@ -496,7 +548,9 @@ __device__ void softmax(const Params& p, Smem<D>& sm) {
       tc_fence_before();
       fence_proxy_async_smem();   // the MMA reads P through the async proxy
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.p_full[buf]);
+      if (lane == 0 && !dry) mbar_arrive(&sm.p_full[buf]);
+      u += x.units;
+      if (!dry) ++g;
     }
     // the rows' sums over the warp's entries, then over the four warps
     float l = lanes_reduce(sum, lane, [](float a, float b) { return a + b; });
@@ -505,17 +559,19 @@ __device__ void softmax(const Params& p, Smem<D>& sm) {
     half_sync(half);
     l = (part[0][my_row] + part[1][my_row]) + (part[2][my_row] + part[3][my_row]);
     half_sync(half);   // all have read it
-    wait(&sm.o_full, seg & 1);
+    if (!dry) wait(&sm.o_full, seg & 1);
     tc_fence_after();
-    if (!waited) pdl_wait();   // no write before the kernel in front has completed
-    waited = true;
-    const bool whole = w.whole();
+    if (!waited && !dry) {   // no write before the kernel in front has completed
+      pdl_wait();
+      waited = true;
+    }
+    const bool live = ok && !dry;
     const float inv = l > 0.f ? 1.f / l : 0.f;
-    if (quad == 0 && my_row < it.rows && ok) {
+    if (quad == 0 && my_row < it.rows && live) {
       if (whole) {
         p.lse[(int64_t)it.row0 + my_row] = (m_ref + log2f(l)) * 0.6931471805599453f;
       } else {
-        float* at = p.part + (((int64_t)blockIdx.x * 2 + (w.tb == 0)) * kRows + my_row) * (D + 4) + D;
+        float* at = p.part + (((int64_t)blockIdx.x * 2 + (ub == 0)) * kRows + my_row) * (D + 4) + D;
         at[0] = m_ref;
         at[1] = l;
       }
@@ -536,11 +592,11 @@ __device__ void softmax(const Params& p, Smem<D>& sm) {
           const int row = 32 * half + i + (lane & 1);
           const __nv_bfloat162 h = lane & 1 ? __floats2bfloat162_rn(other, b)
                                             : __floats2bfloat162_rn(a, other);
-          if (row < it.rows && ok)
+          if (row < it.rows && live)
             *reinterpret_cast<__nv_bfloat162*>(p.O + ((int64_t)it.row0 + row) * D + (col & ~1)) = h;
         }
-      } else if (ok) {
-        float* at = p.part + (((int64_t)blockIdx.x * 2 + (w.tb == 0)) * kRows + 32 * half) * (D + 4) + col;
+      } else if (live) {
+        float* at = p.part + (((int64_t)blockIdx.x * 2 + (ub == 0)) * kRows + 32 * half) * (D + 4) + col;
 #pragma unroll
         for (int i = 0; i < 32; ++i)
           if (32 * half + i < it.rows) at[i * (D + 4)] = __uint_as_float(r[i]);
@@ -548,15 +604,35 @@ __device__ void softmax(const Params& p, Smem<D>& sm) {
     }
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive(&sm.o_free);
+    if (!dry) {
+      if (lane == 0) mbar_arrive(&sm.o_free);
+      ++seg;
+    }
+    dry = false;
   }
 }
 
-// Every CTA sums the batch's tiles up to find its own: each thread over some slots, then over the
-// threads.  CTA 0 leaves the slots' first tiles for the kernel that joins, and reports bad requests.
+// Every CTA finds its own work: each thread looks at some slots, with the starts and lengths in the ring's
+// memory (not in use yet; read from there in one round trip).  CTA 0 leaves the slots' CTAs for the
+// kernel that joins, and reports bad requests.
+constexpr int kCached = 4096;   // requests that are looked at there
+
 template <int D>
-__device__ void find_range(const Params& p, Smem<D>& sm) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = p.c.B;
+__device__ void find_work(const Params& given, Smem<D>& sm) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = given.c.B, G = gridDim.x;
+  Params p = given;
+  if (tid == 0) sm.places = 0;
+  if (B < kCached) {
+    int32_t* const starts = reinterpret_cast<int32_t*>(sm.ring[0]);
+    int32_t* const len = starts + kCached;
+    for (int b = tid; b <= B; b += kThreads) {
+      starts[b] = given.c.starts[b];
+      if (b < B) len[b] = given.c.L[b];
+    }
+    p.c.starts = starts;
+    p.c.L = len;
+    __syncthreads();
+  }
   if (blockIdx.x == 0)
     for (int b = tid; b < B; b += kThreads) {
       const int state = attn_state(p.c, b);
@@ -565,52 +641,52 @@ __device__ void find_range(const Params& p, Smem<D>& sm) {
   const int per = (p.n_slots + kThreads - 1) / kThreads;
   const int lo = min(p.n_slots, tid * per), hi = min(p.n_slots, lo + per);
   const int b0 = lo < hi ? request_at(p, lo) : 0;
-  // visits the thread's items in order: request, item of it, tiles, slot
-  auto each = [&](auto&& visit) {
-    int b = b0;
-    for (int slot = lo; slot < hi; ++slot) {
-      while (b + 1 < B && slot_of(p, b + 1) <= slot) ++b;
-      const int k = b < 0 ? 0 : slot - slot_of(p, b);
-      const bool some = b >= 0 && k < items_of(p, b);
-      visit(b, k, some ? item_of(p, b, k).s.T : 0, slot);
-    }
+  int b, mine = 0;
+  Item it;
+  auto look = [&](int slot) {   // the slot's item; its places, 0: none
+    while (b + 1 < B && slot_of(p, b + 1) <= slot) ++b;
+    const int k = b < 0 ? 0 : slot - slot_of(p, b);
+    it.units = 0;
+    if (b >= 0 && k < items_of(p, b)) it = item_of(p, b, k);
+    return it.units + (it.units > 0 ? kOpen : 0);
   };
-  int mine = 0;
-  each([&](int, int, int T, int) { mine += T; });
-  int before = mine;
+  b = b0;
+#pragma unroll 1
+  for (int slot = lo; slot < hi; ++slot) mine += look(slot);
+  int x = mine;   // places in front of the thread's slots
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(0xffffffffu, before, o);
-    if (lane >= o) before += x;
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
   }
-  if (lane == 31) sm.scan[warp] = before;
+  if (lane == 31) sm.scan[warp] = x;
   __syncthreads();
-  int total = 0, front = 0;
+  int total = 0;
+  x -= mine;
+#pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) front += sm.scan[w];
-    total += sm.scan[w];
+    const int y = sm.scan[w];
+    x += w < warp ? y : 0;
+    total += y;
   }
-  before += front - mine;   // tiles in front of the thread's slots
-  const int G = gridDim.x, q = max((total + G - 1) / G, min(kMinTiles, total));
-  const int start = blockIdx.x * q;
-  if (tid == 0) {
-    sm.range[3] = q;
-    sm.range[4] = total;
-    if (blockIdx.x == 0) p.first_tile[p.n_slots] = q;
-  }
-  const bool holds = start >= before && start < before + mine;
-  if (holds || blockIdx.x == 0) {
-    int x = before;
-    each([&](int b, int k, int T, int slot) {
-      if (start >= x && start < x + T) {
-        sm.range[0] = b;
-        sm.range[1] = k;
-        sm.range[2] = start - x;
+  const int q = max((total + G - 1) / G, min(kMinPlaces, total)), start = blockIdx.x * q;
+  if ((start >= x && start < x + mine) || (blockIdx.x == 0 && lo < hi)) {
+    b = b0;
+#pragma unroll 1
+    for (int slot = lo; slot < hi; ++slot) {
+      const int n = per == 1 ? mine : look(slot);
+      if (start >= x && start < x + n) {
+        sm.first = it;
+        sm.begin = start - x;
+        sm.places = min(q, total - start);
       }
-      if (blockIdx.x == 0) p.first_tile[slot] = x;
-      x += T;
-    });
+      if (blockIdx.x == 0)   // CTAs that hold half tiles of it
+        p.pieces[slot] =
+            n > 0 ? make_int2((x + kOpen) / q, (x + n - 1) / q - (x + kOpen) / q + 1) : make_int2(0, 0);
+      x += n;
+    }
   }
+  fence_proxy_async_smem();   // (the ring's copies come behind these accesses)
   __syncthreads();
 }
 
@@ -651,16 +727,15 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
     tmem_relinquish1();
   }
   // behind the gather, which has waited for everything in front of it, only its rows are waited for
-  // (the first C128 tile, and before any write)
+  // (before the first tile with C128 entries, and before any output)
   if (!p.gathered) pdl_wait();
   pdl_launch_dependents();
-  find_range(p, sm);
+  find_work(p, sm);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   if (warp == 0) {
-    if (lane == 0) producer(p, sm);
-    __syncwarp();
+    producer(p, sm);
   } else if (warp == 1) {
     if (lane == 0) mma(p, sm);
     __syncwarp();
@@ -674,50 +749,51 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
   if (warp == 1) tmem_dealloc1(sm.tmem, 512);
 }
 
-// Joins the parts of items that several CTAs have: grid (slots, rows / 8), a warp per row.
+// Joins the parts of items that several CTAs have: grid (slots, rows / kJoinRows), D / 128 warps per row
+// with four columns per lane, so that the parts of a row are read with many loads in flight.
+constexpr int kJoinRows = 2;
+
 template <int D>
-__global__ void __launch_bounds__(256) few_merge_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kJoinRows * D / 4) few_merge_kernel(const __grid_constant__ Params p) {
   const int lane = threadIdx.x & 31, slot = blockIdx.x, b = request_at(p, slot);
   const int k = b < 0 ? 0 : slot - slot_of(p, b);
   const bool some = b >= 0 && k < items_of(p, b);
   Item it;
   if (some) it = item_of(p, b, k);
   pdl_wait();
+  pdl_launch_dependents();
   if (!some) return;
-  const int q = p.first_tile[p.n_slots], x = p.first_tile[slot];
-  const int c0 = x / q, c1 = (x + it.s.T - 1) / q;   // the CTAs that have the item
-  const int r = 8 * blockIdx.y + (threadIdx.x >> 5);
+  const int2 piece = p.pieces[slot];
+  const int c0 = piece.x, c1 = c0 + piece.y - 1;   // the CTAs that have the item
+  const int r = kJoinRows * blockIdx.y + threadIdx.x / (D / 4), col = 4 * (threadIdx.x % (D / 4));
   if (c0 == c1 || r >= it.rows) return;
   constexpr int kRow = D + 4;
   // CTA c's part: the one that goes on (1) of the first CTA, the one begun before (0) of the others
   auto part = [&](int c) { return p.part + (((int64_t)c * 2 + (c == c0)) * kRows + r) * kRow; };
-  float M = -INFINITY;
-  for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, part(c)[D]);
-  M = warp_max(M);
-  float sum = 0.f;
-  for (int c = c0 + lane; c <= c1; c += 32) sum += exp2f(part(c)[D] - M) * part(c)[D + 1];
-  sum = warp_sum(sum);
-  const float inv = 1.f / sum;
-  float4 acc[D / 128];
-#pragma unroll
-  for (int j = 0; j < D / 128; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-  for (int c = c0; c <= c1; ++c) {
-    const float* pc = part(c);
-    const float f = exp2f(pc[D] - M) * inv;
-#pragma unroll
-    for (int j = 0; j < D / 128; ++j) {
-      const float4 v = *reinterpret_cast<const float4*>(pc + 128 * j + 4 * lane);
-      acc[j].x = fmaf(f, v.x, acc[j].x);
-      acc[j].y = fmaf(f, v.y, acc[j].y);
-      acc[j].z = fmaf(f, v.z, acc[j].z);
-      acc[j].w = fmaf(f, v.w, acc[j].w);
+  // 32 parts at a time: lane i weighs part i; the loads of eight are in flight together
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float M = -INFINITY, sum = 0.f;
+  for (int first = c0; first <= c1; first += 32) {
+    const int n = min(32, c1 - first + 1);
+    const float2 ml = *reinterpret_cast<const float2*>(part(first + min(lane, n - 1)) + D);
+    const float m = lane < n ? ml.x : -INFINITY;
+    const float top = fmaxf(M, warp_max(m)), base = top == -INFINITY ? 0.f : top;
+    const float old = exp2f(M - base), f = lane < n ? exp2f(m - base) : 0.f;
+    M = top;
+    sum = sum * old + warp_sum(f * ml.y);
+    acc = make_float4(acc.x * old, acc.y * old, acc.z * old, acc.w * old);
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) {
+      const float w = __shfl_sync(0xffffffffu, f, i);
+      const float4 v = *reinterpret_cast<const float4*>(part(first + i) + col);
+      acc = make_float4(fmaf(w, v.x, acc.x), fmaf(w, v.y, acc.y), fmaf(w, v.z, acc.z),
+                        fmaf(w, v.w, acc.w));
     }
   }
+  const float inv = 1.f / sum;
   const int64_t row = (int64_t)it.row0 + r;
-#pragma unroll
-  for (int j = 0; j < D / 128; ++j) store_f4(p.O + row * D + 128 * j + 4 * lane, acc[j]);
-  if (lane == 0) p.lse[row] = (M + log2f(sum)) * 0.6931471805599453f;
+  store_f4(p.O + row * D + col, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+  if (col == 0) p.lse[row] = (M + log2f(sum)) * 0.6931471805599453f;
 }
 
 }  // namespace few
@@ -726,7 +802,7 @@ __global__ void __launch_bounds__(256) few_merge_kernel(const __grid_constant__ 
 // ---- host side --------------------------------------------------------------------------------------
 bool tv_few_ok(const tv_shape* s) {
   const int64_t lim = (int64_t)1 << 31;
-  return s->dtype == TV_BF16 && s->d % 128 == 0 && (int64_t)s->B * (s->c128_cap + 16) < lim &&
+  return s->dtype == TV_BF16 && s->d % 128 == 0 && (int64_t)s->B * (s->c128_cap + 63) < lim &&
          (s->page_tokens > 0 ||
           ((int64_t)s->B * s->raw_cap < lim && (int64_t)s->B * s->c4_cap < lim));
 }
@@ -746,7 +822,7 @@ int sm_count() {
 int64_t slots_of(const tv_shape* s, int n_new) {
   return (int64_t)n_new * s->H / tv::few::kRows + s->B;
 }
-size_t table_bytes(const tv_shape* s, int n_new) { return (slots_of(s, n_new) + 1 + 63) / 64 * 256; }
+size_t table_bytes(const tv_shape* s, int n_new) { return (slots_of(s, n_new) + 31) / 32 * 256; }
 
 template <int D>
 cudaError_t launch_few(const tv::few::Params& p, int ctas, int slots, cudaStream_t stream) {
@@ -757,7 +833,8 @@ cudaError_t launch_few(const tv::few::Params& p, int ctas, int slots, cudaStream
   if (e != cudaSuccess) return e;
   e = tv::launch_pdl(few_kernel<D>, dim3(ctas), dim3(kThreads), sizeof(Smem<D>), stream, p);
   if (e != cudaSuccess) return e;
-  return tv::launch_pdl(few_merge_kernel<D>, dim3(slots, kRows / 8), dim3(256), 0, stream, p);
+  return tv::launch_pdl(few_merge_kernel<D>, dim3(slots, kRows / kJoinRows), dim3(kJoinRows * D / 4), 0,
+                        stream, p);
 }
 
 }  // namespace
@@ -783,12 +860,13 @@ int tv_launch_few(const tv_shape* s, int n_new, const int32_t* starts, const voi
   const uint64_t rawrows = rows_or_one(paged ? pool : B * (uint64_t)s->raw_cap);
   // an inactive compressor's maps are pointed at the raw rows (never read: it has no tiles)
   const uint64_t c4rows = !c4 ? rawrows : rows_or_one(paged ? pool / 4 : B * (uint64_t)s->c4_cap);
-  p.c128_stride = gather > 0 ? tv_chunk_c128_stride(s) : s->c128_cap;
+  p.gathered = gather > 0;
+  p.c128_stride = p.gathered ? tv_chunk_c128_stride(s) : s->c128_cap;
   const uint64_t c128rows = !c128 ? rawrows : rows_or_one(B * (uint64_t)p.c128_stride);
   const void* k4 = c4 ? c4K : rawK;
   const void* v4 = c4 ? c4V : rawV;
-  const void* k128 = !c128 ? rawK : gather > 0 ? ws : c128K;
-  const void* v128 = !c128 ? rawV : gather > 0 ? ws + gather : c128V;
+  const void* k128 = !c128 ? rawK : p.gathered ? ws : c128K;
+  const void* v128 = !c128 ? rawV : p.gathered ? ws + gather : c128V;
   const int d = s->d;
   if (!(tv_make_map(&p.mQ, Q, 2, d, (uint64_t)n_new * s->H, 1, kRows) &&
         tv_make_map(&p.mC4K, k4, 2, d, c4rows, 1, 64) && tv_make_map(&p.mC4V, v4, 2, d, c4rows, 1, 64) &&
@@ -801,17 +879,15 @@ int tv_launch_few(const tv_shape* s, int n_new, const int32_t* starts, const voi
   p.H = s->H;
   p.W = s->W;
   p.tail_mode = s->tail_mode;
-  p.paged = paged;
-  p.gathered = gather > 0;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.O = reinterpret_cast<__nv_bfloat16*>(O);
   p.lse = lse;
   p.n_slots = (int)slots_of(s, n_new);
-  p.first_tile = reinterpret_cast<int32_t*>(ws + 2 * gather);
+  p.pieces = reinterpret_cast<int2*>(ws + 2 * gather);
   p.part = reinterpret_cast<float*>(ws + 2 * gather + table_bytes(s, n_new));
   p.status = status;
   tv_attn_test_aid(&p.timeout_ns, &p.withhold_tile);
-  if (gather > 0)
+  if (p.gathered)
     if (int rc = tv_chunk_gather(s, L, c128K, c128V, ws, status, stream)) return rc;
   const int ctas = sm_count(), slots = (int)slots_of(s, n_new);
   const cudaError_t e = d == 512   ? launch_few<512>(p, ctas, slots, stream)
