@@ -346,6 +346,21 @@ def test_attend_long_requests(d, H, before, n):
     s.check_attend()
 
 
+@pytest.mark.parametrize("H,P,W,ms,news", [
+    (64, 1024, 128, (4, 128), [161, 3, 0, 40]), (128, 512, 100, (4, 128), [90, 33]), (24, 0, 0, (4,), [600]),
+    (64, 1536, 300, (128,), [200, 1, 1]), (16, 512, 37, (4, 128), [900]), (40, 0, 1024, (4, 128), [128, 200])])
+def test_attend_many_rows(H, P, W, ms, news):
+    # enough rows for the kernel that shares a tile among 256 of them; the last items are split
+    before = [1900, 130, 7, 511][:len(news)]
+    s = Batch(before, news, H=H, d=512, dtype="bf16", P=P, W=W, ms=ms, q_std=2.0, seed=H + W, pad_front=1,
+              pad_back=2)
+    s.append()
+    s.attend()
+    torch.cuda.synchronize()
+    assert s.status.item() == 0
+    s.check_attend()
+
+
 def test_attend_growing_maxima():
     # logits that grow by hundreds from tile to tile: every tile rescales what is there
     s = Batch([6000, 6000], [1, 1], H=64, d=512, dtype="bf16", P=512, q_std=0.0, seed=13)

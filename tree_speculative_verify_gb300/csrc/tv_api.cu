@@ -746,13 +746,18 @@ extern "C" int tv_chunk_append(const tv_shape* s, int32_t n_new, const int32_t* 
                           Qr, rawK, rawV, c4K, c4V, c128K, c128V, L, status, (cudaStream_t)stream);
 }
 
-// The kernel of a chunk.  Tensor cores, bf16: d = 512 with more than two 64-row items per request on
-// average on the tree attention's clusters, which share a tile of keys and values among 256 rows;
-// otherwise, and for d = 128, 256 and 384, 64 rows per CTA.  CUDA cores: everything else.
+// The kernel of a chunk.  Tensor cores, bf16: d = 512 and more rows than 10240 and than two 64-row items
+// per request on average, on the tree attention's clusters, which share a tile of keys and values
+// among 256 rows; otherwise, and for d = 128, 256 and 384, 64 rows per CTA, which reads a tile for 64 rows
+// but spreads few rows over every SM.  Measured, 64 heads: 16 requests behind 4000 tokens with 8 new tokens
+// each (8192 rows) 76 us with 64 rows per CTA and 101 on clusters, with 16 each 127 and 95; 4 behind
+// 16000 with 16 each 94 and 127, with 32 each (8192 rows) 170 and 123; 64 behind 4000 with 2 each (8192)
+// 88 and 102, with 4 each 150 and 85.  CUDA cores: everything else.
 enum ChunkKernel { kChunkSimt, kChunkFew, kChunkMany };
 static ChunkKernel chunk_kernel(const tv_shape* s, int32_t n_new) {
   if (s->attn_kernel == TV_ATTN_SIMT || !tv_few_ok(s) || !tv_tc_available()) return kChunkSimt;
-  return s->d == 512 && (int64_t)n_new * s->H > 128 * (int64_t)s->B ? kChunkMany : kChunkFew;
+  const int64_t rows = (int64_t)n_new * s->H;
+  return s->d == 512 && rows > 10240 && rows > 128 * (int64_t)s->B ? kChunkMany : kChunkFew;
 }
 
 extern "C" size_t tv_chunk_workspace_size(const tv_shape* s, int32_t n_new) {
@@ -765,7 +770,7 @@ extern "C" size_t tv_chunk_workspace_size(const tv_shape* s, int32_t n_new) {
   // enough for any call of fewer tokens too, whichever kernel takes it
   if (chunk_kernel(s, n_new) == kChunkSimt) return align256(tv_chunk_simt_workspace(s, n_new));
   const size_t few = tv_few_workspace(s, n_new);
-  const size_t many = s->d == 512 ? tv_chunk_tc_workspace(s, n_new) : 0;
+  const size_t many = s->d == 512 ? tv_chunk_tc_workspace(s) : 0;
   return align256(few > many ? few : many);
 }
 
