@@ -136,8 +136,9 @@ struct Params {
   // chunks of new tokens (kChunk): rows of the Q and O maps are all n_new * H rows
   const int32_t* starts;   // [B+1] request b's tokens are rows starts[b] .. starts[b+1] - 1
   int n_new;
-  int n_slots;             // slots of 256-row tiles: at least as many as there are tiles
-  int n_whole;             // slots in front whose items are not split; those behind are, n_chunks times
+  int n_clusters;          // of the grid
+  int32_t* first_item;     // [B+1] items in front of every request (by the grid's first CTA, for the
+                           // kernel that joins; up to kRankMax - 1 requests)
   int64_t raw_lim, c4_lim, c128_lim;   // capacities (c4_cap and c128_cap are strides in rows)
   uint64_t timeout_ns;   // bound of every wait (kTimeoutNs unless a test shortens it)
   int withhold_tile;     // test aid: the producers never issue this tile's K copies (-1: none)
@@ -294,6 +295,12 @@ __global__ void gather_paged_kernel(Paging pg, int comp_mask, int W, int tail_mo
   }
 }
 
+// Chunks of new tokens: the items that are taken whole, a round of one per cluster after the other, and
+// those of the last round, which are split into `chunks` KV chunks each (see split_of).
+struct Split {
+  int items, whole, chunks;
+};
+
 // Shared memory.  The operand buffers differ between the two pairs; the barriers and small arrays
 // sit at the same offsets in every CTA, so a commit or an asynchronous store of one pair can
 // target the other pair's barriers by offset.
@@ -335,6 +342,9 @@ struct Header {
     };
     int32_t starts[kRankMax];     // chunks of new tokens: the starts (up to kRankMax - 1 requests)
   };
+  int32_t first[kRankMax];        // chunks: items in front of every request
+  int scan[kThreads / 32];
+  struct Split split;
 };
 // A P buffer holds 128 rows x 128 entries of bf16 P as two 64-entry panels (K-major, 128-byte
 // swizzle), followed by the 128 rows' fp32 rescale factors.
@@ -457,22 +467,51 @@ struct Item {
 };
 
 // Chunks of new tokens.  Request b's n tokens make n * H rows (token-major) and ceil(n * H / 256)
-// pairs of row tiles; their slots start at floor(starts[b] * H / 256) + b, which leaves every
-// request room for its pairs whatever the others have, so that an item is found by a search of the
-// starts, without a list.  Tokens see different entries: the pair's tiles reach to what its last
-// token sees and the softmax masks the rest.
+// pairs of row tiles, the items; the kernel counts them in its prologue (first_item), so that item i is
+// found by a search.  Batches of kRankMax requests or more take slots instead: request b's start at
+// floor(starts[b] * H / 256) + b, which leaves every request room for its items.  Tokens see different
+// entries: the item's tiles reach to what its last token sees and the softmax masks the rest.
+__device__ __forceinline__ int chunk_items(const Params& p, int s0, int s1, int L) {
+  if (s0 < 0 || s1 <= s0 || s1 > p.n_new || L < s1 - s0 || L > p.raw_lim ||
+      ((p.comp_mask & TV_COMP_C4) && L / 4 > p.c4_lim) ||
+      ((p.comp_mask & TV_COMP_C128) && L / 128 > p.c128_lim))
+    return 0;
+  return (int)(((int64_t)(s1 - s0) * p.H + 255) / 256);
+}
+
+// Items of the last round, if they leave half of the clusters or more idle, are split into as many KV
+// chunks as give every cluster one (at most p.n_chunks, the most that a full cache is worth): 1024 tokens
+// behind 65536, 256 items on 36 clusters, 2093 -> 1913 us.
+__device__ __forceinline__ Split split_of(const Params& p, int items) {
+  const int rest = items % p.n_clusters;
+  Split s;
+  s.items = items;
+  s.chunks = rest > 0 ? max(1, min(p.n_chunks, p.n_clusters / rest)) : 1;
+  s.whole = s.chunks > 1 ? items - rest : items;
+  return s;
+}
+
+__device__ __forceinline__ int slots_of(const Params& p) {
+  return (int)((int64_t)p.n_new * p.H / 256) + p.B;
+}
+
+// first: items in front of the requests, null: slots.
 template <bool kPaged>
-__device__ __forceinline__ void chunk_item(const Params& p, const int32_t* starts, const int32_t* len,
-                                           int slot, int chunk, int sub, Item& it) {
+__device__ __forceinline__ void chunk_item(const Params& p, const Split& split, const int32_t* first_of,
+                                           const int32_t* starts, const int32_t* len, int item,
+                                           int chunk, int sub, Item& it) {
   it.tb = it.te = it.rows = 0;
   it.y.T = 0;
   it.chunk = chunk;
-  it.part = ((slot - p.n_whole) * 256 + 128 * sub) * p.n_chunks + chunk;
+  it.part = ((item - split.whole) * 256 + 128 * sub) * split.chunks + chunk;
   it.nc = 1;
-  int lo = 0, hi = p.B;   // requests whose slots start at or below this one
+  auto front = [&](int b) {
+    return first_of ? first_of[b] : (int)((int64_t)starts[b] * p.H / 256) + b;
+  };
+  int lo = 0, hi = p.B;   // requests that begin at or before this one (those without items too)
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
-    if ((int64_t)starts[mid] * p.H / 256 + mid <= slot)
+    if (front(mid) <= item)
       lo = mid + 1;
     else
       hi = mid;
@@ -480,11 +519,8 @@ __device__ __forceinline__ void chunk_item(const Params& p, const int32_t* start
   const int b = lo - 1;
   if (b < 0) return;
   const int s0 = starts[b], n = starts[b + 1] - s0, L = len[b];
-  const int64_t first = ((int64_t)slot - ((int64_t)s0 * p.H / 256 + b)) * 256, rows = (int64_t)n * p.H;
-  if (s0 < 0 || n <= 0 || s0 + (int64_t)n > p.n_new || first >= rows || L < n || L > p.raw_lim ||
-      ((p.comp_mask & TV_COMP_C4) && L / 4 > p.c4_lim) ||
-      ((p.comp_mask & TV_COMP_C128) && L / 128 > p.c128_lim))
-    return;
+  const int64_t first = (int64_t)(item - front(b)) * 256, rows = (int64_t)n * p.H;
+  if (chunk_items(p, s0, s0 + n, L) == 0 || first >= rows) return;
   it.b = b;
   it.rt = (int)(first / 128) + sub;
   it.row0 = (int)((int64_t)s0 * p.H + first + 128 * sub);
@@ -503,7 +539,7 @@ __device__ __forceinline__ void chunk_item(const Params& p, const int32_t* start
   y.T128 = (y.n128 + 127) / 128;
   y.Traw = (y.nraw + 127) / 128;
   y.T = y.T4 + y.T128 + y.Traw;
-  it.nc = slot < p.n_whole ? 1 : min(p.n_chunks, (y.T + kChunkTiles - 1) / kChunkTiles);
+  it.nc = item < split.whole ? 1 : min(split.chunks, (y.T + kChunkTiles - 1) / kChunkTiles);
   if (chunk >= it.nc) return;
   it.tb = (int)((int64_t)y.T * chunk / it.nc);
   it.te = (int)((int64_t)y.T * (chunk + 1) / it.nc);
@@ -515,16 +551,17 @@ __device__ __forceinline__ bool item_at(const Params& p, const Smem& sm, int k, 
   const int G = (int)(gridDim.x / kClusterCtas), c = (int)(blockIdx.x / kClusterCtas);
   const int pos = (k & 1) ? k * G + (G - 1 - c) : k * G + c;
   if (kChunk) {
-    int slot = pos, chunk = 0;
-    if (pos >= p.n_whole) {   // (all first chunks of the slots behind, then all second ones, ...)
-      const int rest = p.n_slots - p.n_whole;
-      if (pos >= p.n_whole + rest * p.n_chunks) return false;
-      chunk = (pos - p.n_whole) / rest;
-      slot = p.n_whole + (pos - p.n_whole) % rest;
+    const Split& split = sm.h.split;
+    int item = pos, chunk = 0;
+    if (pos >= split.whole) {   // (all first chunks of the items behind, then all second ones, ...)
+      const int rest = split.items - split.whole;
+      if (pos >= split.whole + rest * split.chunks) return false;
+      chunk = (pos - split.whole) / rest;
+      item = split.whole + (pos - split.whole) % rest;
     }
     const bool cached = p.B < kRankMax;   // (see the kernel's prologue)
-    chunk_item<kPaged>(p, cached ? sm.h.starts : p.starts, cached ? sm.h.len : p.L, slot, chunk,
-                       (int)sub, it);
+    chunk_item<kPaged>(p, split, cached ? sm.h.first : nullptr, cached ? sm.h.starts : p.starts,
+                       cached ? sm.h.len : p.L, item, chunk, (int)sub, it);
     return true;
   }
   it.nc = p.n_chunks;
@@ -1378,7 +1415,7 @@ __device__ void rescale_epilogue_o(const Params& p, Smem& sm, uint32_t rank) {
       ++staged;
       continue;
     } else {
-      float* prow = p.part + (kChunk ? it.part + (int64_t)row * p.n_chunks
+      float* prow = p.part + (kChunk ? it.part + (int64_t)row * sm.h.split.chunks
                                      : part_row(p, b, grow, it.chunk)) * (d + 4);
       for (int c = 0; c < 256 / 32; ++c) {
         uint32_t r[32];
@@ -1480,20 +1517,53 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     // CTA reports what makes a request invalid
     pdl_wait();
     pdl_launch_dependents();   // (the merge reads them ahead of its wait)
-    for (int b = threadIdx.x; b < p.B && (p.B < kRankMax || blockIdx.x == 0); b += blockDim.x) {
+    const bool cached = p.B < kRankMax;
+    const int per = cached ? (p.B + kThreads - 1) / kThreads : 0;   // consecutive requests per thread
+    int mine = 0;
+    for (int i = 0; i < per; ++i) {
+      const int b = (int)threadIdx.x * per + i;
+      if (b >= p.B) break;
       const int s0 = p.starts[b], s1 = p.starts[b + 1], L = p.L[b];
-      if (p.B < kRankMax) {
-        sm.h.starts[b] = s0;
-        sm.h.len[b] = L;
-        if (b == p.B - 1) sm.h.starts[p.B] = s1;
+      sm.h.starts[b] = s0;
+      sm.h.len[b] = L;
+      sm.h.first[b] = mine;
+      mine += chunk_items(p, s0, s1, L);
+      if (b == p.B - 1) sm.h.starts[p.B] = s1;
+    }
+    if (cached) {
+      int sum = mine, all = 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += x;
       }
-      if (blockIdx.x == 0) {
-        if (s0 < 0 || s1 < s0 || s1 > p.n_new || (s1 > s0 && L < s1 - s0))
-          record_error(p.status, TV_ERR_ARG);
-        else if (s1 > s0 && (L > p.raw_lim || ((p.comp_mask & TV_COMP_C4) && L / 4 > p.c4_lim) ||
-                             ((p.comp_mask & TV_COMP_C128) && L / 128 > p.c128_lim)))
-          record_error(p.status, TV_ERR_CAPACITY);
+      if (lane == 31) sm.h.scan[warp] = sum;
+      __syncthreads();
+      sum -= mine;
+      for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) sum += sm.h.scan[w];
+        all += sm.h.scan[w];
       }
+      for (int i = 0; i < per; ++i) {
+        const int b = (int)threadIdx.x * per + i;
+        if (b >= p.B) break;
+        sm.h.first[b] += sum;
+        if (blockIdx.x == 0) p.first_item[b] = sm.h.first[b];
+      }
+      if (threadIdx.x == 0) {
+        sm.h.first[p.B] = all;
+        sm.h.split = split_of(p, all);
+        if (blockIdx.x == 0) p.first_item[p.B] = all;
+      }
+    } else if (threadIdx.x == 0) {
+      sm.h.split = split_of(p, slots_of(p));
+    }
+    for (int b = threadIdx.x; b < p.B && blockIdx.x == 0; b += blockDim.x) {
+      const int s0 = p.starts[b], s1 = p.starts[b + 1], L = p.L[b];
+      if (s0 < 0 || s1 < s0 || s1 > p.n_new || (s1 > s0 && L < s1 - s0))
+        record_error(p.status, TV_ERR_ARG);
+      else if (s1 > s0 && chunk_items(p, s0, s1, L) == 0)
+        record_error(p.status, TV_ERR_CAPACITY);
     }
     __syncthreads();
   }
@@ -1588,20 +1658,23 @@ __global__ void gather_c128_kernel(Paging pg, int row_u4, int64_t c128_cap, int6
   }
 }
 
-// Joins the KV chunks of one slot's rows: grid (split slots, 8), a warp per row, 4 rows per warp.
+// Joins the KV chunks of a split item's rows: grid (half of the clusters, 8), a warp per row, 4 rows per
+// warp.
 template <bool kPaged>
 __global__ void __launch_bounds__(256) chunk_merge_kernel(const __grid_constant__ Params p) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  Item it;
-  // (the attention has waited for what this reads)
-  chunk_item<kPaged>(p, p.starts, p.L, p.n_whole + blockIdx.x, 0, 0, it);
-  const int nc = it.nc, rows = min(it.rows, 256);
   pdl_wait();
+  const Split split = split_of(p, p.B < kRankMax ? p.first_item[p.B] : slots_of(p));
+  const int item = split.whole + blockIdx.x;
+  if (item >= split.items) return;
+  Item it;
+  chunk_item<kPaged>(p, split, p.B < kRankMax ? p.first_item : nullptr, p.starts, p.L, item, 0, 0, it);
+  const int nc = it.nc, rows = min(it.rows, 256);
   if (nc == 1) return;
   constexpr int64_t kRow = 512 + 4;
   for (int r = 32 * blockIdx.y + warp; r < min(rows, 32 * (int)blockIdx.y + 32); r += 8) {
     const int64_t row = (int64_t)it.row0 + r;
-    const float* pr = p.part + (it.part + (int64_t)r * p.n_chunks) * kRow;
+    const float* pr = p.part + (it.part + (int64_t)r * split.chunks) * kRow;
     float m = -INFINITY, l = 0.f;   // lane c: chunk c (and c + 32)
     for (int c = lane; c < nc; c += 32) {
       const float mc = pr[c * kRow + 512], lc = pr[c * kRow + 513];
@@ -1999,27 +2072,16 @@ bool tv_chunk_tc_ok(const tv_shape* s) {
 
 constexpr int kMostClusters = 64;   // (a device with more clusters splits no further)
 
-static int64_t chunk_slots(const tv_shape* s, int n_new) {
-  return (int64_t)n_new * s->H / 256 + s->B;
-}
-
-// Items (at most the slots, as the host does not know the requests' sizes) are taken whole, a round of one
-// per cluster after the other; those of the last round, if they leave half of the clusters or more idle,
-// are split into as many KV chunks as give every cluster one, up to one per kChunkTiles tiles of a full
-// cache (1024 tokens behind 65536, 256 items on 36 clusters: 2090 -> 1890 us).  Returns the chunks.
-static int chunk_kv_chunks(const tv_shape* s, int n_new, int* n_whole) {
-  int slots = cluster_slots();
-  if (slots <= 0) slots = 36;
-  if (slots > kMostClusters) slots = kMostClusters;
-  const int64_t items = chunk_slots(s, n_new), rest = items % slots;
+// Most KV chunks of an item: one per kChunkTiles tiles of a full cache.
+static int chunk_kv_chunks(const tv_shape* s) {
   int64_t tiles = 2 + (s->tail_mode == TV_TAIL_WINDOW ? (s->W + 127) / 128 : 1);
   if (s->comp_mask & TV_COMP_C4) tiles += (s->c4_cap + 127) / 128;
   if (s->comp_mask & TV_COMP_C128) tiles += (s->c128_cap + 127) / 128;
-  const int64_t n = rest > 0 ? slots / rest : 1, most = tiles / tv::tc::kChunkTiles;
-  const int chunks = (int)(n < most ? n : most < 1 ? 1 : most);
-  *n_whole = (int)(chunks > 1 ? items - rest : items);
-  return chunks;
+  const int64_t most = tiles / tv::tc::kChunkTiles;
+  return (int)(most < 1 ? 1 : most > kMostClusters ? kMostClusters : most);
 }
+
+static size_t chunk_table_bytes(const tv_shape* s) { return ((size_t)s->B + 1 + 63) / 64 * 256; }
 
 int64_t tv_chunk_c128_stride(const tv_shape* s) { return (s->c128_cap + 63) / 64 * 64; }
 size_t tv_chunk_gather_bytes(const tv_shape* s) {
@@ -2042,7 +2104,8 @@ int tv_chunk_gather(const tv_shape* s, const int32_t* L, const void* c128K, cons
 
 // Split items times KV chunks never exceed the clusters.
 size_t tv_chunk_tc_workspace(const tv_shape* s) {
-  return 2 * tv_chunk_gather_bytes(s) + (size_t)256 * kMostClusters * (512 + 4) * sizeof(float);
+  return 2 * tv_chunk_gather_bytes(s) + chunk_table_bytes(s) +
+         (size_t)256 * kMostClusters * (512 + 4) * sizeof(float);
 }
 
 int tv_launch_chunk_tc(const tv_shape* s, int n_new, const int32_t* starts, const void* Q,
@@ -2085,7 +2148,7 @@ int tv_launch_chunk_tc(const tv_shape* s, int n_new, const int32_t* starts, cons
   p.tail_mode = s->tail_mode;
   p.comp_mask = s->comp_mask;
   p.n_pairs = 0;
-  p.n_chunks = chunk_kv_chunks(s, n_new, &p.n_whole);
+  p.n_chunks = chunk_kv_chunks(s);
   p.n_sel = 0;
   p.tree_rows = 0;
   p.raw_cap = p.raw_lim = s->raw_cap;
@@ -2098,22 +2161,21 @@ int tv_launch_chunk_tc(const tv_shape* s, int n_new, const int32_t* starts, cons
   p.scale_log2 = scale * 1.4426950408889634f;
   p.O = reinterpret_cast<__nv_bfloat16*>(O);
   p.lse = lse;
-  p.part = reinterpret_cast<float*>(ws + 2 * gather);
+  p.first_item = reinterpret_cast<int32_t*>(ws + 2 * gather);
+  p.part = reinterpret_cast<float*>(ws + 2 * gather + chunk_table_bytes(s));
   p.order = nullptr;
   p.status = status;
   p.pg = tv::paging_of(s);
   p.tail_rows = 0;
   p.starts = starts;
   p.n_new = n_new;
-  p.n_slots = (int)chunk_slots(s, n_new);
   p.timeout_ns = (uint64_t)g_timeout_ns.load();
   p.withhold_tile = g_withhold_tile.load();
   if (cluster_slots() <= 0) return tv_check_launch(fn);
   if (gather > 0)
     if (int rc = tv_chunk_gather(s, L, c128K, c128V, ws, status, stream)) return rc;
-  const int64_t items = p.n_whole + (int64_t)(p.n_slots - p.n_whole) * p.n_chunks;
-  int64_t clusters = items < cluster_slots() ? items : cluster_slots();
-  if (clusters > kMostClusters) clusters = kMostClusters;
+  const int clusters = cluster_slots() < kMostClusters ? cluster_slots() : kMostClusters;
+  p.n_clusters = clusters;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(clusters * kClusterCtas));
   cfg.blockDim = dim3(kThreads);
@@ -2131,8 +2193,8 @@ int tv_launch_chunk_tc(const tv_shape* s, int n_new, const int32_t* starts, cons
   if ((paged ? cudaLaunchKernelEx(&cfg, attn_kernel<true, false, true>, p)
              : cudaLaunchKernelEx(&cfg, attn_kernel<false, false, true>, p)) != cudaSuccess)
     return tv_check_launch(fn);
-  if (p.n_chunks > 1) {
-    const dim3 grid((unsigned)(p.n_slots - p.n_whole), 8);
+  if (p.n_chunks > 1 && clusters > 1) {
+    const dim3 grid((unsigned)clusters / 2, 8);
     if ((paged ? tv::launch_pdl(chunk_merge_kernel<true>, grid, dim3(256), 0, stream, p)
                : tv::launch_pdl(chunk_merge_kernel<false>, grid, dim3(256), 0, stream, p)) != cudaSuccess)
       return tv_check_launch(fn);
