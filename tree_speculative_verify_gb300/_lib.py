@@ -413,26 +413,30 @@ def tv_chunk_append(shape, starts, K, V, Q, rope_dim, rope_pairs, inv_freq, g4, 
     """``K``, ``V``: [n_new][d] with unit last stride, both with the same row stride (slices of a wider
     projection's output, say); ``Q``, ``Qr``: [n_new][H][d] or None; ``inv_freq``: [rope_dim / 2]
     fp32 or None."""
-    lib, dev, d = _lib or load(), _here(), shape.d
+    lib, dev, B, d = _lib or load(), _here(), shape.B, shape.d
     dt = torch.bfloat16 if shape.dtype == TV_BF16 else torch.float32
-    f32, i32 = torch.float32, torch.int32
-    for t, name in ((K, "K"), (V, "V")):
-        if t.get_device() != dev:
-            raise ValueError(f"{name}: the tensor must live on the current CUDA device")
-        if t.dtype != dt:
-            raise TypeError(f"{name}: expected {dt}, got {t.dtype}")
-        if t.dim() != 2 or t.shape[1] != d or t.shape[0] != K.shape[0]:
-            raise ValueError(f"{name}: expected [n_new][{d}], got {tuple(t.shape)}")
-        if t.stride(1) != 1 or (t.shape[0] > 1 and t.stride(0) != K.stride(0)):
-            raise ValueError(f"{name}: rows must be contiguous and as far apart as K's")
-    n = K.shape[0]
-    ld = K.stride(0) if n > 1 else d
+    f32, i32, size = torch.float32, torch.int32, K.shape
+    if len(size) != 2 or size[1] != d or V.shape != size:
+        raise ValueError(f"K, V: expected [n_new][{d}], got {tuple(size)} and {tuple(V.shape)}")
+    n, ld = size[0], d
+    if K.is_contiguous() and V.is_contiguous():
+        k, v = _a(K, dt, 0, "K", dev), _a(V, dt, 0, "V", dev)
+    else:
+        ld = K.stride(0) if n > 1 else d
+        for t, name in ((K, "K"), (V, "V")):
+            if t.get_device() != dev:
+                raise ValueError(f"{name}: the tensor must live on the current CUDA device")
+            if t.dtype != dt:
+                raise TypeError(f"{name}: expected {dt}, got {t.dtype}")
+            if t.stride(1) != 1 or (n > 1 and t.stride(0) != ld):
+                raise ValueError(f"{name}: rows must be contiguous and as far apart as K's")
+        k, v = K.data_ptr(), V.data_ptr()
+    rows = n * shape.H * d
     rc = lib.tv_chunk_append(
-        ctypes.byref(shape), n, _a(starts, i32, shape.B + 1, "starts", dev), K.data_ptr(),
-        V.data_ptr(), ld, _a(Q, dt, n * shape.H * d, "Q", dev), rope_dim, rope_pairs,
-        _a(inv_freq, f32, rope_dim // 2, "inv_freq", dev), _a(g4, f32, d, "g4", dev),
-        _a(g128, f32, d, "g128", dev), _a(Qr, dt, n * shape.H * d, "Qr", dev),
-        *_layers(shape, rawK, rawV, c4K, c4V, c128K, c128V, dev), _a(L, i32, shape.B, "L", dev),
+        ctypes.byref(shape), n, _a(starts, i32, B + 1, "starts", dev), k, v, ld,
+        _a(Q, dt, rows, "Q", dev), rope_dim, rope_pairs, _a(inv_freq, f32, rope_dim // 2, "inv_freq", dev),
+        _a(g4, f32, d, "g4", dev), _a(g128, f32, d, "g128", dev), _a(Qr, dt, rows, "Qr", dev),
+        *_layers(shape, rawK, rawV, c4K, c4V, c128K, c128V, dev), _a(L, i32, B, "L", dev),
         _a(status, i32, 1, "status", dev), _s(stream, dev))
     if rc:
         _check("tv_chunk_append", rc)

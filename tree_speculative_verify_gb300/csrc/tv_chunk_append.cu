@@ -92,10 +92,10 @@ __device__ __forceinline__ uint4 pack16<__nv_bfloat16>(const float* f) {
 // vectors: a vector of the first halves of the rotated elements with its partner, or two vectors that
 // need no partner (interleaved pairs lie in one vector); all of a thread's loads are in flight before
 // its stores.  Qr may be Q (each item is read before it is written); then only rotated vectors move.
-template <typename T>
+template <typename T, int U>
 __device__ void turn_rows(const AppendArgs& a, const T* Q, T* Qr, int row0, int row1, int t0,
                           const int* pos, float2* table) {
-  constexpr int VW = VecWidth<T>::n, U = 4;
+  constexpr int VW = VecWidth<T>::n;
   const int half = a.rope / 2, first = a.d - a.rope, tid = threadIdx.x;
   const int tokens = (row1 - 1) / a.H - t0 + 1;
   const bool move = Q != Qr;
@@ -184,6 +184,87 @@ __device__ void turn_rows(const AppendArgs& a, const T* Q, T* Qr, int row0, int 
   }
 }
 
+// The same where the rows go elsewhere and a rotated vector's partner lies in the same warp: interleaved
+// pairs (the vector itself), or halves of a power of two of vectors at a multiple of their length.  Eight
+// neighbouring vectors apart per thread, copied or rotated as they come; less code and half the registers.
+template <typename T>
+__host__ __device__ __forceinline__ bool streams(const AppendArgs& a) {
+  constexpr int VW = VecWidth<T>::n;
+  if (a.rope == 0 || a.pairs == TV_ROPE_PAIRS) return true;
+  const int half = a.rope / 2 / VW;   // vectors
+  return a.rope % (2 * VW) == 0 && half <= 16 && (half & (half - 1)) == 0 && (a.d / VW) % (2 * half) == 0;
+}
+
+template <typename T>
+__device__ void stream_rows(const AppendArgs& a, const T* Q, T* Qr, int row0, int row1, int t0,
+                            const int* pos, float2* table) {
+  constexpr int VW = VecWidth<T>::n, U = 8;
+  const int per_row = a.d / VW, half = a.rope / 2, first = a.d - a.rope, tid = threadIdx.x;
+  const int n = (row1 - row0) * per_row, tokens = (row1 - 1) / a.H - t0 + 1;
+  const int apart = a.pairs == TV_ROPE_PAIRS ? 0 : half / VW;   // lanes to the partner
+  const T* const from = Q + (int64_t)row0 * a.d;
+  T* const to = Qr + (int64_t)row0 * a.d;
+#pragma unroll 1
+  for (int base = 0; base < n; base += U * blockDim.x) {
+    uint4 x[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = base + u * (int)blockDim.x + tid;
+      if (i < n) x[u] = __ldcs(reinterpret_cast<const uint4*>(from + (int64_t)i * VW));
+    }
+    if (base == 0) {   // the angles, while the rows are on their way
+      for (int k = tid; k < tokens * half; k += blockDim.x) {
+        const int p = pos[k / half];
+        if (p >= 0) table[k] = turn_of(p, a.inv_freq[k % half]);
+      }
+      __syncthreads();
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = base + u * (int)blockDim.x + tid;
+      const int r = i / per_row, e = (i - r * per_row) * VW;
+      const int t = i < n ? (row0 + r) / a.H - t0 : 0;
+      const bool live = i < n && pos[t] >= 0;
+      if (__any_sync(0xffffffffu, live && e + VW > first)) {
+        const float2* cs = table + t * half;
+        float f[VW];
+        if (apart == 0) {
+          if (live && e + VW > first) {
+            cvt16(x[u], (T*)nullptr, f);
+#pragma unroll
+            for (int k = 0; k < VW; k += 2)
+              if (e + k >= first) rotate(cs[(e + k - first) / 2], f[k], f[k + 1]);
+            x[u] = pack16<T>(f);
+          }
+        } else {
+          uint4 y;
+          y.x = __shfl_xor_sync(0xffffffffu, x[u].x, apart);
+          y.y = __shfl_xor_sync(0xffffffffu, x[u].y, apart);
+          y.z = __shfl_xor_sync(0xffffffffu, x[u].z, apart);
+          y.w = __shfl_xor_sync(0xffffffffu, x[u].w, apart);
+          if (live && e >= first) {
+            float g[VW];
+            cvt16(x[u], (T*)nullptr, f);
+            cvt16(y, (T*)nullptr, g);
+            const bool second = e - first >= half;
+            const float2* c = cs + (e - first) - (second ? half : 0);
+#pragma unroll
+            for (int k = 0; k < VW; ++k) {
+              if (second) {
+                rotate(c[k], g[k], f[k]);
+              } else {
+                rotate(c[k], f[k], g[k]);
+              }
+            }
+            x[u] = pack16<T>(f);
+          }
+        }
+      }
+      if (live) *reinterpret_cast<uint4*>(to + (int64_t)i * VW) = x[u];
+    }
+  }
+}
+
 // Rows per CTA: a thread moves 128 bytes at a time whether whole rows or their rotated part.
 constexpr int kTurnRows = 32, kTurnTokens = kTurnRows + 1;
 
@@ -197,7 +278,7 @@ __device__ __forceinline__ const int32_t* cached_starts(const Chunk& c, int32_t*
   return copy;
 }
 
-template <typename T>
+template <typename T, bool kStream>
 __global__ void __launch_bounds__(256) append_queries_kernel(AppendArgs a, const T* Q, T* Qr) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   __shared__ int32_t starts_copy[kCachedStarts + 1];
@@ -215,7 +296,11 @@ __global__ void __launch_bounds__(256) append_queries_kernel(AppendArgs a, const
                            : (int)max(0, a.c.L[b]) + t - starts[b];
   }
   __syncthreads();
-  turn_rows(a, Q, Qr, row0, row1, t0, pos, reinterpret_cast<float2*>(smem_raw));
+  float2* table = reinterpret_cast<float2*>(smem_raw);
+  if constexpr (kStream)
+    stream_rows(a, Q, Qr, row0, row1, t0, pos, table);
+  else
+    turn_rows<T, 4>(a, Q, Qr, row0, row1, t0, pos, table);
   pdl_wait();
   pdl_launch_dependents();
 }
@@ -369,9 +454,10 @@ __global__ void __cluster_dims__(kC128Ranks, 1, 1) __launch_bounds__(kThreads)
   if (joined == 0) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// Few tokens: a cluster per request does all of it, its queries and its length included.
+// Few tokens: a cluster per request does all of it, its queries and its length included.  (Four CTAs per
+// SM: 64 requests' 512 CTAs are resident at once.)
 template <typename T>
-__global__ void __cluster_dims__(kC128Ranks, 1, 1) __launch_bounds__(kThreads)
+__global__ void __cluster_dims__(kC128Ranks, 1, 1) __launch_bounds__(kThreads, 4)
     append_requests_kernel(AppendArgs a, Layers<T> y, const T* K, const T* V, const T* Q, T* Qr) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   AppendSmem<T>& sm = *reinterpret_cast<AppendSmem<T>*>(smem_raw);
@@ -388,19 +474,21 @@ __global__ void __cluster_dims__(kC128Ranks, 1, 1) __launch_bounds__(kThreads)
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   const int n = s1 - s0, L1 = L0 + n;
   if (code == TV_OK && n > 0) {
+    // the rank of the first new position begins with keys and values, the others with the queries
+    const int kv = L0 % 128 / kC128Tokens;
     load_gates(a, y, sm);
     for (int blk = L0 / 128; blk <= (L1 - 1) / 128; ++blk)
       append_block(a, y, K, V, b, blk, s0, L0, L1, rank, joined, sm);
-    if (Q != nullptr) {
+    if (Q != nullptr && rank != kv) {
       float2* table = reinterpret_cast<float2*>(smem_raw);   // (over the rows)
       // (rows of this path: few, n_new <= 2B)
-      const int end = s1 * a.H;
-      for (int r0 = s0 * a.H + rank * kTurnRows; r0 < end; r0 += kC128Ranks * kTurnRows) {
-        const int r1 = min(end, r0 + kTurnRows), t0 = r0 / a.H;
+      const int end = s1 * a.H, step = kTurnRows / 2;
+      for (int r0 = s0 * a.H + ((rank - kv - 1) & 7) * step; r0 < end; r0 += (kC128Ranks - 1) * step) {
+        const int r1 = min(end, r0 + step), t0 = r0 / a.H;
         __syncthreads();
         if (threadIdx.x < kTurnTokens) pos[threadIdx.x] = L0 + t0 + (int)threadIdx.x - s0;
         __syncthreads();
-        turn_rows(a, Q, Qr, r0, r1, t0, pos, table);
+        turn_rows<T, 2>(a, Q, Qr, r0, r1, t0, pos, table);
       }
     }
   }
@@ -443,12 +531,10 @@ static int launch_append(const AppendArgs& a, const Layers<T>& y, const void* K,
   const size_t kv = sizeof(AppendSmem<T>) > table ? sizeof(AppendSmem<T>) : table;
   constexpr int kMost = 128 * 1024;   // the most that any call takes: 32 tokens' tables are 64 KB
   static_assert(sizeof(AppendSmem<T>) <= kMost, "shared memory of the appending CTAs");
-  if (cudaFuncSetAttribute(append_blocks_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           kMost) != cudaSuccess ||
-      cudaFuncSetAttribute(append_requests_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           kMost) != cudaSuccess ||
-      cudaFuncSetAttribute(append_queries_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           kMost) != cudaSuccess)
+  if (allow_smem<append_blocks_kernel<T>>(kMost) != cudaSuccess ||
+      allow_smem<append_requests_kernel<T>>(kMost) != cudaSuccess ||
+      allow_smem<append_queries_kernel<T, true>>(kMost) != cudaSuccess ||
+      allow_smem<append_queries_kernel<T, false>>(kMost) != cudaSuccess)
     return tv_check_launch(fn);
   cudaError_t e = cudaSuccess;
   if (n <= 2 * (int64_t)B) {
@@ -460,8 +546,10 @@ static int launch_append(const AppendArgs& a, const Layers<T>& y, const void* K,
                    sizeof(AppendSmem<T>), stream, a, y, (const T*)K, (const T*)V);
     const int64_t rows = (int64_t)n * a.H;
     if (e == cudaSuccess && Q != nullptr)
-      e = launch_pdl(append_queries_kernel<T>, dim3((unsigned)((rows + kTurnRows - 1) / kTurnRows)),
-                     dim3(256), table, stream, a, (const T*)Q, (T*)Qr);
+      e = launch_pdl(Q != Qr && streams<T>(a) ? append_queries_kernel<T, true>
+                                              : append_queries_kernel<T, false>,
+                     dim3((unsigned)((rows + kTurnRows - 1) / kTurnRows)), dim3(256), table, stream, a,
+                     (const T*)Q, (T*)Qr);
     if (e == cudaSuccess)
       e = launch_pdl(append_lengths_kernel, dim3((B + 7) / 8), dim3(256), 0, stream, a);
   }

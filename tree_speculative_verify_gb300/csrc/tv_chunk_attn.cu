@@ -275,35 +275,44 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// Joins the shares of one slot's rows: a warp per row.
+// Joins the shares of a slot's rows: grid (slots, R / 8), a warp per row.
 template <typename T>
 __global__ void __launch_bounds__(256) chunk_simt_merge_kernel(ChunkAttnArgs a, int R, T* O) {
-  const int lane = threadIdx.x & 31, d = a.d;
+  const int lane = threadIdx.x & 31, d = a.d, r = 8 * blockIdx.y + (threadIdx.x >> 5);
   const RowTile t = row_tile(a, R, blockIdx.x);
-  if (t.shares == 1) return;
-  for (int r = threadIdx.x >> 5; r < t.rows; r += blockDim.x >> 5) {
-    const int64_t row = t.row0 + r;
-    const float* pr = a.part + row * a.n_chunks * (d + 4);
-    float M = -INFINITY;
-    for (int c = 0; c < t.shares; ++c) M = fmaxf(M, pr[c * (d + 4) + d]);
-    float sum = 0.f;
-    for (int c = 0; c < t.shares; ++c)
-      sum += exp2f(pr[c * (d + 4) + d] - M) * pr[c * (d + 4) + d + 1];
-    const float inv = 1.f / sum;
-    for (int i = 4 * lane; i < d; i += 128) {
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int c = 0; c < t.shares; ++c) {
-        const float w = exp2f(pr[c * (d + 4) + d] - M) * inv;
-        const float4 v = *reinterpret_cast<const float4*>(pr + c * (d + 4) + i);
-        acc.x = fmaf(w, v.x, acc.x);
-        acc.y = fmaf(w, v.y, acc.y);
-        acc.z = fmaf(w, v.z, acc.z);
-        acc.w = fmaf(w, v.w, acc.w);
-      }
-      store_f4(O + row * d + i, acc);
-    }
-    if (lane == 0) a.lse[row] = (M + log2f(sum)) * 0.6931471805599453f;
+  if (t.shares == 1 || r >= t.rows) return;
+  const int64_t row = t.row0 + r;
+  const int pitch = d + 4;
+  const float* pr = a.part + row * a.n_chunks * pitch;
+  // lane i weighs shares i and i + 32 (there are 64 at most)
+  float m[2], l[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int c = min(lane + 32 * h, t.shares - 1);
+    const float2 ml = *reinterpret_cast<const float2*>(pr + c * pitch + d);
+    m[h] = lane + 32 * h < t.shares ? ml.x : -INFINITY;
+    l[h] = ml.y;
   }
+  const float M = warp_max(fmaxf(m[0], m[1]));
+  float f[2] = {exp2f(m[0] - M), exp2f(m[1] - M)};
+  const float sum = warp_sum(f[0] * l[0] + f[1] * l[1]), inv = 1.f / sum;
+  __shared__ float weights[8][64];   // (lanes past d leave the column loop)
+  float* weight = weights[threadIdx.x >> 5];
+  weight[lane] = f[0];
+  weight[lane + 32] = f[1];
+  __syncwarp();
+  for (int i = 4 * lane; i < d; i += 128) {
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int c = 0; c < t.shares; ++c) {
+      const float w = weight[c];
+      const float4 v = *reinterpret_cast<const float4*>(pr + c * pitch + i);
+      acc = make_float4(fmaf(w, v.x, acc.x), fmaf(w, v.y, acc.y), fmaf(w, v.z, acc.z),
+                        fmaf(w, v.w, acc.w));
+    }
+    store_f4(O + row * d + i, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+  }
+  if (lane == 0) a.lse[row] = (M + log2f(sum)) * 0.6931471805599453f;
 }
 
 // Rows per CTA: 16 for batches whose requests have few rows on average, else as many as O's register
@@ -331,11 +340,10 @@ static cudaError_t launch_simt(const ChunkAttnArgs& a, int64_t slots, const void
                                const void* c4K, const void* c4V, const void* c128K,
                                const void* c128V, const void* rawK, const void* rawV, void* O,
                                cudaStream_t stream) {
-  auto kernel = chunk_simt_kernel<T, R, N, DM>;
   const int smem = (int)sizeof(SimtTile<T, R, N, DM>);
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const cudaError_t e = allow_smem<chunk_simt_kernel<T, R, N, DM>>(smem);
   if (e != cudaSuccess) return e;
-  kernel<<<dim3((unsigned)slots, a.n_chunks), 256, smem, stream>>>(
+  chunk_simt_kernel<T, R, N, DM><<<dim3((unsigned)slots, a.n_chunks), 256, smem, stream>>>(
       a, (const T*)Q, (const T*)c4K, (const T*)c4V, (const T*)c128K, (const T*)c128V,
       (const T*)rawK, (const T*)rawV, (T*)O);
   return cudaGetLastError();
@@ -361,7 +369,7 @@ static int launch_chunk_attn(const ChunkAttnArgs& a, int R, int64_t slots, const
                      : TV_SIMT(32, 32, 512);
 #undef TV_SIMT
   if (e == cudaSuccess && a.n_chunks > 1) {
-    chunk_simt_merge_kernel<T><<<(unsigned)slots, 256, 0, stream>>>(a, R, (T*)O);
+    chunk_simt_merge_kernel<T><<<dim3((unsigned)slots, R / 8), 256, 0, stream>>>(a, R, (T*)O);
     e = cudaGetLastError();
   }
   if (e != cudaSuccess) {

@@ -749,12 +749,17 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
   if (warp == 1) tmem_dealloc1(sm.tmem, 512);
 }
 
-// Joins the parts of items that several CTAs have: grid (slots, rows / kJoinRows), D / 128 warps per row
-// with four columns per lane, so that the parts of a row are read with many loads in flight.
-constexpr int kJoinRows = 2;
+// Joins the parts of items that several CTAs have: grid (slots, 64 / rows per CTA).  Few slots: D / 128
+// warps per row with one vector of columns per lane and the loads of eight parts in flight (an item may
+// have dozens of parts); many: a warp per row, which takes one wave of CTAs instead of four (64 items of
+// two to four parts: 8 us with a warp per row, 12 us with four).
+constexpr int kWideSlots = 48;
 
-template <int D>
-__global__ void __launch_bounds__(kJoinRows * D / 4) few_merge_kernel(const __grid_constant__ Params p) {
+template <int D, bool kWide>
+__global__ void __launch_bounds__(256) few_merge_kernel(const __grid_constant__ Params p) {
+  constexpr int kPerRow = kWide ? D / 4 : 32;       // threads of a row
+  constexpr int kVecs = kWide ? 1 : D / 128;        // vectors of four columns per thread
+  constexpr int kRow = D + 4;
   const int lane = threadIdx.x & 31, slot = blockIdx.x, b = request_at(p, slot);
   const int k = b < 0 ? 0 : slot - slot_of(p, b);
   const bool some = b >= 0 && k < items_of(p, b);
@@ -765,13 +770,14 @@ __global__ void __launch_bounds__(kJoinRows * D / 4) few_merge_kernel(const __gr
   if (!some) return;
   const int2 piece = p.pieces[slot];
   const int c0 = piece.x, c1 = c0 + piece.y - 1;   // the CTAs that have the item
-  const int r = kJoinRows * blockIdx.y + threadIdx.x / (D / 4), col = 4 * (threadIdx.x % (D / 4));
+  const int r = (256 / kPerRow) * blockIdx.y + threadIdx.x / kPerRow, at = 4 * (threadIdx.x % kPerRow);
   if (c0 == c1 || r >= it.rows) return;
-  constexpr int kRow = D + 4;
   // CTA c's part: the one that goes on (1) of the first CTA, the one begun before (0) of the others
   auto part = [&](int c) { return p.part + (((int64_t)c * 2 + (c == c0)) * kRows + r) * kRow; };
-  // 32 parts at a time: lane i weighs part i; the loads of eight are in flight together
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float4 acc[kVecs];
+#pragma unroll
+  for (int j = 0; j < kVecs; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+  // 32 parts at a time: lane i weighs part i
   float M = -INFINITY, sum = 0.f;
   for (int first = c0; first <= c1; first += 32) {
     const int n = min(32, c1 - first + 1);
@@ -781,19 +787,28 @@ __global__ void __launch_bounds__(kJoinRows * D / 4) few_merge_kernel(const __gr
     const float old = exp2f(M - base), f = lane < n ? exp2f(m - base) : 0.f;
     M = top;
     sum = sum * old + warp_sum(f * ml.y);
-    acc = make_float4(acc.x * old, acc.y * old, acc.z * old, acc.w * old);
-#pragma unroll 8
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j)
+      acc[j] = make_float4(acc[j].x * old, acc[j].y * old, acc[j].z * old, acc[j].w * old);
+#pragma unroll (kWide ? 8 : 3)
     for (int i = 0; i < n; ++i) {
       const float w = __shfl_sync(0xffffffffu, f, i);
-      const float4 v = *reinterpret_cast<const float4*>(part(first + i) + col);
-      acc = make_float4(fmaf(w, v.x, acc.x), fmaf(w, v.y, acc.y), fmaf(w, v.z, acc.z),
-                        fmaf(w, v.w, acc.w));
+      const float* from = part(first + i) + at;
+#pragma unroll
+      for (int j = 0; j < kVecs; ++j) {
+        const float4 v = *reinterpret_cast<const float4*>(from + 128 * j);
+        acc[j] = make_float4(fmaf(w, v.x, acc[j].x), fmaf(w, v.y, acc[j].y), fmaf(w, v.z, acc[j].z),
+                             fmaf(w, v.w, acc[j].w));
+      }
     }
   }
   const float inv = 1.f / sum;
   const int64_t row = (int64_t)it.row0 + r;
-  store_f4(p.O + row * D + col, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
-  if (col == 0) p.lse[row] = (M + log2f(sum)) * 0.6931471805599453f;
+#pragma unroll
+  for (int j = 0; j < kVecs; ++j)
+    store_f4(p.O + row * D + at + 128 * j,
+             make_float4(acc[j].x * inv, acc[j].y * inv, acc[j].z * inv, acc[j].w * inv));
+  if (at == 0) p.lse[row] = (M + log2f(sum)) * 0.6931471805599453f;
 }
 
 }  // namespace few
@@ -828,13 +843,15 @@ template <int D>
 cudaError_t launch_few(const tv::few::Params& p, int ctas, int slots, cudaStream_t stream) {
   using namespace tv::few;
   static_assert(sizeof(Smem<D>) <= 232448, "shared memory of one CTA exceeds the 227 KB limit");
-  cudaError_t e = cudaFuncSetAttribute(few_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)sizeof(Smem<D>));
+  cudaError_t e = tv::allow_smem<few_kernel<D>>((int)sizeof(Smem<D>));
   if (e != cudaSuccess) return e;
   e = tv::launch_pdl(few_kernel<D>, dim3(ctas), dim3(kThreads), sizeof(Smem<D>), stream, p);
   if (e != cudaSuccess) return e;
-  return tv::launch_pdl(few_merge_kernel<D>, dim3(slots, kRows / kJoinRows), dim3(kJoinRows * D / 4), 0,
-                        stream, p);
+  if constexpr (1024 % D == 0)   // (whole rows per CTA)
+    if (slots <= kWideSlots)
+      return tv::launch_pdl(few_merge_kernel<D, true>, dim3(slots, kRows * D / 1024), dim3(256), 0, stream,
+                            p);
+  return tv::launch_pdl(few_merge_kernel<D, false>, dim3(slots, kRows / 8), dim3(256), 0, stream, p);
 }
 
 }  // namespace
