@@ -195,10 +195,11 @@ __host__ __device__ __forceinline__ bool streams(const AppendArgs& a) {
   return a.rope % (2 * VW) == 0 && half <= 16 && (half & (half - 1)) == 0 && (a.d / VW) % (2 * half) == 0;
 }
 
-template <typename T>
+// positions() fills pos; it runs while the first rows are on their way.
+template <typename T, typename F>
 __device__ void stream_rows(const AppendArgs& a, const T* Q, T* Qr, int row0, int row1, int t0,
-                            const int* pos, float2* table) {
-  constexpr int VW = VecWidth<T>::n, U = 8;
+                            const int* pos, float2* table, F&& positions) {
+  constexpr int VW = VecWidth<T>::n, U = 4;
   const int per_row = a.d / VW, half = a.rope / 2, first = a.d - a.rope, tid = threadIdx.x;
   const int n = (row1 - row0) * per_row, tokens = (row1 - 1) / a.H - t0 + 1;
   const int apart = a.pairs == TV_ROPE_PAIRS ? 0 : half / VW;   // lanes to the partner
@@ -210,9 +211,10 @@ __device__ void stream_rows(const AppendArgs& a, const T* Q, T* Qr, int row0, in
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int i = base + u * (int)blockDim.x + tid;
-      if (i < n) x[u] = __ldcs(reinterpret_cast<const uint4*>(from + (int64_t)i * VW));
+      if (i < n) x[u] = *reinterpret_cast<const uint4*>(from + (int64_t)i * VW);
     }
-    if (base == 0) {   // the angles, while the rows are on their way
+    if (base == 0) {
+      positions();
       for (int k = tid; k < tokens * half; k += blockDim.x) {
         const int p = pos[k / half];
         if (p >= 0) table[k] = turn_of(p, a.inv_freq[k % half]);
@@ -265,8 +267,11 @@ __device__ void stream_rows(const AppendArgs& a, const T* Q, T* Qr, int row0, in
   }
 }
 
-// Rows per CTA: a thread moves 128 bytes at a time whether whole rows or their rotated part.
-constexpr int kTurnRows = 32, kTurnTokens = kTurnRows + 1;
+// Rows per CTA.  Streams of more than four waves take four times as many, and an ordinary launch: each
+// CTA's wait for the kernel in front costs them more than starting beside it gives (16384 tokens of 64
+// heads behind 41 us of keys and values: 500 -> 365 us, of which this kernel is 324, 6.6 TB/s; in place
+// 271 -> 127 us).
+constexpr int kTurnRows = 32, kLongRows = 128, kTurnTokens = kTurnRows + 1;
 
 constexpr int kCachedStarts = 1024;   // requests whose starts are searched in shared memory
 
@@ -278,29 +283,34 @@ __device__ __forceinline__ const int32_t* cached_starts(const Chunk& c, int32_t*
   return copy;
 }
 
-template <typename T, bool kStream>
+// (at most kTurnTokens tokens: kRows == kLongRows with 8 heads or more)
+template <typename T, bool kStream, int kRows>
 __global__ void __launch_bounds__(256) append_queries_kernel(AppendArgs a, const T* Q, T* Qr) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   __shared__ int32_t starts_copy[kCachedStarts + 1];
   __shared__ int pos[kTurnTokens];
-  const int rows = a.c.n_new * a.H, row0 = blockIdx.x * kTurnRows;   // < 2^31
-  const int row1 = rows - row0 > kTurnRows ? row0 + kTurnRows : rows;
+  const int rows = a.c.n_new * a.H, row0 = blockIdx.x * kRows;   // < 2^31
+  const int row1 = rows - row0 > kRows ? row0 + kRows : rows;
   const int t0 = row0 / a.H, tokens = (row1 - 1) / a.H - t0 + 1;
   // nothing is read that the kernel in front (keys and values) writes: it waits for what is read here,
   // and writes the caches only
-  const int32_t* starts = cached_starts(a.c, starts_copy);
-  if ((int)threadIdx.x < tokens) {
-    const int t = t0 + threadIdx.x, b = request_of(starts, a.c.B, t);
-    pos[threadIdx.x] = b < 0 || starts[b] < 0 || starts[b + 1] > a.c.n_new
-                           ? -1
-                           : (int)max(0, a.c.L[b]) + t - starts[b];
-  }
-  __syncthreads();
+  auto positions = [&] {
+    const int32_t* starts = cached_starts(a.c, starts_copy);
+    if ((int)threadIdx.x < tokens) {
+      const int t = t0 + threadIdx.x, b = request_of(starts, a.c.B, t);
+      pos[threadIdx.x] = b < 0 || starts[b] < 0 || starts[b + 1] > a.c.n_new
+                             ? -1
+                             : (int)max(0, a.c.L[b]) + t - starts[b];
+    }
+    __syncthreads();
+  };
   float2* table = reinterpret_cast<float2*>(smem_raw);
-  if constexpr (kStream)
-    stream_rows(a, Q, Qr, row0, row1, t0, pos, table);
-  else
+  if constexpr (kStream) {
+    stream_rows(a, Q, Qr, row0, row1, t0, pos, table, positions);
+  } else {
+    positions();
     turn_rows<T, 4>(a, Q, Qr, row0, row1, t0, pos, table);
+  }
   pdl_wait();
   pdl_launch_dependents();
 }
@@ -524,17 +534,21 @@ static int launch_append(const AppendArgs& a, const Layers<T>& y, const void* K,
                          const void* Q, void* Qr, cudaStream_t stream) {
   const char* fn = "tv_chunk_append";
   const int n = a.c.n_new, B = a.c.B;
-  // room for the cosines and sines of the tokens that kTurnRows rows may touch
-  const size_t table = (size_t)(kTurnRows < (kTurnRows - 1) / a.H + 2 ? kTurnRows
-                                                                      : (kTurnRows - 1) / a.H + 2) *
-                       (a.rope / 2) * sizeof(float2);
+  // room for the cosines and sines of the tokens that a CTA's rows may touch
+  auto table_of = [&](int rows) {
+    const int tokens = (rows - 1) / a.H + 2 < rows ? (rows - 1) / a.H + 2 : rows;
+    return (size_t)tokens * (a.rope / 2) * sizeof(float2);
+  };
+  const size_t table = table_of(kTurnRows);
   const size_t kv = sizeof(AppendSmem<T>) > table ? sizeof(AppendSmem<T>) : table;
   constexpr int kMost = 128 * 1024;   // the most that any call takes: 32 tokens' tables are 64 KB
   static_assert(sizeof(AppendSmem<T>) <= kMost, "shared memory of the appending CTAs");
   if (allow_smem<append_blocks_kernel<T>>(kMost) != cudaSuccess ||
       allow_smem<append_requests_kernel<T>>(kMost) != cudaSuccess ||
-      allow_smem<append_queries_kernel<T, true>>(kMost) != cudaSuccess ||
-      allow_smem<append_queries_kernel<T, false>>(kMost) != cudaSuccess)
+      allow_smem<append_queries_kernel<T, true, kLongRows>>(kMost) != cudaSuccess ||
+      allow_smem<append_queries_kernel<T, true, kTurnRows>>(kMost) != cudaSuccess ||
+      allow_smem<append_queries_kernel<T, false, kLongRows>>(kMost) != cudaSuccess ||
+      allow_smem<append_queries_kernel<T, false, kTurnRows>>(kMost) != cudaSuccess)
     return tv_check_launch(fn);
   cudaError_t e = cudaSuccess;
   if (n <= 2 * (int64_t)B) {
@@ -545,11 +559,22 @@ static int launch_append(const AppendArgs& a, const Layers<T>& y, const void* K,
     e = launch_pdl(append_blocks_kernel<T>, dim3(slots * kC128Ranks), dim3(kThreads),
                    sizeof(AppendSmem<T>), stream, a, y, (const T*)K, (const T*)V);
     const int64_t rows = (int64_t)n * a.H;
-    if (e == cudaSuccess && Q != nullptr)
-      e = launch_pdl(Q != Qr && streams<T>(a) ? append_queries_kernel<T, true>
-                                              : append_queries_kernel<T, false>,
-                     dim3((unsigned)((rows + kTurnRows - 1) / kTurnRows)), dim3(256), table, stream, a,
-                     (const T*)Q, (T*)Qr);
+    if (e == cudaSuccess && Q != nullptr) {
+      const bool stream_q = Q != Qr && streams<T>(a);
+      const bool long_q = a.H >= 8 && rows >= 16 * 152 * kLongRows;   // (four waves of CTAs)
+      const int per = long_q ? kLongRows : kTurnRows;
+      auto kernel = stream_q ? (long_q ? append_queries_kernel<T, true, kLongRows>
+                                       : append_queries_kernel<T, true, kTurnRows>)
+                             : (long_q ? append_queries_kernel<T, false, kLongRows>
+                                       : append_queries_kernel<T, false, kTurnRows>);
+      const dim3 grid((unsigned)((rows + per - 1) / per));
+      if (long_q) {
+        kernel<<<grid, 256, table_of(per), stream>>>(a, (const T*)Q, (T*)Qr);
+        e = cudaPeekAtLastError();
+      } else {
+        e = launch_pdl(kernel, grid, dim3(256), table_of(per), stream, a, (const T*)Q, (T*)Qr);
+      }
+    }
     if (e == cudaSuccess)
       e = launch_pdl(append_lengths_kernel, dim3((B + 7) / 8), dim3(256), 0, stream, a);
   }
