@@ -70,6 +70,19 @@ __device__ __forceinline__ RowTile row_tile(const ChunkAttnArgs& a, int R, int s
   return t;
 }
 
+// 16 bytes into shared memory behind the thread's back (zeros if not there), in groups.
+__device__ __forceinline__ void copy16(float* to, const void* from, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                   (uint32_t)__cvta_generic_to_shared(to)),
+               "l"(from), "r"(there ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copies_close() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kOpen>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kOpen) : "memory");
+}
+
 template <typename T, int R, int N, int DM>
 struct SimtTile {
   static constexpr int kPitch = DM + 4;   // (rows 4 banks apart)
@@ -142,29 +155,45 @@ __global__ void __launch_bounds__(256)
     for (int c = 0; c < CI; ++c) o[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
   __syncthreads();
+  // The K or V rows of the entries e0 .. e0 + N - 1 on their way into shared memory.
+  auto fetch = [&](float (*to)[Tile::kPitch], const T* s4, const T* s128, const T* sraw, int e0,
+                   const int64_t* at) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int u = 0; u < N * kVecs / 256; ++u) {
+        const int i = u * 256 + tid, r = i / kVecs, c = (i % kVecs) * VW, e = e0 + r;
+        const T* from = e < t.n4 ? s4 : e < t.n4 + t.n128 ? s128 : sraw;
+        const bool there = at[r] >= 0 && c < d;
+        copy16(&to[r][c], from + (there ? at[r] * d + c : 0), there);
+      }
+    } else {
+      uint4 x[N * kVecs / 256];
+#pragma unroll
+      for (int u = 0; u < N * kVecs / 256; ++u) {
+        const int i = u * 256 + tid, r = i / kVecs, c = (i % kVecs) * VW, e = e0 + r;
+        const T* from = e < t.n4 ? s4 : e < t.n4 + t.n128 ? s128 : sraw;
+        x[u] = make_uint4(0u, 0u, 0u, 0u);
+        if (at[r] >= 0 && c < d) x[u] = ld16(from + at[r] * d + c);
+      }
+#pragma unroll
+      for (int u = 0; u < N * kVecs / 256; ++u) {
+        const int i = u * 256 + tid, r = i / kVecs, c = (i % kVecs) * VW;
+        float f[VW];
+        cvt16(x[u], (T*)nullptr, f);
+#pragma unroll
+        for (int k = 0; k < VW; k += 4)
+          *reinterpret_cast<float4*>(&to[r][c + k]) = make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]);
+      }
+    }
+    copies_close();
+  };
+  fetch(sm.k, c4K, c128K, rawK, e_lo, sm.at[0]);
   int parity = 0;
   for (int e0 = e_lo; e0 < e_hi; e0 += N, parity ^= 1) {
-    for (int i = tid; i < N * kVecs; i += 256) {
-      const int r = i / kVecs, c = (i % kVecs) * VW, e = e0 + r;
-      const int64_t row = sm.at[parity][r];
-      uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x;
-      if (row >= 0 && c < d) {
-        const T* ks = e < t.n4 ? c4K : e < t.n4 + t.n128 ? c128K : rawK;
-        const T* vs = e < t.n4 ? c4V : e < t.n4 + t.n128 ? c128V : rawV;
-        x = ld16(ks + row * d + c);
-        y = ld16(vs + row * d + c);
-      }
-      float f[VW];
-      cvt16(x, (T*)nullptr, f);
-#pragma unroll
-      for (int k = 0; k < VW; k += 4)
-        *reinterpret_cast<float4*>(&sm.k[r][c + k]) = make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]);
-      cvt16(y, (T*)nullptr, f);
-#pragma unroll
-      for (int k = 0; k < VW; k += 4)
-        *reinterpret_cast<float4*>(&sm.v[r][c + k]) = make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]);
-    }
+    // V's rows arrive while the logits are formed, the next K rows while O is
+    fetch(sm.v, c4V, c128V, rawV, e0, sm.at[parity]);
     if (tid < N) sm.at[parity ^ 1][tid] = locate(e0 + N + tid);
+    copies_wait<1>();
     __syncthreads();
     // logits: rows ty + 16 i, entries tx + 16 j
     float s[RI][EI];
@@ -222,7 +251,9 @@ __global__ void __launch_bounds__(256)
         o[i][c].w *= alpha;
       }
     }
-    __syncwarp();   // a row's probabilities are written and read by the same half-warp
+    copies_wait<0>();
+    __syncthreads();
+    if (e0 + N < e_hi) fetch(sm.k, c4K, c128K, rawK, e0 + N, sm.at[parity ^ 1]);
     // O: columns 4 tx + 64 c
 #pragma unroll 2
     for (int e = 0; e < N; e += 4) {
