@@ -102,6 +102,8 @@ __global__ void __launch_bounds__(256)
   extern __shared__ __align__(16) unsigned char smem_raw[];
   Tile& sm = *reinterpret_cast<Tile*>(smem_raw);
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, d = a.d;
+  pdl_wait();
+  pdl_launch_dependents();
   if (blockIdx.x == 0 && blockIdx.y == 0)
     for (int b = tid; b < a.c.B; b += 256) {
       const int state = attn_state(a.c, b);
@@ -310,6 +312,8 @@ __global__ void __launch_bounds__(256)
 template <typename T>
 __global__ void __launch_bounds__(256) chunk_simt_merge_kernel(ChunkAttnArgs a, int R, T* O) {
   const int lane = threadIdx.x & 31, d = a.d, r = 8 * blockIdx.y + (threadIdx.x >> 5);
+  pdl_wait();
+  pdl_launch_dependents();
   const RowTile t = row_tile(a, R, blockIdx.x);
   if (t.shares == 1 || r >= t.rows) return;
   const int64_t row = t.row0 + r;
@@ -355,15 +359,23 @@ static int simt_rows(const tv_shape* s, int n_new) {
 static int64_t simt_slots(const tv_shape* s, int n_new) {
   return (int64_t)n_new * s->H / simt_rows(s, n_new) + s->B;
 }
-// Shares of an item's entries: enough CTAs for two per SM, up to the shares of a full cache.
+// Shares of an item's entries: enough CTAs with work that they even out over the SMs, up to the shares
+// of a full cache (there are at least B items when every request has a token).  Small tiles: 100
+// requests of one token, d = 64, 142 us with 2 CTAs with work per SM, 103 with 6, 89 with 10, 86 with
+// 16; of 32 rows (7 requests of 100 tokens, d = 512): 2410 with 2, 2101 with 3; of 64 rows (7 requests
+// of 486, d = 256): 2556 and 2556, but 6 requests of d = 64 behind 0 to 2000 tokens 41 and 46.
+constexpr int kMostShares = 64;
+constexpr int share_ctas(int R) { return 152 * (R == 16 ? 10 : R == 32 ? 3 : 2); }
 static int simt_chunks(const tv_shape* s, int n_new) {
-  const int64_t slots = simt_slots(s, n_new);
+  const int R = simt_rows(s, n_new), ctas = share_ctas(R);
+  int64_t items = (int64_t)n_new * s->H / R;
+  if (items < s->B) items = s->B;
   int64_t entries = (s->tail_mode == TV_TAIL_WINDOW ? s->W : 128) + 64;
   if (s->comp_mask & TV_COMP_C4) entries += s->c4_cap;
   if (s->comp_mask & TV_COMP_C128) entries += s->c128_cap;
-  int64_t n = (2 * 152 + slots - 1) / slots;
+  int64_t n = (ctas + items - 1) / items;
   if (n > (entries + kShare - 1) / kShare) n = (entries + kShare - 1) / kShare;
-  return (int)(n < 1 ? 1 : n > 64 ? 64 : n);
+  return (int)(n < 1 ? 1 : n > kMostShares ? kMostShares : n);
 }
 
 template <typename T, int R, int N, int DM>
@@ -374,10 +386,9 @@ static cudaError_t launch_simt(const ChunkAttnArgs& a, int64_t slots, const void
   const int smem = (int)sizeof(SimtTile<T, R, N, DM>);
   const cudaError_t e = allow_smem<chunk_simt_kernel<T, R, N, DM>>(smem);
   if (e != cudaSuccess) return e;
-  chunk_simt_kernel<T, R, N, DM><<<dim3((unsigned)slots, a.n_chunks), 256, smem, stream>>>(
-      a, (const T*)Q, (const T*)c4K, (const T*)c4V, (const T*)c128K, (const T*)c128V,
-      (const T*)rawK, (const T*)rawV, (T*)O);
-  return cudaGetLastError();
+  return launch_pdl(chunk_simt_kernel<T, R, N, DM>, dim3((unsigned)slots, a.n_chunks), dim3(256), smem,
+                    stream, a, (const T*)Q, (const T*)c4K, (const T*)c4V, (const T*)c128K,
+                    (const T*)c128V, (const T*)rawK, (const T*)rawV, (T*)O);
 }
 
 template <typename T>
@@ -399,10 +410,9 @@ static int launch_chunk_attn(const ChunkAttnArgs& a, int R, int64_t slots, const
         : a.d <= 256 ? TV_SIMT(64, 32, 256)
                      : TV_SIMT(32, 32, 512);
 #undef TV_SIMT
-  if (e == cudaSuccess && a.n_chunks > 1) {
-    chunk_simt_merge_kernel<T><<<dim3((unsigned)slots, R / 8), 256, 0, stream>>>(a, R, (T*)O);
-    e = cudaGetLastError();
-  }
+  if (e == cudaSuccess && a.n_chunks > 1)
+    e = launch_pdl(chunk_simt_merge_kernel<T>, dim3((unsigned)slots, R / 8), dim3(256), 0, stream, a, R,
+                   (T*)O);
   if (e != cudaSuccess) {
     cudaGetLastError();
     return tv_set_error(TV_ERR_CUDA, "tv_chunk_attn: launch failed: %s", cudaGetErrorString(e));
@@ -412,10 +422,14 @@ static int launch_chunk_attn(const ChunkAttnArgs& a, int R, int64_t slots, const
 
 }  // namespace tv
 
-// Rows times shares never exceed 64 (2 * 152 + slots), and slots are below 2 * 152 where there is more
-// than one share; no more is asked for more tokens.
+// Shares s <= ctas / items + 1 with items <= ctas where s > 1, and rows <= R (items + 1), so rows times
+// shares are at most R (ctas + items + s) <= R (2 ctas + 64), for every R that n_new or fewer tokens
+// may give.
 size_t tv_chunk_simt_workspace(const tv_shape* s, int n_new) {
-  const int64_t rows = (int64_t)n_new * s->H * 64, most = 64 * 4 * 152;
+  const int R = s->d > 256 ? 32 : 64;
+  const auto bound = [](int R) { return (int64_t)R * (2 * tv::share_ctas(R) + tv::kMostShares); };
+  const int64_t rows = (int64_t)n_new * s->H * tv::kMostShares;
+  const int64_t most = bound(16) > bound(R) ? bound(16) : bound(R);
   return (size_t)(rows < most ? rows : most) * (s->d + 4) * sizeof(float);
 }
 
