@@ -477,8 +477,7 @@ int tv_pages_compact(const tv_shape* shape, const int32_t* L, int32_t* page_refs
  *   is inactive).  K, V, Q, Qr, the caches and ld_kv's bytes 16-byte aligned.
  * Device errors, each leaving that request as it was (its Qr rows are unspecified): TV_ERR_ARG
  * (starts that leave 0 .. n_new or descend -- the requests behind may then be left out too --, L < 0, no
- * page for a new position), TV_ERR_CAPACITY
- * (L + n > raw_cap or an entry beyond cap_m).
+ * page for a new position), TV_ERR_CAPACITY (L + n > raw_cap or an entry beyond cap_m).
  */
 int tv_chunk_append(const tv_shape* shape, int32_t n_new, const int32_t* starts, const void* K,
                     const void* V, int64_t ld_kv, const void* Q, int32_t rope_dim,
@@ -498,14 +497,16 @@ int tv_chunk_append(const tv_shape* shape, int32_t n_new, const int32_t* starts,
  * n_sel must be 0 (selection lists belong to rounds).
  *   n_new, starts as in tv_chunk_append; Q [n_new][H][d] in; O [n_new][H][d] out (dtype); lse
  *   [n_new][H] fp32 out: natural-log sum of exp(logits); rows of no request are left alone
- *   Q, O and the caches 16-byte aligned; workspace: device buffer of ws_bytes >=
+ *   Q, O and the caches 16-byte aligned, O apart from Q; the chunk's rows are finite, as all rows of
+ *   the caches (a NaN or infinity in a token's row also reaches the tokens in front of it that share
+ *   a tile); workspace: device buffer of ws_bytes >=
  *   tv_chunk_workspace_size(shape, n_new), 256-byte aligned (what is enough for n_new tokens is for
  *   fewer); calls that overlap on the GPU need one each.
  * Host errors: TV_ERR_ARG, TV_ERR_SHAPE, TV_ERR_WORKSPACE, TV_ERR_DTYPE (TV_ATTN_TCGEN05 asked for
  * an unsupported shape).
  * Device errors, that request's rows left alone: TV_ERR_ARG (starts that leave 0 .. n_new or, with
- * all outputs unspecified, descend; L < n), TV_ERR_CAPACITY (L > raw_cap or more entries than cap_m); TV_ERR_ARG for a page
- * that is missing (page 0 is read instead); TV_ERR_TIMEOUT.
+ * all outputs unspecified, descend; L < n), TV_ERR_CAPACITY (L > raw_cap or more entries than
+ * cap_m); TV_ERR_ARG for a page that is missing (page 0 is read instead); TV_ERR_TIMEOUT.
  */
 size_t tv_chunk_workspace_size(const tv_shape* shape, int32_t n_new);
 int tv_chunk_attn(const tv_shape* shape, int32_t n_new, const int32_t* starts, const void* Q,

@@ -64,6 +64,18 @@ def test_attn_refuses(lib, kw, code):
     assert lib.tv_last_error_string().startswith(b"tv_chunk_attn")
 
 
+def test_outputs_that_overlap_the_queries_are_refused(lib):
+    """8 rows of 4 heads (see _shape): the queries end 8 H d es bytes behind their start."""
+    s = _shape()
+    size = 8 * s.H * s.d * (2 if s.dtype == _lib.TV_BF16 else 4)
+    for off in (0, 16, size - 16, 16 - size):
+        assert _attn(lib, O=OK + size, Q=OK + size + off) == -1
+        assert lib.tv_last_error_string() == b"tv_chunk_attn: O overlaps Q"
+    for off in (16, size - 16, 16 - size):     # (Qr may be Q itself)
+        assert _append(lib, Q=OK + size, Qr=OK + size + off) == -1
+        assert lib.tv_last_error_string() == b"tv_chunk_append: Qr overlaps Q and is not Q"
+
+
 def _beam(lib, B=6, width=3, vocab=100, ld=100, dtype=0, logits=OK, scores=OK, done=OK, eos=1, scale=1.0,
           source=OK, token=OK, new=OK, new_done=OK, rank=OK, ws=OK, ws_bytes=1 << 20, st=OK):
     s = _lib.make_shape(B=B, D=1, H=1, d=8, comp_mask=1)

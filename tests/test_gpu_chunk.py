@@ -513,6 +513,94 @@ def test_many_requests_on_tensor_cores():
     s.check_attend(requests=set(rng.integers(0, B, 40).tolist()))
 
 
+def test_more_requests_than_a_cta_keeps_starts_of():
+    """64-row items on tensor cores, more requests than their starts fit into shared memory."""
+    rng = np.random.default_rng(13)
+    B = 4500
+    before = rng.integers(0, 20, B).tolist()
+    news = rng.choice([0, 1, 1, 3], B).tolist()
+    s = Batch(before, news, H=3, d=128, dtype="bf16", seed=13, ms=(4,))
+    s.append()
+    s.attend()
+    torch.cuda.synchronize()
+    assert s.status.item() == 0
+    s.check_attend(requests=set(rng.integers(0, B, 60).tolist()))
+
+
+def test_many_requests_on_clusters():
+    """More requests than the clusters count the items of, 281600 rows in 44 of them."""
+    B = 2100
+    before = [b % 19 for b in range(B)]
+    news = [50 if b % 48 == 7 else 0 for b in range(B)]
+    s = Batch(before, news, H=128, d=512, dtype="bf16", seed=14, ms=(4,))
+    assert s.n * 128 > 128 * B
+    s.append()
+    s.attend()
+    torch.cuda.synchronize()
+    assert s.status.item() == 0
+    s.check_attend(requests={7, 7 + 48 * 20, 7 + 48 * 43})
+
+
+@pytest.mark.parametrize("d,dtype,rope,pairs", [(64, "f32", 64, 0), (64, "f32", 62, 0), (64, "f32", 30, 1),
+                                                (128, "bf16", 64, 0), (128, "bf16", 24, 0)])
+def test_append_long_streams_of_queries(d, dtype, rope, pairs):
+    """More rows than four waves of CTAs, of requests that share CTAs; into other memory and in place."""
+    s = Batch([5, 0, 300], [1200, 7, 1239], H=128, d=d, dtype=dtype, rope=rope, pairs=pairs, pad_front=1,
+              pad_back=2, seed=15, ms=(4,))
+    old = [s.oracle_caches(b) for b in range(s.B)]
+    Q = s.Q.clone()
+    s.append(Q, s.Qr)
+    assert s.status.item() == 0
+    s.check_append(old, s.Qr)
+    assert torch.all(s.Qr[0] == 7) and torch.all(s.Qr[-2:] == 7)
+    s.L.copy_(torch.tensor(s.before, dtype=torch.int32))
+    s.append(Q, Q)
+    assert torch.equal(Q[1:-2], s.Qr[1:-2])
+    assert torch.equal(Q[0], s.Q[0]) and torch.equal(Q[-2:], s.Q[-2:])
+
+
+@pytest.mark.parametrize("news,tile", [([1] * 40, 0), ([2] * 3, 1), ([300], 1)])
+def test_a_wait_that_runs_out_reports_timeout_and_the_context_stays_usable(news, tile):
+    """The producers leave out the K copies of a tile, so the wait for it expires after 200 us; what was
+    issued is drained, and the next call is right again."""
+    before = [3000 - 7 * b for b in range(len(news))]
+    s = Batch(before, news, H=64, d=512, dtype="bf16", P=512, seed=16)
+    s.append()
+    _lib.tv_debug_attn_timeout(200_000, tile)
+    try:
+        s.attend()
+        torch.cuda.synchronize()
+    finally:
+        _lib.tv_debug_attn_timeout(2_000_000_000, -1)
+    assert s.status.item() == -8
+    s.status.zero_()
+    s.O.fill_(7.0)
+    s.lse.fill_(7.0)
+    s.attend()
+    torch.cuda.synchronize()
+    assert s.status.item() == 0
+    s.check_attend(requests={0, len(news) - 1})
+
+
+def test_two_streams_at_once():
+    """Two batches of their own, on two streams: bit for bit what each gives alone."""
+    batches = [Batch([900, 40, 7000], [n, 1, 1], H=64, d=512, dtype="bf16", P=512, seed=17 + n)
+               for n in (1, 250)]
+    want = []
+    for s in batches:
+        s.append()
+        s.attend()
+        torch.cuda.synchronize()
+        want.append((s.O.clone(), s.lse.clone()))
+    streams = [torch.cuda.Stream() for _ in batches]
+    for _ in range(20):
+        for s, stream in zip(batches, streams):
+            s.attend(stream)
+    torch.cuda.synchronize()
+    for s, (O, lse) in zip(batches, want):
+        assert s.status.item() == 0 and torch.equal(s.O, O) and torch.equal(s.lse, lse)
+
+
 def test_prompts_in_chunks_and_rounds_on_one_pool():
     """A prompt appended in two parts behind an empty pool gives the cache that prefill makes, and verify
     rounds go on from it bit for bit as from a prefilled one."""

@@ -691,6 +691,12 @@ static int check_chunk(const tv_shape* s, const char* fn, int32_t n_new, const i
   return TV_OK;
 }
 
+// Whether two buffers of as many bytes share some.
+static bool overlap(const void* a, const void* b, int64_t bytes) {
+  const int64_t apart = (int64_t)((uintptr_t)a - (uintptr_t)b);
+  return apart < bytes && -apart < bytes;
+}
+
 // Null and alignment checks of the cache's layers (rows are moved 16 bytes at a time).
 static int check_layers(const tv_shape* s, const char* fn, const void* rawK, const void* rawV,
                         const void* c4K, const void* c4V, const void* c128K, const void* c128V) {
@@ -741,6 +747,8 @@ extern "C" int tv_chunk_append(const tv_shape* s, int32_t n_new, const int32_t* 
     if (Q != nullptr) TV_REQUIRE(Qr, fn);
     if (((uintptr_t)K | (uintptr_t)V | (uintptr_t)Q | (uintptr_t)(Q ? Qr : nullptr)) & 15u)
       return tv_set_error(TV_ERR_ARG, "%s: K, V, Q and Qr must be 16-byte aligned", fn);
+    if (Q != nullptr && Q != Qr && overlap(Q, Qr, (int64_t)n_new * s->H * s->d * es))
+      return tv_set_error(TV_ERR_ARG, "%s: Qr overlaps Q and is not Q", fn);
   }
   return tv_launch_append(s, n_new, starts, K, V, ld_kv, Q, rope_dim, rope_pairs, inv_freq, g4, g128,
                           Qr, rawK, rawV, c4K, c4V, c128K, c128V, L, status, (cudaStream_t)stream);
@@ -802,6 +810,8 @@ extern "C" int tv_chunk_attn(const tv_shape* s, int32_t n_new, const int32_t* st
   if (ws_bytes < need)
     return tv_set_error(TV_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", fn, ws_bytes,
                         need);
+  if (overlap(Q, O, (int64_t)n_new * s->H * s->d * (s->dtype == TV_BF16 ? 2 : 4)))
+    return tv_set_error(TV_ERR_ARG, "%s: O overlaps Q", fn);
   const ChunkKernel k = chunk_kernel(s, n_new);
   if (k == kChunkSimt && s->attn_kernel == TV_ATTN_TCGEN05)
     return tv_set_error(TV_ERR_DTYPE, "%s: the tcgen05 kernels need bf16, d a multiple of 128 and an "

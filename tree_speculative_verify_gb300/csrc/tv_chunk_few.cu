@@ -230,7 +230,7 @@ __device__ void producer(const Params& p, Smem<D>& sm) {
   const int lane = threadIdx.x & 31;
   Walk w(p, sm);
   int slot = 0, seg = 0;
-  uint32_t phase = 0;
+  uint32_t phase = 0, issued = 0, issued_phase = 0;   // bit per slot: copied into, when last
   bool ok = true;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (!__all_sync(0xffffffffu, mbar_wait(bar, parity, &sm.abort, p.timeout_ns))) {
@@ -244,6 +244,8 @@ __device__ void producer(const Params& p, Smem<D>& sm) {
     for (int s = 0; s < kSlices; ++s) {
       if (!wait(&sm.empty[slot], phase ^ 1)) return;
       if (issue) {
+        issued |= 1u << slot;
+        issued_phase = (issued_phase & ~(1u << slot)) | phase << slot;
         if (lane == 0) mbar_arrive_expect_tx(&sm.full[slot], x.units * 8192);
         __syncwarp();
         if (lane < x.units) tma_load_2d(sm.ring[slot] + lane * 8192, map, 64 * s, row, &sm.full[slot]);
@@ -260,8 +262,10 @@ __device__ void producer(const Params& p, Smem<D>& sm) {
                                                            : (v ? &p.mRawV : &p.mRawK);
   };
   bool waited = !p.gathered;
+  int queries = 0;   // segments whose Q was copied
   for (; ok && w.next(p); ++seg) {
     if (seg > 0 && !wait(&sm.q_free, (seg - 1) & 1)) break;
+    queries = seg + 1;
     if (lane == 0) mbar_arrive_expect_tx(&sm.q_full, kSlices * kRows * 128);
     __syncwarp();
     if (lane < kSlices) tma_load_2d(sm.q[lane], &p.mQ, 64 * lane, w.it.row0, &sm.q_full);
@@ -293,12 +297,11 @@ __device__ void producer(const Params& p, Smem<D>& sm) {
       row = after_row;
     }
   }
-  // nothing of this CTA's may be in flight when it exits: after an abort, what was issued is waited for
-  if (!ok || *reinterpret_cast<volatile int*>(&sm.abort)) {
-    const uint64_t t0 = global_ns();
-    while (global_ns() - t0 < 50000) {
-    }
-  }
+  // no copy may be in flight when the CTA exits, which only an abort can leave behind
+  volatile int never = 0;
+  for (int i = 0; i < kSlots; ++i)
+    if (issued >> i & 1) mbar_wait(&sm.full[i], issued_phase >> i & 1, &never, p.timeout_ns / 4);
+  if (queries > 0) mbar_wait(&sm.q_full, (queries - 1) & 1, &never, p.timeout_ns / 4);
 }
 
 // ---- MMAs (warp 1, lane 0) ------------------------------------------------------------------------
