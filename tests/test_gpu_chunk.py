@@ -582,6 +582,62 @@ def test_a_wait_that_runs_out_reports_timeout_and_the_context_stays_usable(news,
     s.check_attend(requests={0, len(news) - 1})
 
 
+@pytest.mark.parametrize("d,dtype,H", [(512, "bf16", 64), (128, "bf16", 4), (64, "f32", 3)])
+@pytest.mark.parametrize("news", [[1, 1, 2], [90, 1, 100]])
+@pytest.mark.parametrize("caps", [(201, 50, 1), (127, 31, 0), (250, 62, 1)])
+def test_odd_capacities(d, dtype, H, news, caps):
+    """Contiguous layers whose rows per request are no multiple of a tile, full to the last row."""
+    raw, c4, c128 = caps
+    before = [raw - n for n in news]
+    s = Batch(before, news, H=H, d=d, dtype=dtype, seed=raw, q_std=2.0)
+    for k, rows in zip(NAMES, (raw, raw, c4, c4, max(c128, 1), max(c128, 1))):
+        s.t[k] = s.t[k][:, :rows].contiguous()
+    s.shape.raw_cap, s.shape.c4_cap, s.shape.c128_cap = caps
+    s.cap = raw
+    s.ws = torch.full((max(_lib.tv_chunk_workspace_size(s.shape, s.n), 256),), 0xff, dtype=torch.uint8,
+                      device="cuda")
+    if c128 == 0:
+        s.t["c128K"].fill_(9.0)
+    s.append()
+    s.attend()
+    torch.cuda.synchronize()
+    assert s.status.item() == 0 and s.L.tolist() == [raw] * 3
+    assert c128 > 0 or torch.all(s.t["c128K"] == 9.0)
+    s.check_attend()
+
+
+@pytest.mark.parametrize("d,H,n", [(512, 64, 1), (512, 64, 250), (64, 4, 2)])
+def test_offsets_past_32_bits(d, H, n):
+    """The same batch in a small pool and at the far end of one of more than 2^32 elements: the same bits."""
+    P = 1024
+    s = Batch([3000, 5], [n, 1], H=H, d=d, dtype="bf16", P=P, seed=19, rope=16)
+    big_pages = 2 ** 32 // (P * d) + s.pool + 1
+    far = {}
+    for k, m in zip(NAMES, (1, 1, 4, 4, 128, 128)):
+        far[k] = torch.zeros((big_pages, P // m, d), dtype=s.dt, device="cuda")
+        far[k][-s.pool:] = s.t[k]
+    table = s.gpu_table
+    s.append(s.Q, s.Qr)
+    s.attend()
+    torch.cuda.synchronize()
+    near, O, lse, Qr = s.t, s.O.clone(), s.lse.clone(), s.Qr.clone()
+    s.t = far
+    s.far_table = table + (big_pages - s.pool)
+    s.shape.n_pool_pages = big_pages
+    s.shape.page_table = s.far_table.data_ptr()
+    s.L.copy_(torch.tensor(s.before, dtype=torch.int32))
+    for x in (s.O, s.lse, s.Qr):
+        x.fill_(7.0)
+    s.append(s.Q, s.Qr)
+    s.attend()
+    torch.cuda.synchronize()
+    assert s.status.item() == 0
+    assert torch.equal(s.O, O) and torch.equal(s.lse, lse) and torch.equal(s.Qr, Qr)
+    for k in NAMES:
+        assert torch.equal(far[k][-s.pool:], near[k]), k
+        assert not far[k][:-s.pool].any(), k
+
+
 def test_two_streams_at_once():
     """Two batches of their own, on two streams: bit for bit what each gives alone."""
     batches = [Batch([900, 40, 7000], [n, 1, 1], H=64, d=512, dtype="bf16", P=512, seed=17 + n)
