@@ -1658,54 +1658,55 @@ __global__ void gather_c128_kernel(Paging pg, int row_u4, int64_t c128_cap, int6
   }
 }
 
-// Joins the KV chunks of a split item's rows: grid (half of the clusters, 8), a warp per row, 4 rows per
-// warp.
+// Joins the KV chunks of a split item's rows: grid (half of the clusters, 32), a warp per row with the
+// loads of four chunks in flight (4 items of 9 chunks: 35 us with four rows per warp, one after the other).
 template <bool kPaged>
 __global__ void __launch_bounds__(256) chunk_merge_kernel(const __grid_constant__ Params p) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, r = 8 * blockIdx.y + (threadIdx.x >> 5);
   pdl_wait();
   const Split split = split_of(p, p.B < kRankMax ? p.first_item[p.B] : slots_of(p));
   const int item = split.whole + blockIdx.x;
   if (item >= split.items) return;
   Item it;
   chunk_item<kPaged>(p, split, p.B < kRankMax ? p.first_item : nullptr, p.starts, p.L, item, 0, 0, it);
-  const int nc = it.nc, rows = min(it.rows, 256);
-  if (nc == 1) return;
+  const int nc = it.nc;
+  if (nc == 1 || r >= it.rows) return;
   constexpr int64_t kRow = 512 + 4;
-  for (int r = 32 * blockIdx.y + warp; r < min(rows, 32 * (int)blockIdx.y + 32); r += 8) {
-    const int64_t row = (int64_t)it.row0 + r;
-    const float* pr = p.part + (it.part + (int64_t)r * split.chunks) * kRow;
-    float m = -INFINITY, l = 0.f;   // lane c: chunk c (and c + 32)
-    for (int c = lane; c < nc; c += 32) {
-      const float mc = pr[c * kRow + 512], lc = pr[c * kRow + 513];
-      if (lc > 0.f) {
-        const float top = fmaxf(m, mc);
-        l = l * exp2f(m - top) + lc * exp2f(mc - top);
-        m = top;
-      }
-    }
-    const float M = warp_max(m);
-    const float sum = warp_sum(l > 0.f ? l * exp2f(m - M) : 0.f), inv = 1.f / sum;
-    float4 acc[4];
+  const int64_t row = (int64_t)it.row0 + r;
+  const float* pr = p.part + (it.part + (int64_t)r * split.chunks) * kRow;
+  float m[2], l[2];   // lane c: chunks c and c + 32 (there are 64 at most)
 #pragma unroll
-    for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-    for (int c = 0; c < nc; ++c) {
-      const float* pc = pr + c * kRow;
-      const float w = pc[513] > 0.f ? exp2f(pc[512] - M) * inv : 0.f;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float4 v = *reinterpret_cast<const float4*>(pc + 128 * k + 4 * lane);
-        acc[k].x = fmaf(w, v.x, acc[k].x);
-        acc[k].y = fmaf(w, v.y, acc[k].y);
-        acc[k].z = fmaf(w, v.z, acc[k].z);
-        acc[k].w = fmaf(w, v.w, acc[k].w);
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) store_f4(p.O + row * 512 + 128 * k + 4 * lane, acc[k]);
-    if (lane == 0) p.lse[row] = (M + log2f(sum)) * 0.6931471805599453f;
+  for (int h = 0; h < 2; ++h) {
+    const int c = lane + 32 * h;
+    const float2 ml = c < nc ? *reinterpret_cast<const float2*>(pr + c * kRow + 512)
+                             : make_float2(-INFINITY, 0.f);
+    l[h] = ml.y;
+    m[h] = ml.y > 0.f ? ml.x : -INFINITY;   // (a chunk in which the row sees nothing)
   }
+  const float M = warp_max(fmaxf(m[0], m[1]));
+  const float f0 = exp2f(m[0] - M), f1 = exp2f(m[1] - M);
+  const float sum = warp_sum(f0 * l[0] + f1 * l[1]), inv = 1.f / sum;
+  float4 acc[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int c = 0; c < nc; ++c) {
+    const float w = __shfl_sync(0xffffffffu, c < 32 ? f0 : f1, c & 31);
+    const float* pc = pr + c * kRow + 4 * lane;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float4 v = *reinterpret_cast<const float4*>(pc + 128 * k);
+      acc[k].x = fmaf(w, v.x, acc[k].x);
+      acc[k].y = fmaf(w, v.y, acc[k].y);
+      acc[k].z = fmaf(w, v.z, acc[k].z);
+      acc[k].w = fmaf(w, v.w, acc[k].w);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    store_f4(p.O + row * 512 + 128 * k + 4 * lane,
+             make_float4(acc[k].x * inv, acc[k].y * inv, acc[k].z * inv, acc[k].w * inv));
+  if (lane == 0) p.lse[row] = (M + log2f(sum)) * 0.6931471805599453f;
 }
 
 }  // namespace tc
@@ -2194,7 +2195,7 @@ int tv_launch_chunk_tc(const tv_shape* s, int n_new, const int32_t* starts, cons
              : cudaLaunchKernelEx(&cfg, attn_kernel<false, false, true>, p)) != cudaSuccess)
     return tv_check_launch(fn);
   if (p.n_chunks > 1 && clusters > 1) {
-    const dim3 grid((unsigned)clusters / 2, 8);
+    const dim3 grid((unsigned)clusters / 2, 32);
     if ((paged ? tv::launch_pdl(chunk_merge_kernel<true>, grid, dim3(256), 0, stream, p)
                : tv::launch_pdl(chunk_merge_kernel<false>, grid, dim3(256), 0, stream, p)) != cudaSuccess)
       return tv_check_launch(fn);
