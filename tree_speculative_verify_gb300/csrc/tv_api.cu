@@ -754,18 +754,19 @@ extern "C" int tv_chunk_append(const tv_shape* s, int32_t n_new, const int32_t* 
                           Qr, rawK, rawV, c4K, c4V, c128K, c128V, L, status, (cudaStream_t)stream);
 }
 
-// The kernel of a chunk.  Tensor cores, bf16: d = 512 and more rows than 10240 and than two 64-row items
+// The kernel of a chunk.  Tensor cores, bf16: d = 512, more than 6144 rows and more than two 64-row items
 // per request on average, on the tree attention's clusters, which share a tile of keys and values
 // among 256 rows; otherwise, and for d = 128, 256 and 384, 64 rows per CTA, which reads a tile for 64 rows
-// but spreads few rows over every SM.  Measured, 64 heads: 16 requests behind 4000 tokens with 8 new tokens
-// each (8192 rows) 76 us with 64 rows per CTA and 101 on clusters, with 16 each 127 and 95; 4 behind
-// 16000 with 16 each 94 and 127, with 32 each (8192 rows) 170 and 123; 64 behind 4000 with 2 each (8192)
-// 88 and 102, with 4 each 150 and 85.  CUDA cores: everything else.
+// but spreads few rows over every SM.  Measured, 64 heads, pages, us with 64 rows per CTA and on
+// clusters: 4096 rows of 4 requests behind 500, 4000 and 16000 tokens 29 and 43, 43 and 47, 92 and 68;
+// 8192 rows of them 39 and 35, 68 and 44, 166 and 86; of 64 requests (128 rows each) behind 500 and 4000
+// tokens 43 and 47, 79 and 85, with half as many rows again 51 and 47, 109 and 86.  CUDA cores:
+// everything else.
 enum ChunkKernel { kChunkSimt, kChunkFew, kChunkMany };
 static ChunkKernel chunk_kernel(const tv_shape* s, int32_t n_new) {
   if (s->attn_kernel == TV_ATTN_SIMT || !tv_few_ok(s) || !tv_tc_available()) return kChunkSimt;
   const int64_t rows = (int64_t)n_new * s->H;
-  return s->d == 512 && rows > 10240 && rows > 128 * (int64_t)s->B ? kChunkMany : kChunkFew;
+  return s->d == 512 && rows > 6144 && rows > 128 * (int64_t)s->B ? kChunkMany : kChunkFew;
 }
 
 extern "C" size_t tv_chunk_workspace_size(const tv_shape* s, int32_t n_new) {

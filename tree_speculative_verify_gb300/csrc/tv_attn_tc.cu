@@ -423,7 +423,7 @@ __device__ __forceinline__ int64_t tile_row(const Params& p, int kind, int b, in
     return (int64_t)b * p.c4_cap + idx;
   }
   if (kind == kC128) return (int64_t)b * p.c128_cap + idx;
-  // (a chunk's raw tiles start at multiples of 128 and lie on one page)
+  // (a chunk's raw tiles lie on one page each)
   if (kPaged && kChunk) return layer_row(p.pg, b, idx, p.raw_cap, 1, p.status);
   if (kPaged) return (int64_t)b * p.tail_rows + (idx - t0);
   return (int64_t)b * p.raw_cap + idx;
@@ -481,7 +481,7 @@ __device__ __forceinline__ int chunk_items(const Params& p, int s0, int s1, int 
 
 // Items of the last round, if they leave half of the clusters or more idle, are split into as many KV
 // chunks as give every cluster one (at most p.n_chunks, the most that a full cache is worth): 1024 tokens
-// behind 65536, 256 items on 36 clusters, 2093 -> 1913 us.
+// behind 65536, 256 items on 36 clusters, 2093 -> 1913 us (1763 by now).
 __device__ __forceinline__ Split split_of(const Params& p, int items) {
   const int rest = items % p.n_clusters;
   Split s;
@@ -528,7 +528,10 @@ __device__ __forceinline__ void chunk_item(const Params& p, const Split& split, 
   it.pos0 = L - n;
   const int last = (int)(rows < first + 256 ? rows : first + 256) - 1;
   const int p_lo = it.pos0 + (int)first / p.H, p_hi = it.pos0 + last / p.H;
-  const Span span = span_of(p.comp_mask, p.tail_mode, p.W, p_lo, p_hi, kPaged ? 128 : 1);
+  Span span = span_of(p.comp_mask, p.tail_mode, p.W, p_lo, p_hi, 1);
+  // pools: raw tiles that leave the first one's page start at multiples of 128 (each then lies on one)
+  if (kPaged && span.t0 % p.pg.page_tokens + ((span.end - span.t0 + 127) & ~127) > p.pg.page_tokens)
+    span.t0 &= ~127;
   Layout& y = it.y;
   y.L = span.end;
   y.n4 = span.n4;
@@ -539,10 +542,11 @@ __device__ __forceinline__ void chunk_item(const Params& p, const Split& split, 
   y.T128 = (y.n128 + 127) / 128;
   y.Traw = (y.nraw + 127) / 128;
   y.T = y.T4 + y.T128 + y.Traw;
-  it.nc = item < split.whole ? 1 : min(split.chunks, (y.T + kChunkTiles - 1) / kChunkTiles);
-  if (chunk >= it.nc) return;
-  it.tb = (int)((int64_t)y.T * chunk / it.nc);
-  it.te = (int)((int64_t)y.T * (chunk + 1) / it.nc);
+  it.te = y.T;
+  if (item < split.whole) return;
+  it.nc = min(split.chunks, (y.T + kChunkTiles - 1) / kChunkTiles);
+  it.tb = min(y.T, (int)((int64_t)y.T * chunk / it.nc));   // (chunks behind the item's last: none)
+  it.te = min(y.T, (int)((int64_t)y.T * (chunk + 1) / it.nc));
 }
 
 template <bool kPaged, bool kChunk>
@@ -622,13 +626,16 @@ __device__ void producer(const Params& p, Smem& sm, bool role_s, uint32_t sub) {
     issued[i] = false;
     issued_phase[i] = 0;
   }
-  auto acquire = [&]() -> bool {
-    if (!mbar_wait(&sm.h.empty[r.slot], r.phase ^ 1, &sm.h.abort, p.timeout_ns)) {
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    bool done = mbar_wait(bar, parity, &sm.h.abort, p.timeout_ns);
+    if (kPaged) done = __all_sync(0xffffffffu, done);   // (the lanes exchange rows below)
+    if (!done) {
       if (lane == 0) fail(sm, p.status);
       return false;
     }
     return true;
   };
+  auto acquire = [&]() -> bool { return wait(&sm.h.empty[r.slot], r.phase ^ 1); };
   auto leader_full = [&]() { return mapa_cluster(smem_u32(&sm.h.full[r.slot]), leader); };
   auto expect = [&](uint32_t bytes) {
     if (sub == 0) mbar_arrive_expect_tx(&sm.h.full[r.slot], 2 * bytes);
@@ -646,12 +653,30 @@ __device__ void producer(const Params& p, Smem& sm, bool role_s, uint32_t sub) {
     const int b = it.b;
     const Layout& y = it.y;
     const int tree_row = !kChunk && tv_in_range(b * p.D, 0, p.tree_rows, p.status, 2) ? b * p.D : 0;
+    // First rows of a tile's halves.  With page pools lane i looks up tiles tb + i, tb + 32 + i, ..,
+    // 16 tiles ahead: looked up one tile ahead by every lane alike, as contiguous rows are, they held
+    // the copies up (1024 tokens behind 65536: 1903 us, 1766 so).
+    auto row_of = [&](int t) -> int2 {
+      int2 rw = make_int2(0, 0);
+      if (t < it.tb || t >= it.te) return rw;
+      const Tile x = tile_of(y, t);
+      if (!kChunk && x.kind == kExtra) return rw;
+      if (role_s) {
+        rw.x = (int)tile_row<kPaged, kChunk>(p, x.kind, b, x.row0 + (int)sub * (x.nqk / 2), y.t0);
+      } else {
+        rw.x = (int)tile_row<kPaged, kChunk>(p, x.kind, b, x.row0, y.t0);
+        rw.y = kPaged ? (int)tile_row<kPaged, kChunk>(p, x.kind, b, x.row0 + 64, y.t0) : rw.x + 64;
+      }
+      return rw;
+    };
+    int2 rows, ahead;
+    if (kPaged)
+      rows = row_of(it.tb + lane);
+    else
+      ahead = row_of(it.tb);
     // pair O: the previous item's epilogue stages O in the V ring; its slots are free again
     // once the role warps report v_free
-    if (!role_s && q > 0 && !mbar_wait(&sm.h.v_free, (q - 1) & 1, &sm.h.abort, p.timeout_ns)) {
-      if (lane == 0) fail(sm, p.status);
-      break;
-    }
+    if (!role_s && q > 0 && !wait(&sm.h.v_free, (q - 1) & 1)) break;
     ++q;
     if (role_s) {
       for (int j = 0; j < kQSlots && ok; ++j) {
@@ -669,24 +694,17 @@ __device__ void producer(const Params& p, Smem& sm, bool role_s, uint32_t sub) {
         finish(false);
       }
     }
-    // tile rows are computed one tile ahead, so that with paged pools the page-table reads are
-    // in flight while the producer waits for slots
-    auto row_of = [&](int t) -> int2 {
-      int2 rw = make_int2(0, 0);
-      if (t < it.tb || t >= it.te) return rw;
-      const Tile x = tile_of(y, t);
-      if (!kChunk && x.kind == kExtra) return rw;
-      if (role_s) {
-        rw.x = (int)tile_row<kPaged, kChunk>(p, x.kind, b, x.row0 + (int)sub * (x.nqk / 2), y.t0);
-      } else {
-        rw.x = (int)tile_row<kPaged, kChunk>(p, x.kind, b, x.row0, y.t0);
-        rw.y = kPaged ? (int)tile_row<kPaged, kChunk>(p, x.kind, b, x.row0 + 64, y.t0) : rw.x + 64;
-      }
-      return rw;
-    };
-    int2 cur = row_of(it.tb);
     for (int t = it.tb; t < it.te && ok; ++t) {
-      const int2 next = row_of(t + 1);
+      int2 cur;
+      if (kPaged) {
+        const int i = (t - it.tb) & 31;
+        if (i == 0 && t > it.tb) rows = ahead;
+        if (i == 16) ahead = row_of(t + 16 + lane);
+        cur = make_int2(__shfl_sync(0xffffffffu, rows.x, i), __shfl_sync(0xffffffffu, rows.y, i));
+      } else {
+        cur = ahead;
+        ahead = row_of(t + 1);
+      }
       const Tile x = tile_of(y, t);
       if (kOverlap && x.kind == kExtra) pdl_wait_once(waited);   // the scratch rows
       for (int g = 0; g < 2 && ok; ++g) {
@@ -753,7 +771,6 @@ __device__ void producer(const Params& p, Smem& sm, bool role_s, uint32_t sub) {
         }
         finish(loads);
       }
-      cur = next;
     }
   }
   // drain: no copy issued by the pair may still be in flight when the CTA exits (the leader's

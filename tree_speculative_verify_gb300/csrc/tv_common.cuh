@@ -159,13 +159,13 @@ __device__ __forceinline__ int64_t mapped_row(const Paging& pg, int b, int64_t i
     return (int64_t)b * cap + (tv_in_range(idx, 0, cap, status, 5) ? idx : 0);
   if (idx >= cap) idx = cap - 1;
   if (idx < 0) idx = 0;
-  const int64_t rpp = pg.page_tokens / tokens_per_row;
-  const int32_t page = pg.table[(int64_t)b * pg.max_pages + idx / rpp];
+  const uint32_t rpp = (uint32_t)(pg.page_tokens / tokens_per_row), i = (uint32_t)idx;   // < 2^30
+  const int32_t page = pg.table[(int64_t)b * pg.max_pages + i / rpp];
   if (page < 0 || page >= pg.n_pool_pages) {
     record_error(status, TV_ERR_ARG);
-    return ~(idx % rpp);
+    return ~(int64_t)(i % rpp);
   }
-  return (int64_t)page * rpp + idx % rpp;
+  return (int64_t)page * rpp + i % rpp;
 }
 
 // The same for reads: a page id outside the pool addresses page 0, so no access leaves the pool.
