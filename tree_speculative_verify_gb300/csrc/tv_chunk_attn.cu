@@ -360,16 +360,20 @@ static int64_t simt_slots(const tv_shape* s, int n_new) {
   return (int64_t)n_new * s->H / simt_rows(s, n_new) + s->B;
 }
 // Shares of an item's entries: enough CTAs with work that they even out over the SMs, up to the shares
-// of a full cache (there are at least B items when every request has a token).  Small tiles: 100
-// requests of one token, d = 64, 142 us with 2 CTAs with work per SM, 103 with 6, 89 with 10, 86 with
-// 16; of 32 rows (7 requests of 100 tokens, d = 512): 2410 with 2, 2101 with 3; of 64 rows (7 requests
-// of 486, d = 256): 2556 and 2556, but 6 requests of d = 64 behind 0 to 2000 tokens 41 and 46.
+// of a full cache.  Small tiles take many rounds of CTAs (at most one slot in two holds an item when every
+// request has a token): 100 requests of one token, d = 64, 142 us with 2 CTAs with work per SM, 103 with
+// 6, 85 with 10, 82 with 16.  Large ones fill the SMs about once, counted with the slots, of which a few
+// hold nothing: 480 fp32 rows of d = 64 in each of 6 requests 56 us with 6 shares, 70 with 7, which start
+// a second round; d = 512 (32 rows), 7 requests of 1600 rows, 2410 us with 2 CTAs per SM, 2101 with 3.
 constexpr int kMostShares = 64;
 constexpr int share_ctas(int R) { return 152 * (R == 16 ? 10 : R == 32 ? 3 : 2); }
 static int simt_chunks(const tv_shape* s, int n_new) {
   const int R = simt_rows(s, n_new), ctas = share_ctas(R);
   int64_t items = (int64_t)n_new * s->H / R;
-  if (items < s->B) items = s->B;
+  if (R > 16)
+    items += s->B;
+  else if (items < s->B)
+    items = s->B;
   int64_t entries = (s->tail_mode == TV_TAIL_WINDOW ? s->W : 128) + 64;
   if (s->comp_mask & TV_COMP_C4) entries += s->c4_cap;
   if (s->comp_mask & TV_COMP_C128) entries += s->c128_cap;
