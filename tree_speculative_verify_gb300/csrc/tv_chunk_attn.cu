@@ -93,8 +93,15 @@ struct SimtTile {
   int64_t at[2][N];   // rows of this tile's and the next one's entries, -1: none
 };
 
+// CTAs per SM that registers are left for: as many as shared memory holds, at most 2 (small tiles 3).
 template <typename T, int R, int N, int DM>
-__global__ void __launch_bounds__(256)
+constexpr int simt_ctas() {
+  const int fit = (int)(227 * 1024 / sizeof(SimtTile<T, R, N, DM>)), most = R == 16 ? 3 : 2;
+  return fit < most ? fit : most;
+}
+
+template <typename T, int R, int N, int DM>
+__global__ void __launch_bounds__(256, (simt_ctas<T, R, N, DM>()))
     chunk_simt_kernel(ChunkAttnArgs a, const T* Q, const T* c4K, const T* c4V, const T* c128K,
                       const T* c128V, const T* rawK, const T* rawV, T* O) {
   using Tile = SimtTile<T, R, N, DM>;
