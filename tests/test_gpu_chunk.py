@@ -559,7 +559,7 @@ def test_append_long_streams_of_queries(d, dtype, rope, pairs):
     assert torch.equal(Q[0], s.Q[0]) and torch.equal(Q[-2:], s.Q[-2:])
 
 
-@pytest.mark.parametrize("news,tile", [([1] * 40, 0), ([2] * 3, 1), ([300], 1)])
+@pytest.mark.parametrize("news,tile", [([1] * 40, 0), ([1] * 40, 1), ([2] * 3, 0), ([300], 1)])
 def test_a_wait_that_runs_out_reports_timeout_and_the_context_stays_usable(news, tile):
     """The producers leave out the K copies of a tile, so the wait for it expires after 200 us; what was
     issued is drained, and the next call is right again."""

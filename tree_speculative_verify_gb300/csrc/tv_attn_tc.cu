@@ -471,6 +471,10 @@ struct Item {
 // found by a search.  Batches of kRankMax requests or more take slots instead: request b's start at
 // floor(starts[b] * H / 256) + b, which leaves every request room for its items.  Tokens see different
 // entries: the item's tiles reach to what its last token sees and the softmax masks the rest.
+// Bound by the tile's chain of products, softmax and P's move between the pairs (1.7 us per tile of 128
+// entries, 1.3 at the rate of a library's matrix product) and 6 to 7 us per item for Q, the first
+// keys and O.  Measured, 64 heads: 1024 tokens behind 65536 1763 us (1.3 PFLOP/s, 144 of 152 SMs in
+// clusters of four); 2641 tokens of 24 requests, 672 items of 6 tiles, 354 us (0.53 PFLOP/s).
 __device__ __forceinline__ int chunk_items(const Params& p, int s0, int s1, int L) {
   if (s0 < 0 || s1 <= s0 || s1 > p.n_new || L < s1 - s0 || L > p.raw_lim ||
       ((p.comp_mask & TV_COMP_C4) && L / 4 > p.c4_lim) ||

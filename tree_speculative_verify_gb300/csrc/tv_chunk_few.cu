@@ -16,9 +16,8 @@
 // Work is counted in half tiles (64 entries of one item; an item is 64 rows of one request), of which two
 // make a tile: the batch's items stand in one list, request by request, each with kOpen places for opening it
 // and one per half tile, of which CTA c takes q from c q on; they may end one item, hold whole ones and
-// begin another.  An item that one CTA has whole is
-// written at once; the others leave (O, m, l) per CTA in the workspace -- at most two per CTA -- which a
-// second kernel joins in CTA order.
+// begin another.  An item that one CTA has whole is written at once; the others leave (O, m, l) per CTA
+// in the workspace -- at most two per CTA -- which a second kernel joins in CTA order.
 //
 // Softmax: thread (entry, half of the rows) holds the entry's 32 logits; row maxima are reduced over
 // the lanes by halving exchanges and over the four warps of a half through shared memory; a lane keeps
@@ -27,6 +26,13 @@
 //
 // Warps: 0 copies (TMA, a ring of 16 KB slots: 128 entries x 64 dimensions of K, or x 64 columns of
 // V), 1 issues the MMAs, 2..9 softmax and epilogue.  Every wait is bounded as in the tree attention.
+//
+// Measured, d = 512, 64 heads, pages of 1024 tokens, with the gather of C128 entries in front and the join
+// behind: 64 requests of 1024 to 8192 tokens, one new token each, 59 us (207 MB from memory, 28 us at the
+// rate of a copy; the stream itself runs at 5 to 6 TB/s, the gather takes 5 us, finding the work 3, the
+// last item's end 3, the join 5); one request of 8192 tokens 23 us, the length of the chain.  Tried and
+// slower: the gather inside this kernel, C128 boxes of 8 rows straight from the pages, an L2 prefetch of
+// the whole share, whole items per CTA.
 #include <cuda.h>
 #include <math.h>
 
@@ -45,8 +51,12 @@ constexpr int kThreads = 64 + 32 * kSmxWarps;
 constexpr int kSlotBytes = 16384;
 constexpr int kSlots = 8;          // (V slots are taken in pairs: an even number)
 constexpr int kPBytes = 16384;     // P^T of a tile: 128 entries x 64 rows
-constexpr int kOpen = 3;           // places for opening an item
-constexpr int kMinPlaces = 4;      // least places of a CTA while there are CTAs left
+// Places for opening an item (64 requests of one token: 61.5, 60.7, 61.2 and 64.4 us with 2, 3, 4 and 5; 19
+// behind up to 1550 tokens: 26.7 with 2, 24.7 with 3 and 4) and least places of a CTA while there are CTAs
+// left: a whole tile (one request of 8192 tokens: 29.2, 23.7, 25.9, 25.4 and 33.7 us with 1, 2, 3, 4 and 8),
+// two while there is an item whose parts would be too many to join (4 requests of 16000 tokens: 38 us with 2,
+// 32 with 4).
+constexpr int kOpen = 3, kMinPlaces = 2, kLongItem = 48;
 constexpr float kRescaleThreshold = 8.f;   // log2 units
 
 struct Params {
@@ -106,6 +116,7 @@ struct __align__(1024) Smem {
   uint64_t drain;
   float xmax[2][4][kRows];       // [tile parity][lane quadrant][row]: maxima, at a segment's end sums
   int scan[kThreads / 32 + 1];
+  int most[kThreads / 32 + 1];   // and the largest item
   int begin, places;             // the CTA's first place in its first item, places in all
   Item first;                    // its first item
   uint32_t tmem;
@@ -644,7 +655,7 @@ __device__ void find_work(const Params& given, Smem<D>& sm) {
   const int per = (p.n_slots + kThreads - 1) / kThreads;
   const int lo = min(p.n_slots, tid * per), hi = min(p.n_slots, lo + per);
   const int b0 = lo < hi ? request_at(p, lo) : 0;
-  int b, mine = 0;
+  int b, mine = 0, most = 0;
   Item it;
   auto look = [&](int slot) {   // the slot's item; its places, 0: none
     while (b + 1 < B && slot_of(p, b + 1) <= slot) ++b;
@@ -655,14 +666,22 @@ __device__ void find_work(const Params& given, Smem<D>& sm) {
   };
   b = b0;
 #pragma unroll 1
-  for (int slot = lo; slot < hi; ++slot) mine += look(slot);
+  for (int slot = lo; slot < hi; ++slot) {
+    const int n = look(slot);
+    mine += n;
+    most = max(most, n);
+  }
   int x = mine;   // places in front of the thread's slots
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
-  if (lane == 31) sm.scan[warp] = x;
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (lane == 31) {
+    sm.scan[warp] = x;
+    sm.most[warp] = most;
+  }
   __syncthreads();
   int total = 0;
   x -= mine;
@@ -671,8 +690,10 @@ __device__ void find_work(const Params& given, Smem<D>& sm) {
     const int y = sm.scan[w];
     x += w < warp ? y : 0;
     total += y;
+    most = max(most, sm.most[w]);
   }
-  const int q = max((total + G - 1) / G, min(kMinPlaces, total)), start = blockIdx.x * q;
+  const int least = most > kLongItem ? 2 * kMinPlaces : kMinPlaces;
+  const int q = max((total + G - 1) / G, min(least, total)), start = blockIdx.x * q;
   if ((start >= x && start < x + mine) || (blockIdx.x == 0 && lo < hi)) {
     b = b0;
 #pragma unroll 1
