@@ -361,6 +361,20 @@ def test_attend_many_rows(H, P, W, ms, news):
     s.check_attend()
 
 
+@pytest.mark.parametrize("d,dtype,H,P,W", [(512, "bf16", 1024, 512, 1024), (128, "bf16", 1000, 0, 1024),
+                                           (64, "f32", 1024, 512, 1023), (72, "bf16", 333, 0, 1024),
+                                           (512, "bf16", 2, 512, 1024), (512, "f32", 3, 512, 1024)])
+def test_most_heads_and_widest_windows(d, dtype, H, P, W):
+    s = Batch([1500, 3, 1020], [2, 1, 5], H=H, d=d, dtype=dtype, P=P, W=W, rope=8, q_std=2.0, seed=H + d)
+    old = [s.oracle_caches(b) for b in range(s.B)]
+    s.append(s.Q, s.Qr)
+    s.check_append(old, s.Qr)
+    s.attend()
+    torch.cuda.synchronize()
+    assert s.status.item() == 0
+    s.check_attend()
+
+
 def test_attend_growing_maxima():
     # logits that grow by hundreds from tile to tile: every tile rescales what is there
     s = Batch([6000, 6000], [1, 1], H=64, d=512, dtype="bf16", P=512, q_std=0.0, seed=13)

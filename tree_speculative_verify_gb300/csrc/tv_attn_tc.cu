@@ -2085,13 +2085,6 @@ void tv_attn_test_aid(uint64_t* timeout_ns, int* withhold_tile) {
   *withhold_tile = g_withhold_tile.load();
 }
 
-bool tv_chunk_tc_ok(const tv_shape* s) {
-  const int64_t lim = (int64_t)1 << 31;
-  return s->dtype == TV_BF16 && s->d == 512 && (int64_t)s->B * (s->c128_cap + 63) < lim &&
-         (s->page_tokens > 0 ||
-          ((int64_t)s->B * s->raw_cap < lim && (int64_t)s->B * s->c4_cap < lim));
-}
-
 constexpr int kMostClusters = 64;   // (a device with more clusters splits no further)
 
 // Most KV chunks of an item: one per kChunkTiles tiles of a full cache.

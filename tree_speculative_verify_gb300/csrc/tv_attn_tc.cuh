@@ -17,7 +17,6 @@ int tv_launch_attn_tc(const tv_shape* s, const tv::AttnParams<__nv_bfloat16>& p,
                       cudaStream_t stream);
 
 // The same for tv_chunk_attn (bf16, d = 512).
-bool tv_chunk_tc_ok(const tv_shape* s);
 size_t tv_chunk_tc_workspace(const tv_shape* s);
 int tv_launch_chunk_tc(const tv_shape* s, int n_new, const int32_t* starts, const void* Q,
                        const void* c4K, const void* c4V, const void* c128K, const void* c128V,

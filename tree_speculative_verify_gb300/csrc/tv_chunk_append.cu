@@ -278,7 +278,7 @@ constexpr int kTurnRows = 32, kLongRows = 128, kTurnTokens = kTurnRows + 1;
 
 constexpr int kCachedStarts = 1024;   // requests whose starts are searched in shared memory
 
-// The request that starts[0 .. B] (or their copy in shared memory) give for row t.
+// The starts, copied into shared memory where there is room for them.
 __device__ __forceinline__ const int32_t* cached_starts(const Chunk& c, int32_t* copy) {
   if (c.B > kCachedStarts) return c.starts;
   for (int i = threadIdx.x; i <= c.B; i += blockDim.x) copy[i] = c.starts[i];
