@@ -270,10 +270,11 @@ __device__ void stream_rows(const AppendArgs& a, const T* Q, T* Qr, int row0, in
   }
 }
 
-// Rows per CTA.  Streams of more than four waves take four times as many, and an ordinary launch: each
-// CTA's wait for the kernel in front costs them more than starting beside it gives (16384 tokens of 64
-// heads behind 41 us of keys and values: 500 -> 365 us, of which this kernel is 324, 6.6 TB/s; in place
-// 271 -> 127 us).
+// Rows per CTA.  Streams of more than four waves take four times as many, and an ordinary launch:
+// starting beside the keys' and values' CTAs, they stay slow after those have gone (16384 tokens of 64 heads
+// behind 41 us of keys and values: 411 us, 365 one after the other, of which this kernel is 324, 6.6
+// TB/s).  Shorter ones gain by it (10 requests of 32 heads, 38 MB of queries, 33 -> 25 us; in place 16384
+// tokens take 113 us one after the other).
 constexpr int kTurnRows = 32, kLongRows = 128, kTurnTokens = kTurnRows + 1;
 
 constexpr int kCachedStarts = 1024;   // requests whose starts are searched in shared memory
@@ -314,7 +315,8 @@ __global__ void __launch_bounds__(256) append_queries_kernel(AppendArgs a, const
     positions();
     turn_rows<T, 4>(a, Q, Qr, row0, row1, t0, pos, table);
   }
-  pdl_wait();
+  // one CTA's wait is enough for the kernel to complete after the one in front of it
+  if (blockIdx.x == gridDim.x - 1) pdl_wait();
   pdl_launch_dependents();
 }
 
