@@ -652,6 +652,20 @@ def test_offsets_past_32_bits(d, H, n):
         assert not far[k][:-s.pool].any(), k
 
 
+@pytest.mark.parametrize("d,dtype,H,n", [(512, "bf16", 64, 1), (512, "bf16", 64, 200), (128, "bf16", 8, 3),
+                                         (64, "f32", 4, 2)])
+def test_idle_requests_need_no_pages(d, dtype, H, n):
+    """A request without new tokens whose pages are elsewhere (its length stands) is no error."""
+    s = Batch([900, 2000, 40], [n, 0, 1], H=H, d=d, dtype=dtype, P=512, seed=20)
+    s.table[1] = -1
+    s.gpu_table[1] = -1
+    s.append(s.Q, s.Qr)
+    s.attend()
+    torch.cuda.synchronize()
+    assert s.status.item() == 0 and s.L.tolist() == [900 + n, 2000, 41]
+    s.check_attend()
+
+
 def test_two_streams_at_once():
     """Two batches of their own, on two streams: bit for bit what each gives alone."""
     batches = [Batch([900, 40, 7000], [n, 1, 1], H=64, d=512, dtype="bf16", P=512, seed=17 + n)

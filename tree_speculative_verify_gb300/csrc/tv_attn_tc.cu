@@ -1655,15 +1655,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
 // Paged pools: copies each request's C128 entries into contiguous rows of the workspace, `stride` (a
 // multiple of 64) per request.  A page holds 4 entries per 512 tokens, too few for the attention's
 // 64-row boxes.  Rows up to the next multiple of 64 are zeros: the values of masked entries are
-// multiplied by zero probabilities.  A warp per row.
+// multiplied by zero probabilities.  A warp per row; latency-bound (64 requests of up to 64 entries 5 us).
 __global__ void gather_c128_kernel(Paging pg, int row_u4, int64_t c128_cap, int64_t stride, int64_t raw_cap,
-                                   const int32_t* L, const uint4* __restrict__ K,
+                                   const int32_t* starts, const int32_t* L, const uint4* __restrict__ K,
                                    const uint4* __restrict__ V, uint4* gK, uint4* gV,
                                    int32_t* status) {
   pdl_wait();
   pdl_launch_dependents();
   const int b = blockIdx.y, lane = threadIdx.x & 31, Lb = L[b];
-  if (Lb <= 0 || Lb > raw_cap) return;
+  // (a request without new tokens is not looked at, nor are its pages)
+  if (Lb <= 0 || Lb > raw_cap || starts[b + 1] <= starts[b]) return;
   const int n = (Lb - 1) / 128;   // the last token sees no more
   for (int64_t w = (int64_t)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32; w < ((n + 63) & ~63);
        w += (int64_t)gridDim.x * (blockDim.x / 32)) {
@@ -2105,13 +2106,13 @@ size_t tv_chunk_gather_bytes(const tv_shape* s) {
              : 0;
 }
 
-int tv_chunk_gather(const tv_shape* s, const int32_t* L, const void* c128K, const void* c128V,
-                    void* rows, int32_t* status, cudaStream_t stream) {
+int tv_chunk_gather(const tv_shape* s, const int32_t* starts, const int32_t* L, const void* c128K,
+                    const void* c128V, void* rows, int32_t* status, cudaStream_t stream) {
   const int64_t n = (s->c128_cap + 7) / 8;
   uint4* to = reinterpret_cast<uint4*>(rows);
   if (tv::launch_pdl(tv::tc::gather_c128_kernel, dim3((unsigned)(n < 64 ? n : 64), s->B), dim3(256), 0,
                      stream, tv::paging_of(s), s->d * 2 / 16, s->c128_cap, tv_chunk_c128_stride(s),
-                     s->raw_cap, L, (const uint4*)c128K, (const uint4*)c128V, to,
+                     s->raw_cap, starts, L, (const uint4*)c128K, (const uint4*)c128V, to,
                      to + tv_chunk_gather_bytes(s) / 16, status) != cudaSuccess)
     return tv_check_launch("tv_chunk_attn");
   return TV_OK;
@@ -2188,7 +2189,7 @@ int tv_launch_chunk_tc(const tv_shape* s, int n_new, const int32_t* starts, cons
   p.withhold_tile = g_withhold_tile.load();
   if (cluster_slots() <= 0) return tv_check_launch(fn);
   if (gather > 0)
-    if (int rc = tv_chunk_gather(s, L, c128K, c128V, ws, status, stream)) return rc;
+    if (int rc = tv_chunk_gather(s, starts, L, c128K, c128V, ws, status, stream)) return rc;
   const int clusters = cluster_slots() < kMostClusters ? cluster_slots() : kMostClusters;
   p.n_clusters = clusters;
   cudaLaunchConfig_t cfg = {};

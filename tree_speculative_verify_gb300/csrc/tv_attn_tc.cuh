@@ -35,8 +35,8 @@ int tv_launch_few(const tv_shape* s, int n_new, const int32_t* starts, const voi
 // per request and bytes of one of K / V (0: not needed); tensor maps; the test aid's settings.
 int64_t tv_chunk_c128_stride(const tv_shape* s);
 size_t tv_chunk_gather_bytes(const tv_shape* s);
-int tv_chunk_gather(const tv_shape* s, const int32_t* L, const void* c128K, const void* c128V,
-                    void* rows, int32_t* status, cudaStream_t stream);
+int tv_chunk_gather(const tv_shape* s, const int32_t* starts, const int32_t* L, const void* c128K,
+                    const void* c128V, void* rows, int32_t* status, cudaStream_t stream);
 bool tv_make_map(CUtensorMap* m, const void* base, int rank, int d, uint64_t rows, uint64_t batch,
                  uint32_t box_rows);
 void tv_attn_test_aid(uint64_t* timeout_ns, int* withhold_tile);

@@ -929,7 +929,7 @@ int tv_launch_few(const tv_shape* s, int n_new, const int32_t* starts, const voi
   p.status = status;
   tv_attn_test_aid(&p.timeout_ns, &p.withhold_tile);
   if (p.gathered)
-    if (int rc = tv_chunk_gather(s, L, c128K, c128V, ws, status, stream)) return rc;
+    if (int rc = tv_chunk_gather(s, starts, L, c128K, c128V, ws, status, stream)) return rc;
   const int ctas = sm_count(), slots = (int)slots_of(s, n_new);
   const cudaError_t e = d == 512   ? launch_few<512>(p, ctas, slots, stream)
                         : d == 384 ? launch_few<384>(p, ctas, slots, stream)
