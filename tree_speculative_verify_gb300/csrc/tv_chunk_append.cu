@@ -8,7 +8,7 @@
 // four C4 blocks it holds; a completed C128 block is joined over the cluster by the routine that
 // prefill runs.  So every row is read once and entries depend on the stored rows alone.  Queries
 // are rotated on the way from memory to memory.  Both are bound by HBM: 4 d es bytes per token and
-// 2 H d es for its queries.  Measured, bf16, d = 512, 64 heads: 16384 tokens 364 us (328 at the rate of a
+// 2 H d es for its queries.  Measured, bf16, d = 512, 64 heads: 16384 tokens 363 us (328 at the rate of a
 // copy), 41 of them keys, values and entries, whose exponentials, sums and cluster barriers take four
 // times the bytes' 10 us; one token of 64 requests 14 us, of one request 8 us on the GPU, less than the
 // 20 us that a call from Python takes.
