@@ -489,6 +489,52 @@ def test_captured_and_replayed_on_another_stream(d, dtype, P):
     assert s.status.item() == 0
 
 
+@pytest.mark.parametrize("d,dtype,H,n", [(512, "bf16", 64, 8), (512, "bf16", 64, 150), (64, "f32", 4, 40)])
+def test_one_capture_serves_any_starts(d, dtype, H, n):
+    """A graph captured for n new tokens, replayed with other splits of up to n: each replay is what eager
+    calls on caches of its own give, and the rows of no request stay as they are."""
+    cut = n // 3
+    s = Batch([500, 1000, 0], [n - 2, 1, 1], H=H, d=d, dtype=dtype, P=512, rope=16, seed=21, cap=3000)
+    dev = {m: v.cuda() for m, v in s.gates.items()}
+    f = s.inv_freq.cuda()
+
+    def step(t, L, Qr, O, lse, ws, status):
+        _lib.tv_chunk_append(s.shape, s.gpu_starts, *s.KV, s.Q, 16, 0, f, dev[4], dev[128], Qr,
+                             *[t[k] for k in NAMES], L, status)
+        _lib.tv_chunk_attn(s.shape, s.gpu_starts, Qr, t["c4K"], t["c4V"], t["c128K"], t["c128V"],
+                           t["rawK"], t["rawV"], L, 1 / math.sqrt(d), O, lse, ws, status)
+
+    copy = lambda: ({k: v.clone() for k, v in s.t.items()}, s.L.clone(), s.Qr.clone(), s.O.clone(),
+                    s.lse.clone(), s.ws.clone(), s.status.clone())
+    captured, eager = copy(), copy()
+    step(*copy())
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(*captured)
+    for starts in ([0, n - 2, n - 1, n], [0, 1, 2, 3], [2, 2, 2 + cut, 2 + 2 * cut], [0, 0, 0, 0],
+                   [0, 0, n, n]):
+        s.gpu_starts.copy_(torch.tensor(starts, dtype=torch.int32))
+        for x in captured[2:5] + eager[2:5]:
+            x.fill_(7.0)
+        graph.replay()
+        step(*eager)
+        torch.cuda.synchronize()
+        assert captured[6].item() == 0 and eager[6].item() == 0
+        assert all(torch.equal(captured[0][k], eager[0][k]) for k in NAMES)
+        used = torch.zeros(n, dtype=torch.bool)
+        used[starts[0]:starts[-1]] = True
+        for x, y in zip(captured[1:5], eager[1:5]):
+            assert torch.equal(x, y)
+        for x in captured[2:5]:
+            assert torch.all(x[~used.cuda()] == 7.0)
+    news = np.diff(starts)
+    s.before = [int(x - y) for x, y in zip(captured[1].tolist(), news)]
+    s.news, s.starts, s.t, s.L, s.O, s.lse = news, np.array(starts), *captured[:2], *captured[3:5]
+    s.Q = captured[2]
+    s.check_attend()
+
+
 def test_nothing_to_do():
     s = Batch([5, 0], [0, 0], H=4, d=64, pad_back=2)
     before = {k: v.clone() for k, v in s.t.items()}
