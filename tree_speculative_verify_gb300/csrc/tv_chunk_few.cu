@@ -15,8 +15,8 @@
 //
 // Work is counted in half tiles (64 entries of one item; an item is 64 rows of one request), of which two
 // make a tile: the batch's items stand in one list, request by request, each with kOpen places for opening it
-// and one per half tile, of which CTA c takes q from c q on; they may end one item, hold whole ones and
-// begin another.  An item that one CTA has whole is written at once; the others leave (O, m, l) per CTA
+// and one per half tile, which the CTAs share (tv_share.cuh); a share may end one item, hold whole ones
+// and begin another.  An item that one CTA has whole is written at once; the others leave (O, m, l) per CTA
 // in the workspace -- at most two per CTA -- which a second kernel joins in CTA order.
 //
 // Softmax: thread (entry, half of the rows) holds the entry's 32 logits; row maxima are reduced over
@@ -38,6 +38,7 @@
 
 #include "tv_attn_tc.cuh"
 #include "tv_chunk.cuh"
+#include "tv_share.cuh"
 #include "tv_sm100.cuh"
 
 namespace tv {
@@ -51,12 +52,6 @@ constexpr int kThreads = 64 + 32 * kSmxWarps;
 constexpr int kSlotBytes = 16384;
 constexpr int kSlots = 8;          // (V slots are taken in pairs: an even number)
 constexpr int kPBytes = 16384;     // P^T of a tile: 128 entries x 64 rows
-// Places for opening an item (64 requests of one token: 61.5, 60.7, 61.2 and 64.4 us with 2, 3, 4 and 5; 19
-// behind up to 1550 tokens: 26.7 with 2, 24.7 with 3 and 4) and least places of a CTA while there are CTAs
-// left: a whole tile (one request of 8192 tokens: 29.2, 23.7, 25.9, 25.4 and 33.7 us with 1, 2, 3, 4 and 8),
-// two while there is an item whose parts would be too many to join (4 requests of 16000 tokens: 38 us with 2,
-// 32 with 4).
-constexpr int kOpen = 3, kMinPlaces = 2, kLongItem = 48;
 constexpr float kRescaleThreshold = 8.f;   // log2 units
 
 struct Params {
@@ -71,7 +66,7 @@ struct Params {
   float* lse;
   float* part;             // [CTA][2][kRows][d + 4]: 0: an item begun before, 1: one that goes on
   int n_slots;
-  int2* pieces;            // [n_slots] of the slots' items: first CTA, CTAs (written by CTA 0)
+  Piece* pieces;           // [n_slots] of the slots' items (written by CTA 0)
   int32_t* status;
   uint64_t timeout_ns;
   int withhold_tile;       // test aid: no K copies for this tile of a segment (-1: none)
@@ -115,9 +110,10 @@ struct __align__(1024) Smem {
   uint64_t o_full, o_free;       // a segment's O is complete; it has left TMEM
   uint64_t drain;
   float xmax[2][4][kRows];       // [tile parity][lane quadrant][row]: maxima, at a segment's end sums
-  int scan[kThreads / 32 + 1];
-  int most[kThreads / 32 + 1];   // and the largest item
-  int begin, places;             // the CTA's first place in its first item, places in all
+  int64_t scan[kThreads / 32];   // places of the warps' slots
+  int most[kThreads / 32];       // and the largest item
+  int begin;                     // the CTA's first place in its first item
+  int64_t places;                // places in all
   Item first;                    // its first item
   uint32_t tmem;
   int abort;
@@ -146,19 +142,16 @@ __device__ __forceinline__ int request_at(const Params& p, int slot) {   // -1: 
 }
 
 // One CTA's walk over its half tiles, the same in every warp: segments (item, half tiles ub .. ue - 1).
-struct Walk {
+struct Walk : Cut {
   Item it;
   int n_items;   // of the request
-  int left;      // places that remain
-  int ub, ue;
   bool begun;
   template <typename S>
   __device__ Walk(const Params& p, const S& sm) {
     left = sm.places;
     if (left <= 0) return;
     it = sm.first;
-    ub = max(sm.begin - kOpen, 0);
-    left -= max(kOpen - sm.begin, 0);
+    first(sm.begin, sm.places);
     n_items = -1;   // (looked up when the first item is done)
     begun = false;
   }
@@ -173,13 +166,10 @@ struct Walk {
         k = 0;
       }
       it = item_of(p, b, k);
-      ub = 0;
-      left -= kOpen;
+      Cut::next();
     }
     begun = true;
-    ue = min(it.units, ub + left);
-    left -= ue - ub;
-    return ue > ub;   // (the last place may be an item's opening)
+    return take(it.units);
   }
   __device__ bool whole() const { return ub == 0 && ue == it.units; }
 };
@@ -326,7 +316,8 @@ __device__ void mma(const Params& p, Smem<D>& sm) {
   const uint64_t q_desc = smem_desc_sw128(smem_u32(sm.q[0]), 16, 1024);
   const uint64_t p_desc = smem_desc_sw128(smem_u32(sm.p[0]), 16, 1024);
   Walk w(p, sm);
-  int slot = 0, seg = 0, i = 0;   // i: tiles so far
+  int slot = 0, seg = 0;
+  int64_t i = 0;   // tiles so far
   uint32_t phase = 0;
   bool ok = true;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -344,7 +335,7 @@ __device__ void mma(const Params& p, Smem<D>& sm) {
   };
   auto add = [](uint64_t desc, uint32_t bytes) { return desc + (uint64_t)(bytes >> 4); };
   // O += V P of the i-th tile of all, the segment's t-th
-  auto product_o = [&](const Tile& x, int t, int i) {
+  auto product_o = [&](const Tile& x, int t, int64_t i) {
     const int n_k = x.n16 / 16;
     if (!wait(&sm.p_full[i & 1], (i >> 1) & 1)) return;
     tc_fence_after();
@@ -430,7 +421,8 @@ __device__ void softmax(const Params& p, Smem<D>& sm) {
   const float sl2 = p.scale_log2;
   uint8_t* const line = sm.p[0] + (entry >> 3) * 1024 + (entry & 7) * 128;
   Walk w(p, sm);
-  int seg = 0, g = 0;
+  int seg = 0;
+  int64_t g = 0;   // tiles so far
   // A wait that runs out sets the abort flag, after which every wait returns at once: the warps go on
   // through their barriers together and write nothing.
   bool ok = true;
@@ -655,14 +647,15 @@ __device__ void find_work(const Params& given, Smem<D>& sm) {
   const int per = (p.n_slots + kThreads - 1) / kThreads;
   const int lo = min(p.n_slots, tid * per), hi = min(p.n_slots, lo + per);
   const int b0 = lo < hi ? request_at(p, lo) : 0;
-  int b, mine = 0, most = 0;
+  int b, most = 0;
+  int64_t mine = 0;
   Item it;
   auto look = [&](int slot) {   // the slot's item; its places, 0: none
     while (b + 1 < B && slot_of(p, b + 1) <= slot) ++b;
     const int k = b < 0 ? 0 : slot - slot_of(p, b);
     it.units = 0;
     if (b >= 0 && k < items_of(p, b)) it = item_of(p, b, k);
-    return it.units + (it.units > 0 ? kOpen : 0);
+    return places_of(it.units);
   };
   b = b0;
 #pragma unroll 1
@@ -671,10 +664,10 @@ __device__ void find_work(const Params& given, Smem<D>& sm) {
     mine += n;
     most = max(most, n);
   }
-  int x = mine;   // places in front of the thread's slots
+  int64_t x = mine;   // places in front of the thread's slots
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
   most = __reduce_max_sync(0xffffffffu, most);
@@ -683,30 +676,27 @@ __device__ void find_work(const Params& given, Smem<D>& sm) {
     sm.most[warp] = most;
   }
   __syncthreads();
-  int total = 0;
+  int64_t total = 0;
   x -= mine;
 #pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) {
-    const int y = sm.scan[w];
+    const int64_t y = sm.scan[w];
     x += w < warp ? y : 0;
     total += y;
     most = max(most, sm.most[w]);
   }
-  const int least = most > kLongItem ? 2 * kMinPlaces : kMinPlaces;
-  const int q = max((total + G - 1) / G, min(least, total)), start = blockIdx.x * q;
+  const int64_t q = share_of(total, most, G), start = blockIdx.x * q;
   if ((start >= x && start < x + mine) || (blockIdx.x == 0 && lo < hi)) {
     b = b0;
 #pragma unroll 1
     for (int slot = lo; slot < hi; ++slot) {
-      const int n = per == 1 ? mine : look(slot);
+      const int n = per == 1 ? (int)mine : look(slot);
       if (start >= x && start < x + n) {
         sm.first = it;
-        sm.begin = start - x;
+        sm.begin = (int)(start - x);
         sm.places = min(q, total - start);
       }
-      if (blockIdx.x == 0)   // CTAs that hold half tiles of it
-        p.pieces[slot] =
-            n > 0 ? make_int2((x + kOpen) / q, (x + n - 1) / q - (x + kOpen) / q + 1) : make_int2(0, 0);
+      if (blockIdx.x == 0) p.pieces[slot] = piece_of(x, n, q, G);
       x += n;
     }
   }
@@ -792,8 +782,8 @@ __global__ void __launch_bounds__(256) few_merge_kernel(const __grid_constant__ 
   pdl_wait();
   pdl_launch_dependents();
   if (!some) return;
-  const int2 piece = p.pieces[slot];
-  const int c0 = piece.x, c1 = c0 + piece.y - 1;   // the CTAs that have the item
+  const Piece piece = p.pieces[slot];
+  const int c0 = piece.first, c1 = c0 + piece.ctas - 1;   // the CTAs that have the item
   const int r = (256 / kPerRow) * blockIdx.y + threadIdx.x / kPerRow, at = 4 * (threadIdx.x % kPerRow);
   if (c0 == c1 || r >= it.rows) return;
   // CTA c's part: the one that goes on (1) of the first CTA, the one begun before (0) of the others
@@ -924,7 +914,7 @@ int tv_launch_few(const tv_shape* s, int n_new, const int32_t* starts, const voi
   p.O = reinterpret_cast<__nv_bfloat16*>(O);
   p.lse = lse;
   p.n_slots = (int)slots_of(s, n_new);
-  p.pieces = reinterpret_cast<int2*>(ws + 2 * gather);
+  p.pieces = reinterpret_cast<Piece*>(ws + 2 * gather);
   p.part = reinterpret_cast<float*>(ws + 2 * gather + table_bytes(s, n_new));
   p.status = status;
   tv_attn_test_aid(&p.timeout_ns, &p.withhold_tile);
