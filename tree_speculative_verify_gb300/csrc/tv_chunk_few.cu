@@ -830,10 +830,12 @@ __global__ void __launch_bounds__(256) few_merge_kernel(const __grid_constant__ 
 
 // ---- host side --------------------------------------------------------------------------------------
 bool tv_few_ok(const tv_shape* s) {
-  const int64_t lim = (int64_t)1 << 31;
-  return s->dtype == TV_BF16 && s->d % 128 == 0 && (int64_t)s->B * (s->c128_cap + 63) < lim &&
+  // rows of the tensor maps: 31 bits (page pools' raw rows and C4 entries always are)
+  const int64_t lim = (int64_t)1 << 31, B = s->B;
+  return s->dtype == TV_BF16 && s->d % 128 == 0 &&
+         (!(s->comp_mask & TV_COMP_C128) || B * (s->c128_cap + 63) < lim) &&
          (s->page_tokens > 0 ||
-          ((int64_t)s->B * s->raw_cap < lim && (int64_t)s->B * s->c4_cap < lim));
+          (B * s->raw_cap < lim && (!(s->comp_mask & TV_COMP_C4) || B * s->c4_cap < lim)));
 }
 
 namespace {
