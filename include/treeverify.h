@@ -476,8 +476,9 @@ int tv_pages_compact(const tv_shape* shape, const int32_t* L, int32_t* page_refs
  *   [rope_dim / 2] fp32 in; g4, g128 [d] fp32 in and c4K .. c128V out (nullable when the compressor
  *   is inactive).  K, V, Q, Qr, the caches and ld_kv's bytes 16-byte aligned.
  * Device errors, each leaving that request as it was (its Qr rows are unspecified): TV_ERR_ARG
- * (starts that leave 0 .. n_new or descend -- the requests behind may then be left out too --, L < 0, no
- * page for a new position), TV_ERR_CAPACITY (L + n > raw_cap or an entry beyond cap_m).
+ * (starts that leave 0 .. n_new; starts that descend -- others of the batch may then be left as they were
+ * too, and all Qr rows are unspecified --; L < 0; no page for a new position), TV_ERR_CAPACITY (L + n >
+ * raw_cap or an entry beyond cap_m).
  */
 int tv_chunk_append(const tv_shape* shape, int32_t n_new, const int32_t* starts, const void* K,
                     const void* V, int64_t ld_kv, const void* Q, int32_t rope_dim,

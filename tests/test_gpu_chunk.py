@@ -283,6 +283,35 @@ def test_append_with_malformed_starts_changes_only_good_requests(starts):
     torch.cuda.synchronize()
 
 
+DESCENDING = [[0, 1000, 100, 300, 300], [0, 1000, 3, 500, 1000], [0, 900, 900, 900, 3, 3, 3, 3, 1000],
+              [700, 700, 0, 1000], [0, 127, 1, 1000]]
+
+
+@pytest.mark.parametrize("starts", DESCENDING + [None] * 6, ids=lambda s: "random" if s is None else None)
+@pytest.mark.parametrize("P", [0, 512])
+def test_append_with_descending_starts_takes_requests_whole_or_not_at_all(starts, P, request):
+    """Enough tokens for the kernel that searches the starts: a request whose length advances has all its rows
+    and entries, any other none."""
+    rng = np.random.default_rng(len(request.node.name) * 7 + P)
+    for _ in range(1 if starts else 8):
+        at = starts or np.sort(rng.integers(0, 1001, rng.integers(3, 40))).tolist()
+        if not starts:
+            for i in rng.integers(0, len(at), 3):
+                at[i] = int(rng.integers(-50, 1100))
+        B = len(at) - 1
+        s = Batch(rng.integers(0, 300, B).tolist(), [1000] + [0] * (B - 1), d=64, dtype="f32", P=P, rope=16,
+                  seed=len(at), cap=1536)
+        old = [s.oracle_caches(b) for b in range(B)]
+        s.starts = np.array(at)
+        s.gpu_starts = torch.tensor(at, dtype=torch.int32).cuda()
+        s.append()
+        bad = [b for b in range(B) if s.L[b].item() == s.before[b]]
+        s.check_append(old, bad=bad)
+        for b in range(B):
+            if not 0 <= at[b] <= at[b + 1] <= s.n:
+                assert b in bad and s.status.item() == -1
+
+
 # ---- attention ------------------------------------------------------------------------------------
 ATTEND = [  # before, news
     ([0], [1]), ([0, 0, 0], [1, 5, 130]), ([127, 128, 129, 3], [1, 1, 1, 1]), ([1000], [1]),

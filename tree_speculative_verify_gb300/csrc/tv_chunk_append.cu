@@ -435,6 +435,29 @@ __device__ __forceinline__ void load_gates(const AppendArgs& a, const Layers<T>&
 // Many tokens: a cluster per slot of a 128-block.  Request b's blocks take the slots from
 // floor(starts[b] / 128) + 2b on: its n tokens touch at most floor(n / 128) + 2 blocks, so requests
 // stay apart and a slot's request is found by a search of the starts.
+__device__ __forceinline__ int slot_of(int start, int b) { return start / 128 + 2 * b; }
+
+// Whether that search finds request b for each of its slots, which starts that descend elsewhere may
+// prevent: the searches for all of them take the way to b if its steps at or below b lie at or below b's first
+// slot and those above b behind its last one.  Lane i looks at the i-th step, request step_to(); -1: there
+// is none.
+__device__ __forceinline__ int step_to(int B, int b, int lane) {
+  int lo = 0, hi = B, at = -1;
+  for (int step = 0; lo < hi; ++step) {
+    const int mid = (lo + hi) >> 1;
+    if (step == lane) at = mid;
+    if (mid <= b)
+      lo = mid + 1;
+    else
+      hi = mid;
+  }
+  return at;
+}
+__device__ __forceinline__ bool step_holds(int at, int start_at, int b, int start, int n, int L) {
+  const int first = slot_of(start, b), last = first + (L % 128 + n - 1) / 128;
+  return at < 0 || (at <= b ? slot_of(start_at, at) <= first : slot_of(start_at, at) > last);
+}
+
 template <typename T>
 __global__ void __cluster_dims__(kC128Ranks, 1, 1) __launch_bounds__(kThreads)
     append_blocks_kernel(AppendArgs a, Layers<T> y, const T* K, const T* V) {
@@ -449,7 +472,7 @@ __global__ void __cluster_dims__(kC128Ranks, 1, 1) __launch_bounds__(kThreads)
   int lo = 0, hi = a.c.B;
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
-    if (starts[mid] / 128 + 2 * mid <= slot)
+    if (slot_of(starts[mid], mid) <= slot)
       lo = mid + 1;
     else
       hi = mid;
@@ -459,8 +482,10 @@ __global__ void __cluster_dims__(kC128Ranks, 1, 1) __launch_bounds__(kThreads)
   if (b >= 0) {
     const int s0 = starts[b], s1 = starts[b + 1], L0 = a.c.L[b];
     const int state = append_state(a.c, b, s0, s1, L0, threadIdx.x, kThreads);
-    const bool good = !__syncthreads_or(state != TV_OK);
-    const int blk = L0 / 128 + slot - (s0 / 128 + 2 * b);
+    const int at = step_to(a.c.B, b, threadIdx.x & 31);
+    const bool good = !__syncthreads_or(state != TV_OK ||
+                                        !step_holds(at, starts[max(at, 0)], b, s0, s1 - s0, L0));
+    const int blk = L0 / 128 + slot - slot_of(s0, b);
     if (good && s1 > s0 && (int64_t)128 * blk < L0 + (s1 - s0)) {
       load_gates(a, y, sm);
       append_block(a, y, K, V, b, blk, s0, L0, L0 + (s1 - s0), rank, joined, sm);
@@ -516,17 +541,23 @@ __global__ void __cluster_dims__(kC128Ranks, 1, 1) __launch_bounds__(kThreads, 4
   }
 }
 
-// The lengths advance once everything that reads them is done; errors are recorded here.  A warp per
-// request.
+// The lengths advance once everything that reads them is done, of the requests whose blocks were found; errors
+// are recorded here.  A warp per request.
 __global__ void append_lengths_kernel(AppendArgs a) {
+  const int b = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (b >= a.c.B) {
+    pdl_wait();
+    return;
+  }
+  // (nothing is read that the call's kernels in front write; they have waited for those in front of them)
+  const int at = step_to(a.c.B, b, lane), start_at = a.c.starts[max(at, 0)];
+  const int s0 = a.c.starts[b], s1 = a.c.starts[b + 1], L0 = a.c.L[b];
+  const int code = append_state(a.c, b, s0, s1, L0, lane, 32);
+  const bool lost = s1 > s0 && !step_holds(at, start_at, b, s0, s1 - s0, L0);
+  const unsigned arg = __ballot_sync(0xffffffffu, code == TV_ERR_ARG || lost);
+  const int state = arg != 0 ? TV_ERR_ARG : code;
   pdl_wait();
   pdl_launch_dependents();
-  const int b = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (b >= a.c.B) return;
-  const int s0 = a.c.starts[b], s1 = a.c.starts[b + 1], L0 = a.c.L[b];
-  const int found = append_state(a.c, b, s0, s1, L0, lane, 32);
-  const unsigned arg = __ballot_sync(0xffffffffu, found == TV_ERR_ARG);
-  const int state = arg != 0 ? TV_ERR_ARG : found;
   if (lane != 0) return;
   if (state != TV_OK)
     record_error(a.status, state);
