@@ -7,6 +7,7 @@ import pytest
 import torch
 
 from oracle import chunk
+from test_gpu_chunk import Batch
 from tree_speculative_verify_gb300 import _lib
 
 pytestmark = pytest.mark.gpu
@@ -57,3 +58,30 @@ def test_a_work_list_of_more_than_2_31_half_tiles():
             kind = part % 16
             assert ((O[part, 0].double() - want[kind]).abs() <= tol[kind]).all()
             assert ((lse[part, 0].double() - want_lse[kind]).abs() <= tol_lse[kind]).all()
+
+
+@pytest.mark.parametrize("d,dtype", [(128, "bf16"), (512, "bf16"), (64, "f32")])
+def test_more_requests_than_a_grid_has_rows(d, dtype):
+    """Page pools of 70000 slots, six of them in use, before and behind the 65535 that a grid's y takes."""
+    B, at = 70000, [0, 7, 65534, 65535, 65536, 69999]
+    s = Batch([700, 0, 1000, 511, 300, 129], [1, 3, 2, 1, 150, 1], H=4, d=d, dtype=dtype, P=512, rope=16,
+              q_std=2.0, seed=d)
+    table = torch.full((B, s.table.shape[1]), -1, dtype=torch.int32)
+    table[at] = s.table
+    table, L, starts = table.cuda(), torch.full((B,), 77, dtype=torch.int32), torch.zeros(B + 1, dtype=torch.int32)
+    L[at] = torch.tensor(s.before, dtype=torch.int32)
+    starts[1:][at] = torch.tensor(s.news, dtype=torch.int32)
+    s.L, s.gpu_starts = L.cuda(), starts.cumsum(0).to(torch.int32).cuda()
+    s.shape.B, s.shape.page_table = B, table.data_ptr()
+    s.ws = torch.full((_lib.tv_chunk_workspace_size(s.shape, s.n),), 0xff, dtype=torch.uint8, device="cuda")
+    old = [s.oracle_caches(b) for b in range(s.B)]
+    s.append(s.Q, s.Qr)
+    s.attend()
+    torch.cuda.synchronize()
+    assert s.status.item() == 0
+    idle = torch.ones(B, dtype=torch.bool)
+    idle[at] = False
+    assert torch.all(s.L.cpu()[idle] == 77)
+    s.L = s.L[at]
+    s.check_append(old, s.Qr)
+    s.check_attend()

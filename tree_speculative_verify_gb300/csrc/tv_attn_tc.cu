@@ -1655,19 +1655,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
 // Paged pools: copies each request's C128 entries into contiguous rows of the workspace, `stride` (a
 // multiple of 64) per request.  A page holds 4 entries per 512 tokens, too few for the attention's
 // 64-row boxes.  Rows up to the next multiple of 64 are zeros: the values of masked entries are
-// multiplied by zero probabilities.  A warp per row; latency-bound (64 requests of up to 64 entries 5 us).
+// multiplied by zero probabilities.  Grid (requests, up to 64), a warp per row; latency-bound (64 requests of
+// up to 64 entries 5 us).
 __global__ void gather_c128_kernel(Paging pg, int row_u4, int64_t c128_cap, int64_t stride, int64_t raw_cap,
                                    const int32_t* starts, const int32_t* L, const uint4* __restrict__ K,
                                    const uint4* __restrict__ V, uint4* gK, uint4* gV,
                                    int32_t* status) {
   pdl_wait();
   pdl_launch_dependents();
-  const int b = blockIdx.y, lane = threadIdx.x & 31, Lb = L[b];
+  const int b = blockIdx.x, lane = threadIdx.x & 31, Lb = L[b];
   // (a request without new tokens is not looked at, nor are its pages)
   if (Lb <= 0 || Lb > raw_cap || starts[b + 1] <= starts[b]) return;
   const int n = (Lb - 1) / 128;   // the last token sees no more
-  for (int64_t w = (int64_t)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32; w < ((n + 63) & ~63);
-       w += (int64_t)gridDim.x * (blockDim.x / 32)) {
+  for (int64_t w = (int64_t)blockIdx.y * (blockDim.x / 32) + threadIdx.x / 32; w < ((n + 63) & ~63);
+       w += (int64_t)gridDim.y * (blockDim.x / 32)) {
     const bool some = w < n;
     const int64_t src = some ? layer_row(pg, b, w, c128_cap, 128, status) * row_u4 : 0;
     const int64_t dst = ((int64_t)b * stride + w) * row_u4;
@@ -2110,7 +2111,7 @@ int tv_chunk_gather(const tv_shape* s, const int32_t* starts, const int32_t* L, 
                     const void* c128V, void* rows, int32_t* status, cudaStream_t stream) {
   const int64_t n = (s->c128_cap + 7) / 8;
   uint4* to = reinterpret_cast<uint4*>(rows);
-  if (tv::launch_pdl(tv::tc::gather_c128_kernel, dim3((unsigned)(n < 64 ? n : 64), s->B), dim3(256), 0,
+  if (tv::launch_pdl(tv::tc::gather_c128_kernel, dim3(s->B, (unsigned)(n < 64 ? n : 64)), dim3(256), 0,
                      stream, tv::paging_of(s), s->d * 2 / 16, s->c128_cap, tv_chunk_c128_stride(s),
                      s->raw_cap, starts, L, (const uint4*)c128K, (const uint4*)c128V, to,
                      to + tv_chunk_gather_bytes(s) / 16, status) != cudaSuccess)
