@@ -168,6 +168,70 @@ def test_captured_steps_replay():
     assert status[0].item() == 0
 
 
+def _two_groups(n_pool_pages):
+    """Two groups of two beams, their first steps ahead: one request of 100 tokens, one of 50."""
+    wl = workloads.make_workload("beams", B=4, D=1, H=2, d=64, W=8, tail_mode="window", ms=(4, 128), dtype="f32",
+                                 L=[100, 0, 50, 0], k=1, steps=1, p_match=0.5, seed=3, kv_scale=0.5)
+    shape, st = engine.alloc_pool(wl, page_tokens=512, n_pool_pages=n_pool_pages)
+    rb = engine.alloc_round(wl, shape)
+    engine.prefill(shape, st, rb)
+    return shape, st, rb, engine.alloc_beams(shape, width=2, eos=5)
+
+
+@pytest.mark.parametrize("own_stream", [False, True])
+def test_a_step_that_runs_out_of_pages_can_be_repeated(own_stream):
+    """The copies of both groups' partial pages need two pages more than the two that are held.  The failed
+    step is taken back, one group given up, and the step repeated as it goes in a pool with room."""
+    g = torch.Generator().manual_seed(5)
+    logits = torch.randn((4, 40), generator=g).cuda()
+    want_shape, want_st, want_rb, want = _two_groups(8)
+    engine.beam_step(want_shape, want_st, want_rb, want, logits)
+    shape, st, rb, beams = _two_groups(2)
+    stream = torch.cuda.Stream() if own_stream else None
+    before = [t.clone() for t in (beams.scores, beams.done, st.L, st.page_table, st.page_refs)]
+    torch.cuda.synchronize()
+    engine.beam_step(shape, st, rb, beams, logits, stream=stream)
+    torch.cuda.synchronize()
+    assert rb.status.item() == -4 and not torch.equal(beams.scores, before[0])
+    assert all(torch.equal(a, b) for a, b in zip((st.L, st.page_table, st.page_refs), before[2:]))
+    engine.beam_undo(beams, stream)
+    torch.cuda.synchronize()
+    assert torch.equal(beams.scores, before[0]) and torch.equal(beams.done, before[1])
+    rb.status.zero_()
+    beams.scores[2:] = -math.inf
+    torch.cuda.synchronize()
+    engine.beam_step(shape, st, rb, beams, logits, stream=stream)
+    torch.cuda.synchronize()
+    assert rb.status.item() == 0 and want_rb.status.item() == 0
+    for a, b in ((beams.scores, want.scores), (beams.token, want.token), (beams.source, want.source),
+                 (st.L, want_st.L)):
+        assert torch.equal(a[:2], b[:2])
+    assert beams.source[2:].tolist() == [-1, -1] and st.L.tolist() == [100, 100, 0, 0]
+    for b in range(2):
+        for name, m in (("rawK", 1), ("rawV", 1), ("c4K", 4), ("c4V", 4)):
+            rows = [getattr(x, name)[int(x.page_table[b, 0])][:100 // m] for x in (st, want_st)]
+            assert torch.equal(*rows), name
+
+
+def test_captured_steps_keep_what_is_in_front_of_the_last():
+    """A captured step, replayed twice: undoing takes back the second replay."""
+    shape, st, rb, beams = _two_groups(12)
+    x = torch.randn((4, 40), generator=torch.Generator().manual_seed(6)).cuda()
+    engine.beam_step(shape, st, rb, beams, x)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        engine.beam_step(shape, st, rb, beams, x, stream=torch.cuda.current_stream())
+    graph.replay()
+    torch.cuda.synchronize()
+    scores, done = beams.scores.clone(), beams.done.clone()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert rb.status.item() == 0 and not torch.equal(beams.scores, scores)
+    engine.beam_undo(beams)
+    assert torch.equal(beams.scores, scores) and torch.equal(beams.done, done)
+
+
 def test_beams_over_a_managed_pool():
     """Beam search over a toy model whose keys, values and logits depend on the whole sequence: a prompt
     in one chunk, then beams that are selected, reordered and extended.  The pool's beams must hold the

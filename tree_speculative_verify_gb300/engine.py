@@ -345,7 +345,8 @@ def chunk_attention(shape, st, rb, starts, Q, workspace, O=None, lse=None, scale
 @dataclass
 class Beams:
     """Beam search over a managed pool: ``width`` neighbouring slots are one group.  ``scores`` starts
-    as 0 in a group's first slot and -inf in the others (they become copies of it)."""
+    as 0 in a group's first slot and -inf in the others (they become copies of it); -inf in all of a
+    group's slots releases them in the next step."""
     width: int
     eos: int
     scores: torch.Tensor      # [B] fp32
@@ -354,6 +355,12 @@ class Beams:
     token: torch.Tensor       # [B] int32, the tokens to append next
     rank: torch.Tensor        # [B] int32
     workspace: torch.Tensor
+    last_scores: torch.Tensor = None   # [B] fp32, [B] int32: scores and done in front of the last step
+    last_done: torch.Tensor = None
+
+    def __post_init__(self):
+        if self.last_scores is None:
+            self.last_scores, self.last_done = self.scores.clone(), self.done.clone()
 
 
 def alloc_beams(shape, width, eos, device="cuda"):
@@ -369,11 +376,25 @@ def alloc_beams(shape, width, eos, device="cuda"):
 def beam_step(shape, st, rb, beams, logits, scale=1.0, stream=None):
     """Selects the groups' best continuations from ``logits`` [B][vocab] (the rows of done and empty
     slots do not count) and reorders the pool's pages by them: slot b then holds the cache of the
-    beam that ``beams.token[b]`` continues."""
+    beam that ``beams.token[b]`` continues.  If the pool runs out of pages (``rb.status``:
+    TV_ERR_CAPACITY), no slot changes, and ``beam_undo`` makes ``beams`` match them again."""
+    _copy(((beams.last_scores, beams.scores), (beams.last_done, beams.done)), stream)
     _lib.tv_beam_select(shape, beams.width, logits, beams.scores, beams.done, beams.eos, scale,
                         beams.source, beams.token, beams.scores, beams.done, beams.rank,
                         beams.workspace, rb.status, stream)
     fork(shape, st, rb, beams.source, None, stream)
+
+
+def beam_undo(beams, stream=None):
+    """Takes back what the last ``beam_step`` made of ``beams.scores`` and ``beams.done``, so that it can be
+    repeated with the same logits once pages are free."""
+    _copy(((beams.scores, beams.last_scores), (beams.done, beams.last_done)), stream)
+
+
+def _copy(pairs, stream):
+    with torch.cuda.stream(stream):     # (None: the current one)
+        for to, source in pairs:
+            to.copy_(source)
 
 
 def verify_round(shape, st, rb, scale=None, stream=None, commit=True, select=False, scored=False,
