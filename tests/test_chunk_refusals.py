@@ -116,3 +116,13 @@ def test_bindings_check_their_tensors():
                            None, None, None, None)
     with pytest.raises(ValueError, match="logits"):
         _lib.tv_beam_select(s, 2, torch.zeros(3, 10), *[None] * 2, 0, 1.0, *[None] * 7)
+
+
+@pytest.mark.parametrize("width", [0, 4, 33])
+def test_beams_of_a_width_that_does_not_divide_the_slots_are_refused(lib, width):
+    from tree_speculative_verify_gb300 import engine
+    with pytest.raises(ValueError, match="width"):
+        engine.alloc_beams(_shape(B=6), width, 2, device="cpu")
+    assert engine.alloc_beams(_shape(B=6), 3, 2, device="cpu").scores.tolist() == [0.0, -float("inf"),
+                                                                                  -float("inf")] * 2
+    assert engine.alloc_beams(_shape(B=0, raw_cap=0, c4_cap=0, c128_cap=0), 4, 2, device="cpu").done.numel() == 0

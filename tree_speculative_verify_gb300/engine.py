@@ -364,11 +364,14 @@ class Beams:
 
 
 def alloc_beams(shape, width, eos, device="cuda"):
+    """Buffers of a search with ``width`` beams per group; ``width`` divides the shape's B."""
+    size = _lib.tv_beam_workspace_size(shape, width)
+    if size == 0 and shape.B > 0:
+        raise ValueError(_lib.load().tv_last_error_string().decode())
     i = lambda: torch.zeros(shape.B, dtype=torch.int32, device=device)
     scores = torch.full((shape.B,), -math.inf, dtype=torch.float32, device=device)
     scores[::width] = 0.0
-    ws = torch.empty(max(_lib.tv_beam_workspace_size(shape, width), 256), dtype=torch.uint8,
-                     device=device)
+    ws = torch.empty(max(size, 256), dtype=torch.uint8, device=device)
     return Beams(width=width, eos=eos, scores=scores, done=i(), source=i(), token=i(), rank=i(),
                  workspace=ws)
 
