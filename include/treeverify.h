@@ -102,7 +102,7 @@ typedef struct CUstream_st* tv_stream_t; /* the same handle type as cudaStream_t
 /* tv_shape.attn_kernel */
 #define TV_ATTN_AUTO 0    /* tensor-core kernel where supported, else the SIMT kernel */
 #define TV_ATTN_SIMT 1    /* CUDA-core fp32 kernel: any supported shape, fp32 or bf16 */
-#define TV_ATTN_TCGEN05 2 /* tcgen05 tensor-core kernel: bf16, d == 512 */
+#define TV_ATTN_TCGEN05 2 /* tcgen05 tensor-core kernels: bf16; trees d == 512, chunks d % 128 == 0 */
 /* rope_pairs of tv_chunk_append */
 #define TV_ROPE_HALVES 0
 #define TV_ROPE_PAIRS 1
@@ -523,9 +523,11 @@ int tv_chunk_attn(const tv_shape* shape, int32_t n_new, const int32_t* starts, c
  * of slot b and ln p as in tv_token_logprobs, slot b's candidates are its tokens t with x[t] > -inf
  * and score scores[b] + ln p(t); a beam that has ended (done[b] != 0) has one, itself: token eos at
  * score scores[b].  A score of -inf: an empty slot, no candidates.  The `width` best candidates of
- * the group go on (equal scores: the lower slot first, then the lower id; scores are compared in
- * fp64): a beam with candidates among them keeps its best in its own slot, the others fill the
- * group's free slots in ascending order, best first.  Per slot:
+ * the group go on (equal scores: the lower slot first, then the lower id; scores are formed and
+ * compared in fp64, but the log of a beam's sum over the vocabulary comes from tv_token_logprobs in
+ * fp32: of candidates of different beams closer than 2^-18 either may come first): a beam with
+ * candidates among them keeps its best in its own slot, the others fill the group's free slots in
+ * ascending order, best first.  Per slot:
  *   source [B] int32: the slot it continues (0 .. B-1), -1 if candidates ran out: what tv_pages_fork
  *          takes, which copies and releases the pages; token [B] int32 (-1 without a source);
  *          new_scores [B] fp32 (-inf without a source); new_done [B] int32: 1 if the source had
@@ -549,7 +551,7 @@ int tv_beam_select(const tv_shape* shape, int32_t width, int32_t vocab, int64_t 
 
 /*
  * Testing aid for the failure path of the tensor-core attention (the report has no counterpart).
- * Sets, for every later tv_tree_verify_attn launch of the tcgen05 kernel in this process:
+ * Sets, for every later tv_tree_verify_attn or tv_chunk_attn launch of a tcgen05 kernel in this process:
  *   timeout_ns     the bound of every device-side wait (default 2000000000 = 2 s; > 0);
  *   withhold_tile  one KV tile index (within each work item's tile range) whose K copies the
  *                  producers never issue, or -1 for none (the default).

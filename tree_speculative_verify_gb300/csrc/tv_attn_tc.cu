@@ -1537,7 +1537,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     // the starts and lengths, which the kernel before this one may have written; the grid's first
     // CTA reports what makes a request invalid
     pdl_wait();
-    pdl_launch_dependents();   // (the merge reads them ahead of its wait)
+    pdl_launch_dependents();   // (the merge waits for this kernel before it reads anything)
     const bool cached = p.B < kRankMax;
     const int per = cached ? (p.B + kThreads - 1) / kThreads : 0;   // consecutive requests per thread
     int mine = 0;

@@ -22,7 +22,10 @@
 // Softmax: thread (entry, half of the rows) holds the entry's 32 logits; row maxima are reduced over
 // the lanes by halving exchanges and over the four warps of a half through shared memory; a lane keeps
 // its row's running maximum (raised lazily, by more than 2^8, as P in bf16 and l in fp32 allow), and the
-// sums of a thread's own probabilities are only reduced at the item's end.
+// sums of a thread's own probabilities are only reduced at the item's end.  P is rounded to bf16, because both
+// operands of an MMA have one type and V is bf16: relative errors of at most 2^-8 per entry, of either
+// sign, which average out over the entries (1024 to 8192 tokens: 0.0020 of O's norm from the 64-bit
+// result, 0.0017 with P in fp32, most of it O's own rounding); l sums the probabilities in fp32 as they are.
 //
 // Warps: 0 copies (TMA, a ring of 16 KB slots: 128 entries x 64 dimensions of K, or x 64 columns of
 // V), 1 issues the MMAs, 2..9 softmax and epilogue.  Every wait is bounded as in the tree attention.
