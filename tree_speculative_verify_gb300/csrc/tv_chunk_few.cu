@@ -31,9 +31,9 @@
 // V), 1 issues the MMAs, 2..9 softmax and epilogue.  Every wait is bounded as in the tree attention.
 //
 // Measured, d = 512, 64 heads, pages of 1024 tokens, with the gather of C128 entries in front and the join
-// behind: 64 requests of 1024 to 8192 tokens, one new token each, 59 us (207 MB from memory, 28 us at the
+// behind: 64 requests of 1024 to 8192 tokens, one new token each, 58 us (207 MB from memory, 28 us at the
 // rate of a copy; the stream itself runs at 5 to 6 TB/s, the gather takes 5 us, finding the work 3, the
-// last item's end 3, the join 5); one request of 8192 tokens 23 us, the length of the chain.  Tried and
+// last item's end 3, the join 5); one request of 8192 tokens 22 us, the length of the chain.  Tried and
 // slower: the gather inside this kernel, C128 boxes of 8 rows straight from the pages, an L2 prefetch of
 // the whole share, whole items per CTA.
 #include <cuda.h>
